@@ -73,6 +73,9 @@ typedef enum {
 
 typedef enum { CSA2_FULL = 0, CSA2_REINDEX = 1, CSA2_REUSE = 2 } csa2_mode;
 
+/* Element types of the calls that take more than one (section 8 and 9). */
+typedef enum { CSA2_F32 = 0, CSA2_BF16 = 1, CSA2_F16 = 2 } csa2_dtype;
+
 /* Device counter slots (uint32 each). */
 enum {
     CSA2_CNT_FP4_SATURATED = 0,   /* 16-channel groups whose amax exceeded 2688 */
@@ -302,7 +305,80 @@ typedef struct {
 
 csa2_status csa2_layer_step(const csa2_layer_args *args, void *stream);
 
+/* ---- 8. cache rows by number ----------------------------------------------
+ * Latents quantised into given rows of a cache, and rows read back as values,
+ * for callers that place entries themselves (a slot allocator, a prompt cache
+ * restored or copied row by row, a chunk whose later layers use the stored
+ * values).  Neither call touches seq_base or seq_len.
+ *
+ * csa2_cache_write: row rows[i] receives the FP4 encoding of x[i] (the encode
+ * of csa2_quantize_append at m = 1) and, if key is not NULL, the FP8 encoding
+ * of key[i]; otherwise the row's indexer key stays as it was.
+ *   rows [n]; x [n][512], rows ld_x elements apart; key [n][d_idx], rows
+ *   ld_key elements apart, of the same element type as x (type).
+ *   The rows of a call are distinct: a row that appears twice holds bytes of
+ *   either entry.  |x| > 2688 saturates (infinities too, CSA2_CNT_FP4_SATURATED
+ *   counts the groups); NaN latents and keys are outside the contract.
+ * csa2_cache_read: x[i] = the 512 values of row rows[i] (E2M1 code x E4M3
+ * scale: exact in every type) and, if key is not NULL, key[i] = the indexer
+ * key's values in fp32 (exact).  A row may appear any number of times.
+ * Both: a negative row number is padding (nothing is read or written for it: x[i]
+ * and key[i] of a read stay as they were); a row number >= cap is skipped the same way and
+ * counted in CSA2_CNT_BAD_INPUT.  n == 0 is a no-op.  x, key: 16-byte aligned,
+ * ld_x >= 512, ld_key >= d_idx, both a multiple of 16 bytes; rows: 8-byte
+ * aligned.  The cache's kidx and kscale may be NULL when key is. */
+csa2_status csa2_cache_write(const csa2_cache *cache, const int64_t *rows, int64_t n,
+                             const void *x, csa2_dtype type, int64_t ld_x, const void *key,
+                             int64_t ld_key, uint32_t *counters, void *stream);
+csa2_status csa2_cache_read(const csa2_cache *cache, const int64_t *rows, int64_t n, void *x,
+                            csa2_dtype type, int64_t ld_x, float *key, int64_t ld_key,
+                            uint32_t *counters, void *stream);
+
+/* ---- 9. dense attention of query groups -------------------------------------
+ * Group g is the queries off[g] .. off[g+1]-1; every head of each of them
+ * attends to the first n_g entries of sequence seq[g], n_g = len[g], or all
+ * seq_len[seq[g]] entries when len is NULL.  No mask beyond that: a group is
+ *   - the queries of many sequences over one prompt they share (its entries
+ *     are read once for the whole group), merged with each query's attention
+ *     over its own entries: pass csa2_sparse_attn's out and lse as prev_out
+ *     and prev_lse (several levels of shared prompts: one call per level, each
+ *     taking the last one's fp32 out and lse); or
+ *   - a decoder sequence's queries over an encoder's entries, of any length.
+ * For every query i of the group and head h, over the entries v_j, j < n_g:
+ *   out[i][h] = (sum_j e^(x_j) v_j + e^(prev_lse[i][h]) prev_out[i][h]) / L,
+ *   x_j = sm_scale * q[i][h] . v_j,  L = sum_j e^(x_j) + e^(prev_lse[i][h]),
+ *   lse[i][h] = log L,
+ * without the prev terms when prev_out is NULL or prev_lse[i][h] is -inf (its
+ * prev_out is then not read).  With nothing to attend to (n_g = 0 and no prev)
+ * out is 0 and lse -inf.  Rows of no group are left as they were.
+ *   seq [ng], off [ng+1] ascending in [0, nq], len [ng]: a group outside the
+ *   contract (sequence, offsets, n_g < 0, above seq_len or above max_n) is
+ *   skipped and counted in CSA2_CNT_BAD_INPUT, its rows left as they were;
+ *   q [nq][H][512] of q_type CSA2_BF16 or CSA2_F16, 1 <= H <= 128;
+ *   prev_out [nq][H][512] fp32 and prev_lse [nq][H], both or neither;
+ *   out [nq][H][512] of out_type (fp32: may be prev_out itself);
+ *   lse [nq][H] or NULL (may be prev_lse itself);
+ *   max_n: host bound on every n_g; it sets how a group's entries are divided.
+ * Arithmetic as in csa2_sparse_attn: exact f16 latents, q as f16 (bf16: exact
+ * for magnitudes in [2^-14, 65504]), softmax weights rounded to f16 (relative
+ * 2^-11), every sum in fp32; results do not depend on the run (fixed order).
+ * Group arrays: 4-byte aligned; q, prev_out, out, workspace: 16-byte. */
+typedef struct {
+    const int32_t *seq;        /* [ng] */
+    const int32_t *off;        /* [ng + 1] */
+    const int32_t *len;        /* [ng] or NULL */
+    int32_t ng;
+    int32_t nq;                /* queries that q, out and lse hold */
+} csa2_groups;
+
+csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, int64_t max_n,
+                            const void *q, csa2_dtype q_type, int32_t H, float sm_scale,
+                            const float *prev_out, const float *prev_lse, void *out,
+                            csa2_dtype out_type, float *lse, void *workspace, size_t ws_bytes,
+                            uint32_t *counters, void *stream);
+
 /* ---- workspace sizes (host-only, no GPU work) ------------------------------ */
+size_t csa2_dense_workspace_size(int32_t ng, int32_t nq, int32_t H, int64_t max_n);
 size_t csa2_index_workspace_size(int32_t nq, int32_t group, int32_t h_idx, int32_t d_idx);
 size_t csa2_topk_workspace_size(int32_t nq, int64_t max_n);
 size_t csa2_attn_workspace_size(int32_t nq, int32_t H, int32_t k_max, int32_t n_win);

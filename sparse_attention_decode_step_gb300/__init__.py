@@ -19,6 +19,7 @@ FULL, REINDEX, REUSE = 0, 1, 2
 D = 512
 CNT_FP4_SATURATED, CNT_CAPACITY, CNT_BAD_INPUT, CNT_TIMEOUT = 0, 1, 2, 3
 NUM_COUNTERS = 4
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 _lock = threading.Lock()
 _lib = None
@@ -30,7 +31,8 @@ EXPORTS = ["csa2_quantize_append", "csa2_quantize_append_project", "csa2_index_f
            "csa2_pool_select", "csa2_sparse_attn", "csa2_layer_step", "csa2_index_workspace_size",
            "csa2_topk_workspace_size", "csa2_attn_workspace_size", "csa2_layer_workspace_size",
            "csa2_status_string", "csa2_launch_count", "csa2_topk_noalloc",
-           "csa2_topk_noalloc_max_scratch"]
+           "csa2_topk_noalloc_max_scratch", "csa2_cache_write", "csa2_cache_read",
+           "csa2_dense_attn", "csa2_dense_workspace_size"]
 
 
 class CsaError(RuntimeError):
@@ -47,6 +49,11 @@ class _Cache(ctypes.Structure):
 class _Queries(ctypes.Structure):
     _fields_ = [("q_seq", ctypes.c_void_p), ("q_pos", ctypes.c_void_p), ("nq", ctypes.c_int32),
                 ("group", ctypes.c_int32)]
+
+
+class _Groups(ctypes.Structure):
+    _fields_ = [("seq", ctypes.c_void_p), ("off", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("ng", ctypes.c_int32), ("nq", ctypes.c_int32)]
 
 
 class _LayerArgs(ctypes.Structure):
@@ -87,6 +94,10 @@ def lib() -> ctypes.CDLL:
                 "csa2_sparse_attn": [vp, vp, vp, i64, vp, i32, vp, i32, vp, i32, vp, i32,
                                      ctypes.c_float, vp, vp, vp, sz, vp, vp],
                 "csa2_layer_step": [vp, vp],
+                "csa2_cache_write": [vp, vp, i64, vp, i32, i64, vp, i64, vp, vp],
+                "csa2_cache_read": [vp, vp, i64, vp, i32, i64, vp, i64, vp, vp],
+                "csa2_dense_attn": [vp, vp, i64, vp, i32, i32, ctypes.c_float, vp, vp, vp, i32, vp,
+                                    vp, sz, vp, vp],
             }
             for name, args in sig.items():
                 f = getattr(L, name)
@@ -100,6 +111,8 @@ def lib() -> ctypes.CDLL:
             L.csa2_attn_workspace_size.restype = sz
             L.csa2_layer_workspace_size.argtypes = [vp]
             L.csa2_layer_workspace_size.restype = sz
+            L.csa2_dense_workspace_size.argtypes = [i32, i32, i32, i64]
+            L.csa2_dense_workspace_size.restype = sz
             L.csa2_status_string.argtypes = [ctypes.c_int]
             L.csa2_status_string.restype = ctypes.c_char_p
             L.csa2_launch_count.argtypes = []
@@ -156,14 +169,38 @@ class Cache:
         self.seq_len = torch.zeros(self.batch, dtype=torch.int32, device=dev)
         self.base_host = base
 
+    @classmethod
+    def over(cls, codes, scales, kidx, kscale, seq_base, seq_len, m: int) -> "Cache":
+        """A cache over tensors that the caller already holds (nothing is copied):
+        codes [cap][256], scales [cap][32], kidx [cap][d_idx] uint8, kscale [cap]
+        fp32, seq_base [batch + 1] int64, seq_len [batch] int32, cap a multiple of 8.
+        kidx and kscale may be None for a cache that is only attended."""
+        for t, dt in ((codes, torch.uint8), (scales, torch.uint8), (kidx, torch.uint8),
+                      (kscale, torch.float32), (seq_base, torch.int64), (seq_len, torch.int32)):
+            if t is not None and (t.dtype != dt or not t.is_contiguous()):
+                raise CsaError(f"cache tensor must be contiguous {dt}, got {t.dtype}")
+        cap = codes.shape[0]
+        d_idx = kidx.shape[1] if kidx is not None else 128
+        if (tuple(codes.shape) != (cap, 256) or tuple(scales.shape) != (cap, 32)
+                or (kidx is None) != (kscale is None) or (kidx is not None and kidx.shape[0] != cap)
+                or (kscale is not None and kscale.numel() != cap)
+                or seq_base.numel() != seq_len.numel() + 1):
+            raise CsaError("cache tensors do not fit together")
+        c = cls.__new__(cls)
+        c.batch, c.cap, c.d_idx, c.m = seq_len.numel(), cap, d_idx, m
+        c.codes, c.scales, c.kidx, c.kscale = codes, scales, kidx, kscale
+        c.seq_base, c.seq_len, c.base_host = seq_base, seq_len, None
+        return c
+
     def struct(self, seq=None) -> _Cache:
         """The C struct; with seq = b, a one-sequence view of sequence b."""
+        keys = (None, None) if self.kidx is None else (self.kidx.data_ptr(), self.kscale.data_ptr())
         if seq is None:
-            return _Cache(self.codes.data_ptr(), self.scales.data_ptr(), self.kidx.data_ptr(),
-                          self.kscale.data_ptr(), self.seq_base.data_ptr(), self.seq_len.data_ptr(),
+            return _Cache(self.codes.data_ptr(), self.scales.data_ptr(), *keys,
+                          self.seq_base.data_ptr(), self.seq_len.data_ptr(),
                           self.cap, self.batch, self.d_idx, self.m)
-        return _Cache(self.codes.data_ptr(), self.scales.data_ptr(), self.kidx.data_ptr(),
-                      self.kscale.data_ptr(), self.seq_base.data_ptr() + 8 * int(seq),
+        return _Cache(self.codes.data_ptr(), self.scales.data_ptr(), *keys,
+                      self.seq_base.data_ptr() + 8 * int(seq),
                       self.seq_len.data_ptr() + 4 * int(seq), self.cap, 1, self.d_idx, self.m)
 
 
@@ -176,6 +213,26 @@ class Queries:
 
     def struct(self) -> _Queries:
         return _Queries(self.q_seq.data_ptr(), self.q_pos.data_ptr(), self.nq, self.group)
+
+
+class Groups:
+    """Query groups of dense_attn: group g is the queries off[g] .. off[g+1]-1 and
+    attends to the first length[g] entries (None: all) of sequence seq[g]."""
+
+    def __init__(self, seq, off, length=None, device="cuda"):
+        def dev(t):
+            if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32 and t.is_contiguous():
+                return t
+            return torch.as_tensor(t, dtype=torch.int32).to(device).contiguous()
+        self.seq, self.off = dev(seq), dev(off)
+        self.length = None if length is None else dev(length)
+        self.ng = self.seq.numel()
+        if self.off.numel() != self.ng + 1 or (length is not None and self.length.numel() != self.ng):
+            raise CsaError("groups need seq [ng], off [ng + 1] and length [ng]")
+
+    def struct(self, nq: int) -> _Groups:
+        return _Groups(self.seq.data_ptr(), self.off.data_ptr(),
+                       self.length.data_ptr() if self.length is not None else None, self.ng, nq)
 
 
 def new_counters(device="cuda"):
@@ -280,6 +337,91 @@ def sparse_attn(cache: Cache, qs: Queries, idx, cnt, q, win, n_win, out, lse=Non
                                   _ptr(q), H, _ptr(win), wcap, _ptr(win_start), int(n_win),
                                   float(sm_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
                                   _ptr(counters), _stream()), "csa2_sparse_attn")
+
+
+def _on_current_device(*tensors):
+    """A call runs on the current device's stream, so its tensors live there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != dev:
+            raise CsaError(f"tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _rows(t, width, what):
+    """Pointer and row stride of a [n][width] tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise CsaError("tensor is not on a CUDA device")
+    if t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+        raise CsaError(f"{what} must be [n][{width}] with contiguous rows, got {tuple(t.shape)}")
+    # (a single row's stride is arbitrary)
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else -(-width // 8) * 8
+
+
+def _row_args(cache, rows, x, key, key_type, what):
+    if rows.dtype != torch.int64 or rows.dim() != 1:
+        raise CsaError(f"rows must be int64 [n], got {rows.dtype} {tuple(rows.shape)}")
+    n = rows.shape[0]
+    if x.dtype not in _DTYPES or (key is not None and key.dtype != key_type):
+        raise CsaError(f"{what}: element type {x.dtype}, key {None if key is None else key.dtype}")
+    if x.shape[0] != n or (key is not None and key.shape[0] != n):
+        raise CsaError(f"{what}: rows, x and key differ in length")
+    xp, kp = _rows(x, D, "x"), _rows(key, cache.d_idx, "key")
+    _on_current_device(cache.codes, rows, x, key)
+    return n, xp, kp
+
+
+def cache_write(cache: Cache, rows, x, key=None, counters=None):
+    """Quantises x [n][512] (fp32, bf16 or f16, any row stride) into the cache rows
+    rows [n] (int64, distinct; negative: skipped), and key [n][d_idx] (x's type)
+    into their indexer keys if it is given."""
+    n, (xp, ld_x), (kp, ld_k) = _row_args(cache, rows, x, key, x.dtype, "cache_write")
+    cs = cache.struct()
+    _check(lib().csa2_cache_write(ctypes.byref(cs), _ptr(rows), n, xp, _DTYPES[x.dtype], ld_x, kp,
+                                  ld_k, _ptr(counters), _stream()), "csa2_cache_write")
+
+
+def cache_read(cache: Cache, rows, x, key=None, counters=None):
+    """Reads the cache rows rows [n] (int64; negative: skipped) into x [n][512] (fp32,
+    bf16 or f16: exact) and, if given, their indexer keys into key [n][d_idx] fp32."""
+    n, (xp, ld_x), (kp, ld_k) = _row_args(cache, rows, x, key, torch.float32, "cache_read")
+    cs = cache.struct()
+    _check(lib().csa2_cache_read(ctypes.byref(cs), _ptr(rows), n, xp, _DTYPES[x.dtype], ld_x, kp,
+                                 ld_k, _ptr(counters), _stream()), "csa2_cache_read")
+
+
+def dense_workspace_size(ng, nq, H, max_n) -> int:
+    return int(lib().csa2_dense_workspace_size(ng, nq, H, max_n))
+
+
+def dense_attn(cache: Cache, groups: Groups, q, out, lse=None, *, prev=None, sm_scale=1.0,
+               max_n=None, ws=None, counters=None):
+    """Attention of each group's queries q [nq][H][512] (bf16 or f16) over all the
+    entries of the group's sequence, into out [nq][H][512] (fp32, bf16 or f16) and
+    lse [nq][H]; prev = (out, lse) of an earlier partial result (fp32) is merged in.
+    max_n bounds the entries of any group (default: the cache's rows)."""
+    nq, H = int(q.shape[0]), int(q.shape[1])
+    po, pl = prev if prev is not None else (None, None)
+    if q.dtype not in (torch.bfloat16, torch.float16) or out.dtype not in _DTYPES:
+        raise CsaError(f"dense_attn: q {q.dtype}, out {out.dtype}")
+    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
+        raise CsaError(f"dense_attn: q {tuple(q.shape)}, out {tuple(out.shape)}")
+    for t, shape in ((po, q.shape), (pl, q.shape[:2]), (lse, q.shape[:2])):
+        if t is not None and (t.dtype != torch.float32 or t.shape != shape):
+            raise CsaError(f"dense_attn: lse and prev must be fp32 {tuple(shape)}")
+    qp = _ptr(q)
+    _on_current_device(cache.codes, groups.seq, q, po, pl, out, lse, ws)
+    max_n = cache.cap if max_n is None else int(max_n)
+    if ws is None:
+        need = dense_workspace_size(groups.ng, nq, H, max_n)
+        ws = workspace(need, q.device) if need else None
+    cs, gs = cache.struct(), groups.struct(nq)
+    _check(lib().csa2_dense_attn(ctypes.byref(cs), ctypes.byref(gs), max_n, qp,
+                                 _DTYPES[q.dtype], H, float(sm_scale), _ptr(po), _ptr(pl),
+                                 _ptr(out), _DTYPES[out.dtype], _ptr(lse), _ptr(ws),
+                                 ws.numel() if ws is not None else 0, _ptr(counters), _stream()),
+           "csa2_dense_attn")
 
 
 class Layer:

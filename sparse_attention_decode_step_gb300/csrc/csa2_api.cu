@@ -95,6 +95,27 @@ size_t attn_workspace_bytes(int nq, int H, int k_max, int n_win)
     return 0;
 }
 
+// Row tiles of 64 (query, head) rows, at most ceil(nq H / 64) + ng - 1 of them
+// (each group rounds up); their entries are divided over as many CTAs as fill
+// the GPU, at least two 128-entry tiles each.
+DensePlan dense_plan(int ng, int nq, int H, int64_t max_n)
+{
+    DensePlan d{};
+    if (ng < 1 || nq < 1 || H < 1) return d;
+    const int64_t rows = (int64_t)nq * H;
+    d.tiles = (int)((rows + kDenseRows - 1) / kDenseRows + (ng < nq ? ng : nq) - 1);
+    const int64_t ktiles = (max_n + 127) / 128;
+    int64_t s = device_sm_count() / d.tiles;
+    if (s > (ktiles + 1) / 2) s = (ktiles + 1) / 2;
+    if (s < 1) s = 1;
+    d.splits = (int)s;
+    if (d.splits > 1) {
+        d.off_ml = (size_t)d.tiles * d.splits * kDenseRows * CSA2_D * 4;
+        d.total = d.off_ml + (size_t)d.tiles * d.splits * 2 * kDenseRows * 4;
+    }
+    return d;
+}
+
 }  // namespace csa2
 
 using namespace csa2;
@@ -533,6 +554,112 @@ csa2_status csa2_layer_step(const csa2_layer_args *a, void *stream)
                             a->wcap, a->win_start, a->n_win, a->sm_scale, a->out, a->lse,
                             ws + pl.off_attn_ws, pl.total - pl.off_attn_ws, a->counters,
                             a->mode != CSA2_REUSE ? 1 : 0, stream);
+}
+
+// ---------------------------------------------------------------- cache rows by number
+namespace {
+
+csa2_status check_rows(const csa2_cache *cache, const int64_t *rows, int64_t n, const void *x, csa2_dtype type,
+                       int64_t ld_x, const void *key, int64_t ld_key, int key_bytes, const uint32_t *counters)
+{
+    csa2_status s = check_cache(cache, key != nullptr);
+    if (s != CSA2_OK) return s;
+    CSA2_REQUIRE(type == CSA2_F32 || type == CSA2_BF16 || type == CSA2_F16, CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(n >= 0 && n <= (1LL << 31), CSA2_ERR_INVALID_ARG);
+    if (n == 0) return CSA2_OK;
+    const int bytes = type == CSA2_F32 ? 4 : 2;
+    if (key_bytes == 0) key_bytes = bytes;
+    CSA2_REQUIRE(rows && x, CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(ld_x >= CSA2_D && ld_x < (1LL << 31), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(al8(rows) && al16(x) && (ld_x * bytes) % 16 == 0 && (counters == nullptr || al4(counters)),
+                 CSA2_ERR_ALIGN);
+    if (key) {
+        CSA2_REQUIRE(ld_key >= cache->d_idx && ld_key < (1LL << 31), CSA2_ERR_INVALID_ARG);
+        CSA2_REQUIRE(al16(key) && (ld_key * key_bytes) % 16 == 0, CSA2_ERR_ALIGN);
+    }
+    return CSA2_OK;
+}
+
+}  // namespace
+
+csa2_status csa2_cache_write(const csa2_cache *cache, const int64_t *rows, int64_t n, const void *x, csa2_dtype type,
+                             int64_t ld_x, const void *key, int64_t ld_key, uint32_t *counters, void *stream)
+{
+    csa2_status s = check_rows(cache, rows, n, x, type, ld_x, key, ld_key, 0, counters);
+    if (s != CSA2_OK || n == 0) return s;
+    return cuda_status(launch_cache_write(*cache, rows, n, x, type, ld_x, key, ld_key, counters,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+csa2_status csa2_cache_read(const csa2_cache *cache, const int64_t *rows, int64_t n, void *x, csa2_dtype type,
+                            int64_t ld_x, float *key, int64_t ld_key, uint32_t *counters, void *stream)
+{
+    csa2_status s = check_rows(cache, rows, n, x, type, ld_x, key, ld_key, 4, counters);
+    if (s != CSA2_OK || n == 0) return s;
+    return cuda_status(launch_cache_read(*cache, rows, n, x, type, ld_x, key, ld_key, counters,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- dense attention
+size_t csa2_dense_workspace_size(int32_t ng, int32_t nq, int32_t H, int64_t max_n)
+{
+    if (max_n < 0) return 0;
+    return dense_plan(ng, nq, H, max_n).total;
+}
+
+csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, int64_t max_n, const void *q,
+                            csa2_dtype q_type, int32_t H, float sm_scale, const float *prev_out,
+                            const float *prev_lse, void *out, csa2_dtype out_type, float *lse, void *workspace,
+                            size_t ws_bytes, uint32_t *counters, void *stream)
+{
+    csa2_status s = check_cache(cache, false);
+    if (s != CSA2_OK) return s;
+    CSA2_REQUIRE(groups != nullptr && groups->ng >= 0 && groups->nq >= 0, CSA2_ERR_INVALID_ARG);
+    if (groups->ng == 0 || groups->nq == 0) return CSA2_OK;
+    CSA2_REQUIRE(groups->seq && groups->off && q && out, CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(max_n >= 0 && max_n < (1LL << 31), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE((prev_out == nullptr) == (prev_lse == nullptr), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(H >= 1 && H <= 128 && (q_type == CSA2_BF16 || q_type == CSA2_F16), CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(out_type == CSA2_F32 || out_type == CSA2_BF16 || out_type == CSA2_F16, CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE((int64_t)groups->nq * H < (1LL << 30) && groups->ng < (1 << 24), CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(al4(groups->seq) && al4(groups->off) && (groups->len == nullptr || al4(groups->len)) && al16(q) &&
+                     al16(out) && (prev_out == nullptr || (al16(prev_out) && al4(prev_lse))) &&
+                     (lse == nullptr || al4(lse)) && (counters == nullptr || al4(counters)),
+                 CSA2_ERR_ALIGN);
+    const DensePlan pl = dense_plan(groups->ng, groups->nq, H, max_n);
+    if (pl.total) {
+        CSA2_REQUIRE(workspace, CSA2_ERR_INVALID_ARG);
+        CSA2_REQUIRE(al16(workspace), CSA2_ERR_ALIGN);
+        CSA2_REQUIRE(ws_bytes >= pl.total, CSA2_ERR_CAPACITY);
+    }
+    DenseParams p{};
+    p.codes = cache->codes;
+    p.scales = cache->scales;
+    p.seq_base = cache->seq_base;
+    p.seq_len = cache->seq_len;
+    p.cap = cache->cap;
+    p.batch = cache->batch;
+    p.g_seq = groups->seq;
+    p.g_off = groups->off;
+    p.g_len = groups->len;
+    p.ng = groups->ng;
+    p.nq = groups->nq;
+    p.H = H;
+    p.max_n = max_n;
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_type = q_type;
+    p.sm_scale = sm_scale;
+    p.prev_out = prev_out;
+    p.prev_lse = prev_lse;
+    p.out = out;
+    p.out_type = out_type;
+    p.lse = lse;
+    p.tiles = pl.tiles;
+    p.splits = pl.splits;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + pl.off_ml);
+    p.counters = counters;
+    return cuda_status(launch_dense(p, static_cast<cudaStream_t>(stream)));
 }
 
 const char *csa2_status_string(csa2_status s)

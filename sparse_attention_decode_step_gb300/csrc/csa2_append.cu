@@ -15,50 +15,6 @@
 
 namespace csa2 {
 
-// Smallest positive E4M3 byte b with 6 * value(b) >= amax (amax > 0); 0x7E and
-// *sat when even 6 * 448 is too small.
-__device__ __forceinline__ uint32_t fp4_scale_byte(float amax, bool *sat)
-{
-    if (6.0f * 448.0f < amax) { *sat = true; return 0x7Eu; }
-    uint32_t lo = 0, hi = 0x7E;       // value(hi) * 6 >= amax, value(lo) * 6 < amax (lo = 0 -> 0)
-    while (hi - lo > 1) {
-        uint32_t mid = (lo + hi) >> 1;
-        if (6.0f * e4m3_pos_value(mid) >= amax) hi = mid; else lo = mid;
-    }
-    return hi;
-}
-
-// E2M1 code of x under scale s: round to nearest, ties to the even code.
-// Midpoints between magnitudes {0, .5, 1, 1.5, 2, 3, 4, 6} are {.25, .75,
-// 1.25, 1.75, 2.5, 3.5, 5}; at a tie with midpoint k the result goes up when
-// code k + 1 is even (k odd).  Every m_k * s is exact in fp32.
-__device__ __forceinline__ uint32_t fp4_code(float x, float s)
-{
-    float a = fabsf(x);
-    uint32_t c = 0;
-    c += (a > 0.25f * s);
-    c += (a >= 0.75f * s);
-    c += (a > 1.25f * s);
-    c += (a >= 1.75f * s);
-    c += (a > 2.5f * s);
-    c += (a >= 3.5f * s);
-    c += (a > 5.0f * s);
-    if (c != 0 && x < 0.0f) c |= 8u;
-    return c;
-}
-
-// Value of E2M1 code `code` (sign bit 3) under scale s: magnitudes 0, 0.5, 1,
-// 1.5, 2, 3, 4, 6 built as fp32 bit patterns (index i >= 2: exponent
-// 126 + i / 2, mantissa bit i & 1; index 1: 0.5).
-__device__ __forceinline__ float fp4_value(uint32_t code, float s)
-{
-    const uint32_t i = code & 7u;
-    const uint32_t bits = (i >= 2u) ? (((126u + (i >> 1)) << 23) | ((i & 1u) << 22))
-                                    : (i == 1u ? (126u << 23) : 0u);
-    const float v = __uint_as_float(bits) * s;
-    return (code & 8u) ? -v : v;
-}
-
 // FP4 part of entry e of sequence b (warp = b * n_ent + e), one 16-channel
 // group per lane: block compression, encode, store of codes and scale.
 // Returns the cache row, or -1 when the entry is not stored (past the batch,

@@ -112,4 +112,40 @@ size_t attn_workspace_bytes(int nq, int H, int k_max, int n_win);
 int attn_max_splits();
 cudaError_t launch_attn_tc(const AttnParams &p, cudaStream_t st);
 
+// ---- cache rows by number
+cudaError_t launch_cache_write(const csa2_cache &c, const int64_t *rows, int64_t n, const void *x,
+                               int x_type, int64_t ld_x, const void *key, int64_t ld_key,
+                               uint32_t *counters, cudaStream_t st);
+cudaError_t launch_cache_read(const csa2_cache &c, const int64_t *rows, int64_t n, void *x,
+                              int x_type, int64_t ld_x, float *key, int64_t ld_key,
+                              uint32_t *counters, cudaStream_t st);
+
+// ---- dense attention of query groups
+constexpr int kDenseRows = 64;          // (query, head) rows per CTA
+struct DenseParams {
+    const uint8_t *codes, *scales;
+    const int64_t *seq_base;
+    const int32_t *seq_len;
+    int64_t cap;
+    int batch;
+    const int32_t *g_seq, *g_off, *g_len;
+    int ng, nq, H;
+    int64_t max_n;
+    const uint16_t *q;
+    int q_type;
+    float sm_scale;
+    const float *prev_out, *prev_lse;
+    void *out;
+    int out_type;
+    float *lse;
+    int tiles;          // bound on the row tiles of all groups
+    int splits;         // CTAs per row tile
+    float *part_o;      // [tiles][splits][64][512] unnormalised sums
+    float *part_ml;     // [tiles][splits][m | l][64]
+    uint32_t *counters;
+};
+struct DensePlan { int tiles, splits; size_t off_ml, total; };
+DensePlan dense_plan(int ng, int nq, int H, int64_t max_n);
+cudaError_t launch_dense(const DenseParams &p, cudaStream_t st);
+
 }  // namespace csa2
