@@ -414,13 +414,12 @@ def dense_attn(cache: Cache, groups: Groups, q, out, lse=None, *, prev=None, sm_
     _on_current_device(cache.codes, groups.seq, q, po, pl, out, lse, ws)
     max_n = cache.cap if max_n is None else int(max_n)
     if ws is None:
-        need = dense_workspace_size(groups.ng, nq, H, max_n)
-        ws = workspace(need, q.device) if need else None
+        ws = workspace(dense_workspace_size(groups.ng, nq, H, max_n), q.device)
     cs, gs = cache.struct(), groups.struct(nq)
     _check(lib().csa2_dense_attn(ctypes.byref(cs), ctypes.byref(gs), max_n, qp,
                                  _DTYPES[q.dtype], H, float(sm_scale), _ptr(po), _ptr(pl),
-                                 _ptr(out), _DTYPES[out.dtype], _ptr(lse), _ptr(ws),
-                                 ws.numel() if ws is not None else 0, _ptr(counters), _stream()),
+                                 _ptr(out), _DTYPES[out.dtype], _ptr(lse), _ptr(ws), ws.numel(),
+                                 _ptr(counters), _stream()),
            "csa2_dense_attn")
 
 

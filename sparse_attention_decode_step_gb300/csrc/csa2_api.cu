@@ -95,24 +95,23 @@ size_t attn_workspace_bytes(int nq, int H, int k_max, int n_win)
     return 0;
 }
 
-// Row tiles of 64 (query, head) rows, at most ceil(nq H / 64) + ng - 1 of them
-// (each group rounds up); their entries are divided over as many CTAs as fill
-// the GPU, at least two 128-entry tiles each.
+// One pair of CTAs per two SMs, or per tile when there are fewer: at most
+// ceil(nq H / 128) + ng - 1 row tiles (each group rounds up) of ceil(max_n / 256)
+// entry tiles.
 DensePlan dense_plan(int ng, int nq, int H, int64_t max_n)
 {
     DensePlan d{};
     if (ng < 1 || nq < 1 || H < 1) return d;
-    const int64_t rows = (int64_t)nq * H;
-    d.tiles = (int)((rows + kDenseRows - 1) / kDenseRows + (ng < nq ? ng : nq) - 1);
-    const int64_t ktiles = (max_n + 127) / 128;
-    int64_t s = device_sm_count() / d.tiles;
-    if (s > (ktiles + 1) / 2) s = (ktiles + 1) / 2;
-    if (s < 1) s = 1;
-    d.splits = (int)s;
-    if (d.splits > 1) {
-        d.off_ml = (size_t)d.tiles * d.splits * kDenseRows * CSA2_D * 4;
-        d.total = d.off_ml + (size_t)d.tiles * d.splits * 2 * kDenseRows * 4;
-    }
+    const int64_t rows = ((int64_t)nq * H + kDenseRows - 1) / kDenseRows + (ng < nq ? ng : nq) - 1;
+    const int64_t ents = (max_n + kDenseEntries - 1) / kDenseEntries;
+    int64_t pairs = device_sm_count() / 2;
+    if (pairs > kDensePairsMax) pairs = kDensePairsMax;
+    if (ents < 1 || pairs > rows * ents) pairs = rows * ents;
+    if (pairs < 1) pairs = 1;
+    d.pairs = (int)pairs;
+    d.off_ml = (size_t)pairs * 2 * kDenseRows * CSA2_D * 4;
+    d.off_begin = d.off_ml + (size_t)pairs * 2 * 2 * kDenseRows * 4;
+    d.total = d.off_begin + align_up((size_t)pairs * sizeof(DenseBegin), 256);
     return d;
 }
 
@@ -627,11 +626,9 @@ csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, 
                      (lse == nullptr || al4(lse)) && (counters == nullptr || al4(counters)),
                  CSA2_ERR_ALIGN);
     const DensePlan pl = dense_plan(groups->ng, groups->nq, H, max_n);
-    if (pl.total) {
-        CSA2_REQUIRE(workspace, CSA2_ERR_INVALID_ARG);
-        CSA2_REQUIRE(al16(workspace), CSA2_ERR_ALIGN);
-        CSA2_REQUIRE(ws_bytes >= pl.total, CSA2_ERR_CAPACITY);
-    }
+    CSA2_REQUIRE(workspace, CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(al16(workspace), CSA2_ERR_ALIGN);
+    CSA2_REQUIRE(ws_bytes >= pl.total, CSA2_ERR_CAPACITY);
     DenseParams p{};
     p.codes = cache->codes;
     p.scales = cache->scales;
@@ -654,10 +651,10 @@ csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, 
     p.out = out;
     p.out_type = out_type;
     p.lse = lse;
-    p.tiles = pl.tiles;
-    p.splits = pl.splits;
+    p.pairs = pl.pairs;
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + pl.off_ml);
+    p.begin = reinterpret_cast<DenseBegin *>(static_cast<uint8_t *>(workspace) + pl.off_begin);
     p.counters = counters;
     return cuda_status(launch_dense(p, static_cast<cudaStream_t>(stream)));
 }

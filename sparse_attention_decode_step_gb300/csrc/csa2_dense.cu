@@ -7,18 +7,33 @@
 //     out = (sum_j e^(x_j - M) v_j + e^(lse_prev - M) out_prev) / L,
 //     lse = M + log L,  L = the same sum without v_j and out_prev.
 //
-// One CTA = 64 rows of a group x a range of 128-entry tiles of its sequence,
-// laid out with the ENTRIES as the MMA's M = 128:
-//     S^T [128 entries x 64 rows] = V [128 x 512] . Q^T
-//     O^T [512 ch x 64 rows]     += V^T [512 x 128] . P^T
-// V is dequantised once per tile into 128-byte-swizzled f16 shared memory
-// (E2M1 x E4M3 is exact in f16); both products read the same bytes.  S^T, O^T
-// and the running row sums live in tensor memory, all sums in fp32; P is
-// rounded to f16 (relative 2^-11; at most 256 with the lazy rescaling below).
-// Warps 0..15 dequantise and run the softmax, warp 16 issues the MMAs.  The
-// reference maximum of a row moves only when a logit exceeds it by 8 (log2
-// units).  A row tile's entries are divided over `splits` CTAs, whose partial
-// results a second kernel joins in a fixed order (no atomics).
+// A pair of CTAs (one cluster) works on a tile of 128 rows, 64 in each CTA, and
+// 256 entries at a time, with both SMs' tensor cores as one (cta_group::2):
+//     S [128 rows x 256 entries]  = Q [128 x 512] . K^T          (M 128, N 256)
+//     O [128 rows x 512 channels] += P [128 x 256] . V           (M 128, 2 x N 256)
+// An SM then holds 64 rows' O (256 TMEM columns) and two S buffers (2 x 128),
+// and an MMA of N = 256 reads 6 KB of shared memory for 64 cycles of products
+// (measured: 4,056 MAC per cycle and SM; M = 128 entries x N = 64 rows, the
+// layout of the sparse attention, reads 6 KB for 32 cycles' worth and runs at
+// 2,705).  Each CTA dequantises its half of both operands (E2M1 x E4M3 is exact
+// in f16): as K, its 128 entries x all channels; as V, all 256 entries x its 256
+// channels.  The f16 operands never fit at once, so they pass through a ring of
+// eight 16 KB slots, each feeding four MMAs: a K slot is 128 entries x 64
+// channels (K-major), a V slot 32 entries x 256 channels (MN-major).
+//
+// Warps of a CTA: 0..7 softmax (two per TMEM lane quarter), 8..15 producers, 16
+// issues the MMAs (the first CTA of the pair only).  S is double buffered: the
+// product of tile i + 1's scores runs while tile i's softmax does, so the order on
+// the tensor pipe is S(0) S(1) O(0) S(2) O(1) ...  All sums are fp32; P is
+// rounded to f16 (relative 2^-11; at most 2^8, since the reference maximum of a
+// row moves whenever a logit exceeds it by 8 in log2 units, and O is then
+// rescaled in TMEM).
+//
+// Work is counted in tiles of 128 rows x 256 entries over all groups, and each
+// pair takes an equal run of them whatever the groups' sizes.  A pair whose
+// run begins or ends inside a row tile leaves that tile's sums in the
+// workspace (at most two such pieces per pair); a second kernel joins the
+// pieces in a fixed order, so results do not depend on timing.
 #include <cuda_fp16.h>
 
 #include "csa2_attn_device.cuh"
@@ -28,21 +43,26 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kDThreads = 544;                 // warps 0..15 workers, warp 16 MMA issuer
-constexpr int kDWorkers = 512;
-constexpr int kDWarps = 16;
-constexpr int kTileN = 128;                    // entries per tile (MMA M)
-constexpr int kTileR = kDenseRows;             // rows per CTA (MMA N)
-constexpr uint32_t kDV = kTileN * CSA2_D * 2;  // 128 KB
-constexpr uint32_t kDQ = kTileR * CSA2_D * 2;  // 64 KB
-constexpr uint32_t kDP = kTileN * kTileR * 2;  // 16 KB
-constexpr uint32_t kDVAtom = kTileN * 128;
-constexpr uint32_t kDQAtom = kTileR * 128;
+constexpr int kWarpsSoft = 8, kWarpsProd = 8;   // (a producer warp per ring slot)
+constexpr int kThreads = 32 * (kWarpsSoft + kWarpsProd + 1);
+constexpr int kSoft = 32 * kWarpsSoft;
+constexpr int kRowsPair = kDenseRows;          // rows per pair of CTAs
+constexpr int kRowsCta = kRowsPair / 2;
+constexpr int kEnt = kDenseEntries;            // entries per tile
+constexpr int kSlots = 8;
+constexpr uint32_t kSlot = 16384;
+constexpr uint32_t kQBytes = kRowsCta * CSA2_D * 2;     // 64 KB: [8 atoms][64 rows][128 B]
+constexpr uint32_t kQAtom = kRowsCta * 128;
+constexpr uint32_t kPBytes = kRowsCta * kEnt * 2;       // 32 KB: [4 atoms][64 rows][128 B]
+constexpr uint32_t kVAtom = 32 * 128;                   // V slot: [4 atoms of 64 channels][32 entries][128 B]
+constexpr uint32_t kColS = 256;                // TMEM: O in columns 0 .. 255, S buffer b from 256 + 128 b
+constexpr int kJoinThreads = 512;
 constexpr float kLazy = 8.0f;                  // log2 units
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-static_assert(kTileR == 64, "lane and column maps below");
+static_assert(kRowsPair == 128 && kEnt == 256, "lane and column maps below");
 
+// ------------------------------------------------------------------ groups and work
 // What a group asks for.  bad: its arguments are out of contract and its rows
 // are left as they are.
 struct Group {
@@ -70,24 +90,41 @@ __device__ __forceinline__ Group group_of(const DenseParams &p, int g)
     return r;
 }
 
-// The group that row tile `tile` (counted over all groups) belongs to, and the
-// tile's number within it; found by one warp.  false: past the last tile.
-// count_bad: count the groups that are out of contract.
-__device__ __forceinline__ bool find_tile(const DenseParams &p, int64_t tile, int lane, bool count_bad, int *g_out,
-                                          int *t_out)
+__device__ __forceinline__ int64_t row_tiles(const Group &g) { return g.bad ? 0 : (g.rows + kRowsPair - 1) / kRowsPair; }
+__device__ __forceinline__ int64_t ent_tiles(const Group &g) { return g.bad ? 0 : (g.n + kEnt - 1) / kEnt; }
+
+// Sum over all groups of their tiles (one warp; count_bad: counts the groups
+// that are out of contract).
+__device__ __forceinline__ int64_t total_units(const DenseParams &p, int lane, bool count_bad)
+{
+    int64_t sum = 0;
+    for (int g = lane; g < p.ng; g += 32) {
+        const Group gr = group_of(p, g);
+        if (gr.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
+        sum += row_tiles(gr) * ent_tiles(gr);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+// First unit of a pair's run: equal runs, none of them empty (of U units in all,
+// pairs past U have none).
+__device__ __forceinline__ int64_t run_begin(const DenseParams &p, int64_t pair, int64_t U)
+{
+    const int64_t P = min((int64_t)p.pairs, U);
+    return pair < P ? pair * U / P : U;
+}
+
+// The group that unit u (< the total) belongs to, and the units before it (one warp).
+__device__ __forceinline__ void find_unit(const DenseParams &p, int64_t u, int lane, int *g_out, int64_t *before_out)
 {
     int64_t before = 0;
-    bool found = false;
     for (int g0 = 0; g0 < p.ng; g0 += 32) {
-        const int g = g0 + lane;
         int64_t mine = 0;
-        if (g < p.ng) {
-            const Group gr = group_of(p, g);
-            if (gr.bad) {
-                if (count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
-            } else {
-                mine = (gr.rows + kTileR - 1) / kTileR;
-            }
+        if (g0 + lane < p.ng) {
+            const Group gr = group_of(p, g0 + lane);
+            mine = row_tiles(gr) * ent_tiles(gr);
         }
         int64_t upto = mine;
 #pragma unroll
@@ -95,50 +132,160 @@ __device__ __forceinline__ bool find_tile(const DenseParams &p, int64_t tile, in
             const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += v;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, before + upto > tile);
-        if (hit != 0u && !found) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, before + upto > u);
+        if (hit != 0u) {
             const int l = __ffs(hit) - 1;
-            const int64_t first = before + __shfl_sync(0xffffffffu, upto - mine, l);
             *g_out = g0 + l;
-            *t_out = (int)(tile - first);
-            found = true;
-            if (!count_bad) return true;
+            *before_out = before + __shfl_sync(0xffffffffu, upto - mine, l);
+            return;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    return found;
+    *g_out = p.ng;
+    *before_out = before;
 }
 
-__device__ __forceinline__ void dworkers_sync()
+// One pair's pieces of work in order: entries k0 .. k1 (in tiles) of a row tile.
+struct Work {
+    Group gr;
+    int g;
+    int64_t rt;          // row tile of the group
+    int64_t kt;          // tiles of entries of the group
+    int64_t k0, k1;
+    int64_t left;        // units left after this piece
+
+    __device__ __forceinline__ void start(const DenseParams &p, int g_, int64_t in_group, int64_t units)
+    {
+        left = units;
+        if (units <= 0) return;
+        g = g_;
+        gr = group_of(p, g);
+        kt = ent_tiles(gr);
+        rt = in_group / kt;
+        k0 = in_group - rt * kt;
+        k1 = min(kt, k0 + left);
+        left -= k1 - k0;
+    }
+    __device__ __forceinline__ bool next(const DenseParams &p)
+    {
+        if (left <= 0) return false;
+        if (++rt == row_tiles(gr)) {
+            do { gr = group_of(p, ++g); } while (row_tiles(gr) * ent_tiles(gr) == 0);
+            kt = ent_tiles(gr);
+            rt = 0;
+        }
+        k0 = 0;
+        k1 = min(kt, left);
+        left -= k1;
+        return true;
+    }
+};
+
+// ------------------------------------------------------------------ pairs of CTAs
+__device__ __forceinline__ uint32_t cta_rank()
 {
-    asm volatile("bar.sync 1, %0;" ::"n"(kDWorkers) : "memory");
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
 
-__device__ __forceinline__ bool dworkers_and(bool v)
+__device__ __forceinline__ uint32_t in_cta(uint32_t saddr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+
+// Arrives on a barrier of either CTA.  What the arrival announces is written to
+// this CTA's own shared memory or TMEM and read by this SM's tensor core (the
+// proxy fence before it orders that), so CTA scope is enough; at cluster scope
+// the release waits for the warp's outstanding loads and an acquire drops L1
+// (measured 1,900 cycles per ring slot against 300).
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Every wait of both CTAs ends: the flag of each is raised.
+__device__ __forceinline__ void raise_abort(int *flag)
+{
+    const uint32_t a = smem_u32(flag);
+    for (uint32_t r = 0; r < 2; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(a, r)), "r"(1) : "memory");
+}
+
+__device__ __forceinline__ void mma2(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on `bar` of both CTAs once every earlier MMA of this thread completed.
+__device__ __forceinline__ void commit2(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
+
+__device__ __forceinline__ bool soft_any(bool v)
 {
     uint32_t r;
     asm volatile(
         "{\n"
         ".reg .pred pin, pout;\n"
         "setp.ne.u32 pin, %1, 0;\n"
-        "bar.red.and.pred pout, 1, %2, pin;\n"
+        "bar.red.or.pred pout, 1, %2, pin;\n"
         "selp.u32 %0, 1, 0, pout;\n"
         "}\n"
         : "=r"(r)
-        : "r"((uint32_t)v), "n"(kDWorkers)
+        : "r"((uint32_t)v), "n"(kSoft)
         : "memory");
     return r != 0;
 }
 
-__device__ __forceinline__ void store_out(void *out, int type, int64_t at, float v)
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
 {
-    if (type == CSA2_F32) static_cast<float *>(out)[at] = v;
-    else if (type == CSA2_BF16) static_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
-    else static_cast<__half *>(out)[at] = __float2half_rn(v);
+    float a[16], b[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) { a[i] = v[i]; b[i] = v[16 + i]; }
+    tmem_st16(taddr, a);
+    tmem_st16(taddr + 16, b);
 }
 
-// A row's partial softmax (m in log2 units, l) joined with the caller's
-// partial result: the weights of the two, and the joint lse.
+// ------------------------------------------------------------------ results
+__device__ __forceinline__ void store4(void *out, int type, int64_t at, float a, float b, float c, float d)
+{
+    if (type == CSA2_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = make_float4(a, b, c, d);
+    } else if (type == CSA2_BF16) {
+        uint32_t lo, hi;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(d), "f"(c));
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(out) + at) = make_uint2(lo, hi);
+    } else {
+        *reinterpret_cast<uint2 *>(static_cast<__half *>(out) + at) =
+            make_uint2(f32x2_to_f16x2(a, b), f32x2_to_f16x2(c, d));
+    }
+}
+
+// A row's softmax (m in log2 units, l) joined with the caller's partial
+// result: the weights of the two, and the joint lse.
 struct Joined { float own, prev, lse; };
 
 __device__ __forceinline__ Joined join_prev(float m, float l, bool any_prev, float prev_lse)
@@ -156,439 +303,573 @@ __device__ __forceinline__ Joined join_prev(float m, float l, bool any_prev, flo
     return j;
 }
 
-__global__ void __launch_bounds__(kDThreads, 1) dense_attn_kernel(DenseParams p)
+// Rows of a group without entries: the caller's partial result, or nothing.
+__device__ __forceinline__ void empty_rows(const DenseParams &p, const Group &gr, int first, int step)
 {
-    const int split = (int)(blockIdx.x % (unsigned)p.splits);
-    const int64_t tile_id = blockIdx.x / (unsigned)p.splits;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *sV = smem;                        // [8 atoms][128 entries][128 B]
-    uint8_t *sQ = sV + kDV;                    // [8 atoms][64 rows][128 B]
-    uint8_t *sP = sQ + kDQ;                    // [128 entries][64 rows] f16
-    float *sRed = reinterpret_cast<float *>(sP + kDP);   // [4 quarters][64 rows]
-    float *sM = sRed + 4 * 64;                 // reference max per row (log2 units)
-    float *sAlpha = sM + 64;
-    float *sL = sAlpha + 64;
-    float *sOwn = sL + 64;                     // weight of the row's own sums in the output
-    float *sPrev = sOwn + 64;                  // weight of the caller's partial result
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sPrev + 64);
-    uint64_t *bar_v = bars;                    // [2]: V channel half h stored
-    uint64_t *bar_o = bars + 2;                // [2]: PV channel blocks 2h, 2h + 1 done
-    uint64_t *bar_s = bars + 4, *bar_p = bars + 5, *bar_done = bars + 6, *bar_q = bars + 7;
-    int *sFlag = reinterpret_cast<int *>(bars + 8);      // [0] abort [1] rescale [2] need max
-    int *sTile = sFlag + 4;                    // [0] found [1] group [2] tile of the group
-    uint32_t *sTmem = reinterpret_cast<uint32_t *>(sTile + 4);
-    volatile int *abort_flag = sFlag;
-
-    if (tid == 0) {
-        for (int c = 0; c < 2; ++c) {
-            mbar_init(&bar_v[c], kDWarps);
-            mbar_init(&bar_o[c], 1);
-        }
-        mbar_init(bar_s, 1);
-        mbar_init(bar_p, kDWarps);
-        mbar_init(bar_done, 1);
-        mbar_init(bar_q, 1);
-        for (int i = 0; i < 4; ++i) sFlag[i] = 0;
-        fence_barrier_init();
-    }
-    if (tid < 64) { sM[tid] = -INFINITY; sAlpha[tid] = 1.f; sL[tid] = 0.f; }
-    if (warp == 0) { tmem_alloc(sTmem, 512); tmem_relinquish(); }
-    pdl_wait();
-    pdl_trigger();
-    if (warp == 1) {
-        int g = 0, t = 0;
-        const bool ok = find_tile(p, tile_id, lane, split == 0 && tile_id == 0, &g, &t);
-        if (lane == 0) { sTile[0] = ok; sTile[1] = g; sTile[2] = t; }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *sTmem;
-    const bool found = sTile[0] != 0;
-    Group gr{};
-    if (found) gr = group_of(p, sTile[1]);
-    const int64_t row0 = gr.row0 + (int64_t)sTile[2] * kTileR;
-    const int n_rows = found ? (int)min((int64_t)kTileR, gr.rows - (int64_t)sTile[2] * kTileR) : 0;
-    const int all_tiles = (gr.n + kTileN - 1) / kTileN;
-    const int tps = (all_tiles + p.splits - 1) / p.splits;
-    const int t_begin = min(all_tiles, split * tps);
-    const int n_tiles = found ? min(all_tiles, t_begin + tps) - t_begin : 0;
-    const int e_begin = t_begin * kTileN;                       // first entry of this CTA
-    const int e_end = min(gr.n, (t_begin + n_tiles) * kTileN);  // one past its last
-
-    const uint32_t quarter = (uint32_t)(warp & 3);
-    const int ent = (int)(quarter * 32 + lane);       // softmax: entry of the tile = TMEM lane
-    const int r0 = 16 * (warp >> 2);                  // softmax: rows r0 .. r0 + 15
-    const uint32_t lane_q = (quarter * 32u) << 16;
-    const uint32_t tS = tmem, tO = tmem + 64, tL = tmem + 320 + (uint32_t)(r0 & 63) + lane_q;
-
-    // ---- loads: warp w fills entries 8 w .. 8 w + 7 of a tile, 8 lanes per
-    // entry; register slot 2 h + x holds entry 4 x + (lane >> 3), channels
-    // 256 h + 32 sub .. + 31
-    const int sub = lane & 7, rho = sub >> 1;
-    uint4 gc[4];
-    uint32_t gsc[4];
-    auto load_half = [&](int tile, int h) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int e = e_begin + tile * kTileN + 8 * warp + 4 * x + (lane >> 3);
-            gc[2 * h + x] = make_uint4(0, 0, 0, 0);
-            gsc[2 * h + x] = 0;
-            if (e < e_end) {
-                const int64_t r = gr.base + e;
-                gc[2 * h + x] = __ldg(reinterpret_cast<const uint4 *>(p.codes + r * CSA2_CODE_BYTES) + 8 * h + sub);
-                gsc[2 * h + x] = __ldg(reinterpret_cast<const uint16_t *>(p.scales + r * CSA2_SCALE_BYTES) + 8 * h + sub);
-            }
-        }
-    };
-    // channel half h of this warp's entries into sV (entries past the end are
-    // zero); the pieces are rotated so that 8 lanes hit 8 bank groups
-    auto store_half = [&](int h) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int t = 2 * h + x, r = 8 * warp + 4 * x + (lane >> 3);
-            const uint32_t p0 = scale_pair(gsc[t] & 0xFFu), p1 = scale_pair((gsc[t] >> 8) & 0xFFu);
-            uint32_t w[4] = {gc[t].x, gc[t].y, gc[t].z, gc[t].w};
-            uint32_t sp[4] = {p0, p0, p1, p1};
-            if (rho & 1) {
-                const uint32_t w0 = w[0], s0 = sp[0];
-                w[0] = w[1]; w[1] = w[2]; w[2] = w[3]; w[3] = w0;
-                sp[0] = sp[1]; sp[1] = sp[2]; sp[2] = sp[3]; sp[3] = s0;
-            }
-            if (rho & 2) {
-                uint32_t a = w[0], b = w[1];
-                w[0] = w[2]; w[1] = w[3]; w[2] = a; w[3] = b;
-                a = sp[0]; b = sp[1];
-                sp[0] = sp[2]; sp[1] = sp[3]; sp[2] = a; sp[3] = b;
-            }
-            uint8_t *dst = sV + (4 * h + (sub >> 1)) * kDVAtom;
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                *reinterpret_cast<uint4 *>(dst + sw128((uint32_t)r, (uint32_t)(4 * (sub & 1) + ((m + rho) & 3)))) =
-                    fp4x8_to_f16(w[m], sp[m]);
-        }
-    };
-
-    if (n_tiles > 0) {
-        // ---- Q: raw 16-bit rows land in the V tile, then go as f16 into the
-        // swizzled sQ (rows past the tile's are zero)
-        if (warp < kDWarps) { load_half(0, 0); load_half(0, 1); }
-        const uint32_t qbytes = (uint32_t)n_rows * CSA2_D * 2;
-        if (tid == 0) {
-            mbar_arrive_expect_tx(bar_q, qbytes);
-            bulk_load(sV, p.q + row0 * CSA2_D, qbytes, bar_q);
-        }
-        volatile int no_abort = 0;
-        if (!mbar_wait(bar_q, 0, &no_abort)) sFlag[0] = 1;
-        for (int i = tid; i < kTileR * (CSA2_D / 8); i += kDThreads) {
-            const int r = i / (CSA2_D / 8), c8 = i % (CSA2_D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < n_rows) {
-                v = *reinterpret_cast<const uint4 *>(sV + r * 1024 + c8 * 16);
-                if (p.q_type == CSA2_BF16)
-                    v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z),
-                                   bf16x2_to_f16x2(v.w));
-            }
-            *reinterpret_cast<uint4 *>(sQ + (c8 >> 3) * kDQAtom + sw128(r, c8 & 7)) = v;
-        }
-        fence_async_smem();
-    }
-    __syncthreads();
-
-    if (n_tiles > 0 && warp == kDWarps) {
-        // ============================================== MMA issuer
-        if (lane == 0) {
-            const uint32_t id_qk = instr_desc(128, kTileR, 0, 0, 0, 0);
-            const uint32_t id_pv = instr_desc(128, kTileR, 0, 0, 1, 1);
-            const uint32_t v0 = smem_u32(sV), q0 = smem_u32(sQ), p0 = smem_u32(sP);
-            for (int i = 0; i < n_tiles; ++i) {
-                bool run = true;
-                for (int h = 0; h < 2 && run; ++h) {
-                    if (!mbar_wait<true>(&bar_v[h], i & 1, abort_flag)) { run = false; break; }
-                    tc_fence_after();
-#pragma unroll
-                    for (int k16 = 0; k16 < 16; ++k16) {
-                        const int ks = 16 * h + k16;
-                        mma_f16(tS, smem_desc(v0 + (ks >> 2) * kDVAtom + (ks & 3) * 32, 16, 1024, kLayoutSW128),
-                                smem_desc(q0 + (ks >> 2) * kDQAtom + (ks & 3) * 32, 16, 1024, kLayoutSW128), id_qk,
-                                ks > 0);
-                    }
-                }
-                if (!run) { *abort_flag = 1; break; }
-                mma_commit(bar_s);
-                if (!mbar_wait<true>(bar_p, i & 1, abort_flag)) { *abort_flag = 1; break; }
-                tc_fence_after();
-#pragma unroll
-                for (int mb = 0; mb < 4; ++mb) {
-#pragma unroll
-                    for (int ks = 0; ks < kTileN / 16; ++ks)
-                        mma_f16(tO + 64 * mb, smem_desc(v0 + 2 * mb * kDVAtom + ks * 2048, kDVAtom, 1024, kLayoutSW128),
-                                smem_desc(p0 + ks * 2048, kDVAtom, 1024, kLayoutSW128), id_pv,
-                                (i > 0 || ks > 0) ? 1u : 0u);
-                    if (mb & 1) mma_commit(&bar_o[mb >> 1]);
-                }
-            }
-            mma_commit(bar_done);       // once every MMA issued above has completed
-        }
-    } else if (n_tiles > 0) {
-        // ============================================== 16 worker warps
-        const float l2s = p.sm_scale * kLog2e;
-        {
-            float z[16];
-#pragma unroll
-            for (int h = 0; h < 16; ++h) z[h] = 0.f;
-            tmem_st16(tL, z);
-            tmem_wait_st();
-        }
-        bool ok = !sFlag[0];
-        for (int i = 0; i < n_tiles && ok; ++i) {
-            const bool valid = e_begin + i * kTileN + ent < e_end;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                bool got = true;
-                if (i > 0) {
-                    got = __all_sync(0xffffffffu, mbar_wait<true>(&bar_o[h], (i - 1) & 1, abort_flag));
-                    tc_fence_after();
-                }
-                if (got) store_half(h);
-                else ok = false;
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_v[h]);
-            }
-            const bool more = i + 1 < n_tiles;
-            if (more) load_half(i + 1, 0);
-
-            // ---- softmax of this entry, rows r0 .. r0 + 15
-            const bool got_s = ok && mbar_wait<true>(bar_s, i & 1, abort_flag);
-            tc_fence_after();
-            float x[16];
-            if (got_s) {
-                tmem_ld16(tS + lane_q + (uint32_t)r0, x);
-                tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int h = 0; h < 16; ++h) x[h] = 0.f;
-            }
-            bool over = false;
-#pragma unroll
-            for (int h4 = 0; h4 < 4; ++h4) {
-                const float4 m4 = reinterpret_cast<const float4 *>(sM + r0)[h4];
-                const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int h = 4 * h4 + j;
-                    x[h] = valid ? x[h] * l2s : -INFINITY;
-                    over |= x[h] > mm[j] + kLazy;
-                }
-            }
-            if (over) sFlag[2] = i + 1;
-            ok = dworkers_and(got_s);
-            if (!ok) {
-                if (tid == 0) *abort_flag = 1;
-                break;
-            }
-            if (sFlag[2] == i + 1) {
-                float r[16];
-#pragma unroll
-                for (int h = 0; h < 16; ++h) r[h] = x[h];
-                warp_reduce16<true>(r, lane);
-                if (lane < 16) sRed[quarter * 64 + r0 + lane] = r[0];
-                dworkers_sync();
-                if (tid < 64) {
-                    const float tmax = fmaxf(fmaxf(sRed[tid], sRed[64 + tid]), fmaxf(sRed[128 + tid], sRed[192 + tid]));
-                    const float m_old = sM[tid];
-                    float alpha = 1.f;
-                    if (tmax > m_old + kLazy) {
-                        alpha = (m_old == -INFINITY) ? 0.f : fast_exp2(m_old - tmax);
-                        sM[tid] = tmax;
-                        if (i > 0) sFlag[1] = 1;
-                    }
-                    sAlpha[tid] = alpha;
-                }
-                dworkers_sync();
-                if (sFlag[1] != 0) {
-                    // O^T and the running sums *= alpha per row; the previous tile's PV
-                    // has completed (both of its barriers were waited above)
-                    float al[16];
-#pragma unroll
-                    for (int h = 0; h < 16; ++h) al[h] = sAlpha[r0 + h];
-                    float o[16];
-                    tmem_ld16(tL, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int h = 0; h < 16; ++h) o[h] *= al[h];
-                    tmem_st16(tL, o);
-#pragma unroll 1
-                    for (int mb = 0; mb < 4; ++mb) {
-                        const uint32_t ta = tO + 64 * mb + (uint32_t)r0 + lane_q;
-                        tmem_ld16(ta, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int h = 0; h < 16; ++h) o[h] *= al[h];
-                        tmem_st16(ta, o);
-                    }
-                    tmem_wait_st();
-                }
-                dworkers_sync();
-                if (tid == 0) sFlag[1] = 0;
-            }
-#pragma unroll
-            for (int h = 0; h < 16; ++h) {
-                // (no finite logit yet: e^-inf = 0 for all, and a NaN stays one)
-                const float mm = sM[r0 + h];
-                x[h] = fast_exp2(x[h] - (mm == -INFINITY ? 0.f : mm));
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                *reinterpret_cast<uint4 *>(sP + sw128((uint32_t)ent, (uint32_t)(r0 / 8 + c))) =
-                    make_uint4(f32x2_to_f16x2(x[8 * c], x[8 * c + 1]), f32x2_to_f16x2(x[8 * c + 2], x[8 * c + 3]),
-                               f32x2_to_f16x2(x[8 * c + 4], x[8 * c + 5]), f32x2_to_f16x2(x[8 * c + 6], x[8 * c + 7]));
-            fence_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_p);
-            if (more) load_half(i + 1, 1);
-            float o[16];
-            tmem_ld16(tL, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int h = 0; h < 16; ++h) o[h] += x[h];
-            tmem_st16(tL, o);
-            tmem_wait_st();
-        }
-        if (!ok) *abort_flag = 1;
-    }
-    if (n_tiles > 0) {
-        volatile int no_abort = 0;
-        if (!mbar_wait<true>(bar_done, 0, &no_abort)) *abort_flag = 1;
-        tc_fence_after();
-        if (warp < kDWarps) {
-            float l[16];
-            tmem_ld16(tL, l);
-            tmem_wait_ld();
-            warp_reduce16<false>(l, lane);
-            if (lane < 16) sRed[quarter * 64 + r0 + lane] = l[0];
-        }
-    }
-    __syncthreads();
-    const bool failed = *abort_flag != 0;
-    if (tid == 0 && failed) count_event(p.counters, CSA2_CNT_TIMEOUT);
-    const bool any = n_tiles > 0 && !failed;
-    if (tid < 64) {
-        const float l = any ? (sRed[tid] + sRed[64 + tid]) + (sRed[128 + tid] + sRed[192 + tid]) : 0.f;
-        const float m = !any ? -INFINITY : l != l ? 0.f : sM[tid];     // (a NaN row is not an empty one)
-        if (p.splits > 1) {
-            if (found) {
-                float *ml = p.part_ml + (tile_id * p.splits + split) * 128;
-                ml[tid] = m;
-                ml[64 + tid] = l;
-            }
-            sOwn[tid] = 1.f;
-        } else if (tid < n_rows) {
-            const Joined j = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[row0 + tid] : 0.f);
-            sOwn[tid] = j.own;
-            sPrev[tid] = j.prev;
-            if (p.lse) p.lse[row0 + tid] = j.lse;
-        }
-    }
-    __syncthreads();
-    if (found && warp < kDWarps && (p.splits == 1 || any)) {
-        // lane = channel 128 mb + 32 quarter + lane, 16 rows each
-#pragma unroll 1
-        for (int mb = 0; mb < 4; ++mb) {
-            float o[16];
-            if (any) {
-                tmem_ld16(tO + 64 * mb + (uint32_t)r0 + lane_q, o);
-                tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int h = 0; h < 16; ++h) o[h] = 0.f;
-            }
-            const int c = 128 * mb + ent;
-            if (p.splits > 1) {
-                float *dst = p.part_o + ((tile_id * p.splits + split) * 64 + r0) * CSA2_D + c;
-#pragma unroll
-                for (int h = 0; h < 16; ++h) dst[h * CSA2_D] = o[h];
-            } else {
-#pragma unroll
-                for (int h = 0; h < 16; ++h) {
-                    if (r0 + h >= n_rows) break;
-                    const int64_t at = (row0 + r0 + h) * CSA2_D + c;
-                    float v = any ? o[h] * sOwn[r0 + h] : 0.f;
-                    const float pw = sPrev[r0 + h];
-                    if (pw != 0.f) v = fmaf(p.prev_out[at], pw, v);
-                    store_out(p.out, p.out_type, at, v);
-                }
-            }
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 0) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
+    for (int64_t i = first; i < gr.rows * (CSA2_D / 4); i += step) {
+        const int64_t row = gr.row0 + i / (CSA2_D / 4);
+        const int c = (int)(i % (CSA2_D / 4)) * 4;
+        const float pl = p.prev_out ? p.prev_lse[row] : -INFINITY;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (pl > -INFINITY || pl != pl) v = *reinterpret_cast<const float4 *>(p.prev_out + row * CSA2_D + c);
+        store4(p.out, p.out_type, row * CSA2_D + c, v.x, v.y, v.z, v.w);
+        if (c == 0 && p.lse) p.lse[row] = pl;
     }
 }
 
-// Joins the splits of each row tile and the caller's partial result, in split
-// order.  A CTA takes 4 rows, 128 threads (4 channels each) per row.
-__global__ void __launch_bounds__(512) dense_join_kernel(DenseParams p)
+__global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 {
-    __shared__ int sTile[3];
-    const int64_t tile_id = blockIdx.x / (kTileR / 4);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cta_rank();
+    const int pair = (int)(blockIdx.x >> 1);
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *sRing = smem;                     // [8 slots][16 KB]
+    uint8_t *sQ = sRing + kSlots * kSlot;
+    uint8_t *sP = sQ + kQBytes;
+    float *sRed = reinterpret_cast<float *>(sP + kPBytes);   // [4 threads of a row][64 rows]
+    float *sM = sRed + 4 * kRowsCta;           // reference max per row (log2 units)
+    float *sAlpha = sM + kRowsCta;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sAlpha + kRowsCta);
+    uint64_t *bar_full = bars;                 // [8] (first CTA's) slot filled by both CTAs
+    uint64_t *bar_empty = bars + 8;            // [8] slot's MMAs done
+    uint64_t *bar_s = bars + 16;               // [2] S buffer complete
+    uint64_t *bar_p = bars + 18;               // (first CTA's) P stored by both CTAs
+    uint64_t *bar_o = bars + 19;               // a tile's O products done
+    uint64_t *bar_q = bars + 20;               // (first CTA's) Q stored by both CTAs
+    uint64_t *bar_done = bars + 21;            // (first CTA's) every MMA done
+    int64_t *sUnit = reinterpret_cast<int64_t *>(bars + 22); // [0] total [1] units before the group
+    int *sFlag = reinterpret_cast<int *>(bars + 24);         // [0] abort
+    uint32_t *sTmem = reinterpret_cast<uint32_t *>(sFlag + 1);
+    int *sGroup = sFlag + 2;
+    volatile int *abort_flag = sFlag;
+
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&bar_full[i], 2);
+            mbar_init(&bar_empty[i], 1);
+        }
+        mbar_init(&bar_s[0], 1);
+        mbar_init(&bar_s[1], 1);
+        mbar_init(bar_p, 2 * kWarpsSoft);
+        mbar_init(bar_o, 1);
+        mbar_init(bar_q, 2 * kWarpsSoft);
+        mbar_init(bar_done, 1);
+        sFlag[0] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sTmem)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
     pdl_wait();
     pdl_trigger();
-    if (tid < 32) {
-        int g = 0, t = 0;
-        const bool ok = find_tile(p, tile_id, tid, false, &g, &t);
-        if (tid == 0) { sTile[0] = ok; sTile[1] = g; sTile[2] = t; }
+    if (warp == 1) {
+        const int64_t U = total_units(p, lane, blockIdx.x == 0);
+        int g = 0;
+        int64_t before = 0;
+        const int64_t u0 = run_begin(p, pair, U);
+        if (u0 < U) find_unit(p, u0, lane, &g, &before);
+        if (lane == 0) { sUnit[0] = U; sUnit[1] = before; *sGroup = g; }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *sTmem;
+    const int64_t U = sUnit[0];
+    const int64_t u0 = run_begin(p, pair, U), u1 = run_begin(p, pair + 1, U);
+    Work w;
+    w.start(p, *sGroup, u0 - sUnit[1], u1 - u0);
+    if (tid == 0 && rank == 0) {
+        // for the join: the row tile that this pair begins in
+        DenseBegin d{};
+        d.total = U;
+        if (u1 > u0) {
+            d.first = u0 - w.k0;
+            d.last = d.first + w.kt;
+            d.row0 = w.gr.row0 + w.rt * kRowsPair;
+            d.rows = (int)min((int64_t)kRowsPair, w.gr.rows - w.rt * kRowsPair);
+        }
+        p.begin[pair] = d;
+    }
+    bool more = u1 > u0;
+
+    if (warp == kWarpsSoft + kWarpsProd) {
+        // ============================================== MMA issuer
+        if (rank == 0 && lane == 0) {
+            const uint32_t id_s = instr_desc(128, 256, 0, 0, 0, 0);
+            const uint32_t id_o = instr_desc(128, 256, 0, 0, 0, 1);
+            const uint64_t dq = smem_desc(smem_u32(sQ), 16, 1024, kLayoutSW128);
+            const uint64_t dp = smem_desc(smem_u32(sP), 16, 1024, kLayoutSW128);
+            const uint64_t dk = smem_desc(smem_u32(sRing), 16, 1024, kLayoutSW128);
+            const uint64_t dv = smem_desc(smem_u32(sRing), kVAtom, 1024, kLayoutSW128);
+            uint32_t fills = 0;                // parity of the ring's fill (8 slots at a time)
+            uint32_t tile = 0, pieces = 0;
+            bool ok = true;
+            auto scores = [&](uint32_t buf) {
+#pragma unroll
+                for (int j = 0; j < kSlots; ++j) {
+                    ok = ok && mbar_wait<true>(&bar_full[j], fills, abort_flag);
+                    if (!ok) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma2(tmem + kColS + 128 * buf, dq + ((j * kQAtom + ks * 32) >> 4), dk + ((j * kSlot + ks * 32) >> 4),
+                             id_s, (j > 0 || ks > 0) ? 1u : 0u);
+                    commit2(&bar_empty[j]);
+                }
+                commit2(&bar_s[buf]);
+                fills ^= 1;
+            };
+            for (; more && ok; more = w.next(p), ++pieces) {
+                const int n_tiles = (int)(w.k1 - w.k0);
+                ok = mbar_wait<true>(bar_q, pieces & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                scores(tile & 1);
+                for (int i = 0; i < n_tiles && ok; ++i, ++tile) {
+                    if (i + 1 < n_tiles) scores((tile + 1) & 1);
+                    ok = ok && mbar_wait<true>(bar_p, tile & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < kSlots; ++j) {
+                        ok = ok && mbar_wait<true>(&bar_full[j], fills, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = 0; ks < 2; ++ks) {
+                            const uint64_t a = dp + (((j >> 1) * kQAtom + (2 * (j & 1) + ks) * 32) >> 4);
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                mma2(tmem + 128 * c, a, dv + ((j * kSlot + c * 2 * kVAtom + ks * 2048) >> 4), id_o,
+                                     (i > 0 || j > 0 || ks > 0) ? 1u : 0u);
+                        }
+                        commit2(&bar_empty[j]);
+                    }
+                    if (!ok) break;
+                    commit2(bar_o);
+                    fills ^= 1;
+                }
+            }
+            if (!ok) raise_abort(sFlag);
+            // every MMA has completed before the pair gives its TMEM and shared memory back
+            volatile int no_abort = 0;
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                             smem_u32(bar_done))
+                         : "memory");
+            if (!mbar_wait<true>(bar_done, 0, &no_abort)) raise_abort(sFlag);
+        }
+    } else if (warp >= kWarpsSoft) {
+        // ============================================== producers
+        // Warp j fills slot j of every block of eight, 8 units (32 channels of one
+        // entry: 16 code bytes, 2 scales) per lane; one proxy fence and one arrival
+        // per 16 KB.  The 8 lanes of a store phase hold 8 entries' same piece, so
+        // that the swizzle spreads them over all banks.  The next block's codes are
+        // loaded as soon as this block's are converted.
+        const int pw = warp - kWarpsSoft;
+        const int e8 = lane & 7, half = (lane >> 3) & 1, sub = lane >> 4;
+        const uint32_t full = in_cta(smem_u32(&bar_full[pw]), 0);
+        uint8_t *const slot = sRing + pw * kSlot;
+        uint32_t fills = 1;                    // parity of the next wait on "empty": the first pass is free
+        bool ok = true;
+        uint4 gc[8];
+        uint32_t gs[8];
+        for (; more && ok; more = w.next(p)) {
+            const int n_tiles = (int)(w.k1 - w.k0), n_blocks = 2 * n_tiles;
+            // the blocks: S(0) S(1) O(0) S(2) O(1) ... O(last)
+            auto is_k = [&](int b) { return b == 0 || ((b & 1) != 0 && b != n_blocks - 1); };
+            auto load = [&](int b) {
+                const bool k = is_k(b);
+                const int tile = b == 0 ? 0 : b == n_blocks - 1 ? n_tiles - 1 : (b & 1) ? (b + 1) >> 1 : (b >> 1) - 1;
+                // unit u: K entry 16 u + 8 sub + e8 of this CTA's 128, channels 64 pw + 32 half ..;
+                // V entry 32 pw + 8 (u & 3) + e8, channels 256 (u >> 2) + 128 rank + 64 sub + 32 half ..
+                const int64_t e = (w.k0 + tile) * kEnt + e8 + (k ? 128 * (int)rank + 8 * sub : 32 * pw);
+                const int ch = 32 * half + (k ? 64 * pw : 128 * (int)rank + 64 * sub);
+                const uint8_t *c = p.codes + (w.gr.base + e) * CSA2_CODE_BYTES + (ch >> 1);
+                const uint8_t *s = p.scales + (w.gr.base + e) * CSA2_SCALE_BYTES + (ch >> 4);
+                const int64_t left = w.gr.n - e;      // entries from this thread's first one on
+                if (k) {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        gc[u] = make_uint4(0, 0, 0, 0);
+                        gs[u] = 0;
+                        if (16 * u < left) {
+                            gc[u] = __ldg(reinterpret_cast<const uint4 *>(c + 16 * u * CSA2_CODE_BYTES));
+                            gs[u] = __ldg(reinterpret_cast<const uint16_t *>(s + 16 * u * CSA2_SCALE_BYTES));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        gc[u] = make_uint4(0, 0, 0, 0);
+                        gs[u] = 0;
+                        if (8 * (u & 3) < left) {
+                            gc[u] = __ldg(reinterpret_cast<const uint4 *>(c + 8 * (u & 3) * CSA2_CODE_BYTES + 128 * (u >> 2)));
+                            gs[u] = __ldg(reinterpret_cast<const uint16_t *>(s + 8 * (u & 3) * CSA2_SCALE_BYTES + 16 * (u >> 2)));
+                        }
+                    }
+                }
+            };
+            load(0);
+            for (int b = 0; b < n_blocks && ok; ++b) {
+                const bool k = is_k(b);
+                // unit u goes to dst + u * step (K: rows 16 apart; V: rows 8 apart, atoms 2 apart)
+                uint8_t *dst = slot + (k ? 8 * sub * 128 : sub * kVAtom) + e8 * 128;
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_empty[pw], fills, abort_flag));
+                if (!ok) break;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t p0 = scale_pair(gs[u] & 0xFFu), p1 = scale_pair(gs[u] >> 8);
+                    uint8_t *d = dst + (k ? 16 * u * 128 : 8 * (u & 3) * 128 + (u >> 2) * 2 * kVAtom);
+                    // (rows are a multiple of 8 past e8: the swizzle is that of row e8)
+                    *reinterpret_cast<uint4 *>(d + (((4 * half + 0) ^ e8) << 4)) = fp4x8_to_f16(gc[u].x, p0);
+                    *reinterpret_cast<uint4 *>(d + (((4 * half + 1) ^ e8) << 4)) = fp4x8_to_f16(gc[u].y, p0);
+                    *reinterpret_cast<uint4 *>(d + (((4 * half + 2) ^ e8) << 4)) = fp4x8_to_f16(gc[u].z, p1);
+                    *reinterpret_cast<uint4 *>(d + (((4 * half + 3) ^ e8) << 4)) = fp4x8_to_f16(gc[u].w, p1);
+                }
+                if (b + 1 < n_blocks) load(b + 1);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_at(full);
+                fills ^= 1;
+            }
+        }
+        if (!ok && lane == 0) raise_abort(sFlag);
+    } else {
+        // ============================================== softmax
+        // TMEM lane l < 64 of a buffer holds row l, entries 0 .. 127 of the tile
+        // (O: the first 128 channels of each 256), lane 64 + l the rest.
+        const int quarter = warp & 3, ch = warp >> 2;              // ch: which half of the columns
+        const uint32_t lane_q = (uint32_t)(quarter * 32) << 16;
+        const int row = 32 * (quarter & 1) + lane;
+        const int ent0 = 128 * (quarter >> 1) + 64 * ch;           // its 64 entries of a tile
+        const int which = 2 * (quarter >> 1) + ch;                 // of the row's four threads
+        const uint32_t p_bar = in_cta(smem_u32(bar_p), 0), q_bar = in_cta(smem_u32(bar_q), 0);
+        uint8_t *p_row = sP + which * kQAtom;
+        const float l2s = p.sm_scale * kLog2e;
+        uint32_t tile = 0;
+        bool ok = true;
+        for (; more && ok; more = w.next(p)) {
+            const int64_t row0 = w.gr.row0 + w.rt * kRowsPair + kRowsCta * (int)rank;
+            const int n_rows = (int)max((int64_t)0, min((int64_t)kRowsCta, w.gr.rows - w.rt * kRowsPair - kRowsCta * (int)rank));
+            // ---- Q as f16 (rows past the tile's are zero); every earlier MMA has completed
+            for (int i = tid; i < kRowsCta * (CSA2_D / 8); i += kSoft) {
+                const int r = i / (CSA2_D / 8), c8 = i % (CSA2_D / 8);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < n_rows) {
+                    v = __ldg(reinterpret_cast<const uint4 *>(p.q + (row0 + r) * CSA2_D) + c8);
+                    if (p.q_type == CSA2_BF16)
+                        v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z),
+                                       bf16x2_to_f16x2(v.w));
+                }
+                *reinterpret_cast<uint4 *>(sQ + (c8 >> 3) * kQAtom + sw128(r, c8 & 7)) = v;
+            }
+            if (tid < kRowsCta) sM[tid] = -INFINITY;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_at(q_bar);
+            soft_sync();
+            float l = 0.f;
+            const int n_tiles = (int)(w.k1 - w.k0);
+            for (int i = 0; i < n_tiles; ++i, ++tile) {
+                const uint32_t tS = tmem + kColS + 128 * (tile & 1) + 64 * ch + lane_q;
+                bool got = mbar_wait<true>(&bar_s[tile & 1], (tile >> 1) & 1, abort_flag);
+                tc_fence_after();
+                const int64_t left = w.gr.n - (w.k0 + i) * kEnt - ent0;     // entries of this thread's 64
+                float m = sM[row], top = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    tmem_ld32(tS + 32 * h, x);
+                    tmem_wait_ld();
+                    if (left >= 64) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) top = fmaxf(top, x[c] * l2s);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) top = fmaxf(top, 32 * h + c < left ? x[c] * l2s : -INFINITY);
+                    }
+                }
+                // (a wait that gave up takes the same path, and the vote makes every thread
+                // leave together)
+                if (soft_any(top > m + kLazy || !got)) {
+                    sRed[which * kRowsCta + row] = top;
+                    ok = !soft_any(!got || *abort_flag);
+                    if (!ok) break;
+                    if (tid < kRowsCta) {
+                        const float t = fmaxf(fmaxf(sRed[tid], sRed[kRowsCta + tid]),
+                                              fmaxf(sRed[2 * kRowsCta + tid], sRed[3 * kRowsCta + tid]));
+                        const float old = sM[tid];
+                        const bool moves = t > old + kLazy;
+                        sAlpha[tid] = !moves ? 1.f : old == -INFINITY ? 0.f : fast_exp2(old - t);
+                        if (moves) sM[tid] = t;
+                    }
+                    soft_sync();
+                    m = sM[row];
+                    const float alpha = sAlpha[row];
+                    if (i > 0) {
+                        l *= alpha;
+                        // O *= alpha, once the previous tile's products have completed
+                        const bool done = __all_sync(0xffffffffu, mbar_wait<true>(bar_o, (tile - 1) & 1, abort_flag));
+                        const bool moved = __any_sync(0xffffffffu, alpha != 1.f);
+                        tc_fence_after();
+                        if (done && moved) {
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                float o[32];
+                                const uint32_t ta = tmem + 128 * ch + 32 * c + lane_q;
+                                tmem_ld32(ta, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                                tmem_st32(ta, o);
+                            }
+                            tmem_wait_st();
+                        }
+                        if (!done) raise_abort(sFlag);
+                    }
+                }
+                // P is free once the previous tile's products have completed
+                if (tile > 0 && !mbar_wait<true>(bar_o, (tile - 1) & 1, abort_flag)) raise_abort(sFlag);
+                const float mref = m == -INFINITY ? 0.f : m;    // (no finite logit yet: e^-inf = 0, a NaN stays one)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    tmem_ld32(tS + 32 * h, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        x[c] = fast_exp2(fmaf(x[c], l2s, -mref));
+                        if (left < 64) x[c] = 32 * h + c < left ? x[c] : 0.f;
+                    }
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) s4[c & 3] += x[c];
+                    l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(p_row + sw128((uint32_t)row, (uint32_t)(4 * h + c))) =
+                            make_uint4(f32x2_to_f16x2(x[8 * c], x[8 * c + 1]), f32x2_to_f16x2(x[8 * c + 2], x[8 * c + 3]),
+                                       f32x2_to_f16x2(x[8 * c + 4], x[8 * c + 5]),
+                                       f32x2_to_f16x2(x[8 * c + 6], x[8 * c + 7]));
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(p_bar);
+            }
+            if (!ok) break;
+            // ---- the piece's sums: complete rows are finished, others left for the join
+            const bool whole = w.k0 == 0 && w.k1 == w.kt;
+            const bool done = mbar_wait<true>(bar_o, (tile - 1) & 1, abort_flag);
+            tc_fence_after();
+            sRed[which * kRowsCta + row] = l;
+            ok = !soft_any(!done || *abort_flag);
+            if (!ok) break;
+            l = (sRed[row] + sRed[kRowsCta + row]) + (sRed[2 * kRowsCta + row] + sRed[3 * kRowsCta + row]);
+            const float m = l != l ? 0.f : sM[row];             // (a NaN row is not an empty one)
+            const int chan = 256 * ch + 128 * (quarter >> 1);
+            const int64_t piece = 2 * (int64_t)pair + (w.k0 == 0 ? 1 : 0);
+            Joined j{1.f, 0.f, 0.f};
+            if (whole) {
+                if (row < n_rows) j = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[row0 + row] : 0.f);
+                soft_sync();                   // (all four threads of a row have read prev_lse, which may be lse itself)
+                if (row < n_rows && which == 0 && p.lse) p.lse[row0 + row] = j.lse;
+            } else if (which == 0) {
+                float *ml = p.part_ml + piece * 2 * kRowsPair + kRowsCta * (int)rank + row;
+                ml[0] = m;
+                ml[kRowsPair] = l;
+            }
+            const float own = j.own, pw = j.prev;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float o[32];
+                tmem_ld32(tmem + 128 * ch + 32 * c + lane_q, o);
+                tmem_wait_ld();
+                if (whole && row < n_rows) {
+                    const int64_t at = (row0 + row) * CSA2_D + chan + 32 * c;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float4 v = make_float4(o[4 * k] * own, o[4 * k + 1] * own, o[4 * k + 2] * own, o[4 * k + 3] * own);
+                        if (pw != 0.f) {
+                            const float4 q4 = *reinterpret_cast<const float4 *>(p.prev_out + at + 4 * k);
+                            v = make_float4(fmaf(q4.x, pw, v.x), fmaf(q4.y, pw, v.y), fmaf(q4.z, pw, v.z), fmaf(q4.w, pw, v.w));
+                        }
+                        store4(p.out, p.out_type, at + 4 * k, v.x, v.y, v.z, v.w);
+                    }
+                } else if (row < n_rows) {
+                    float *dst = p.part_o + (piece * kRowsPair + kRowsCta * (int)rank + row) * CSA2_D + chan + 32 * c;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<float4 *>(dst + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            soft_sync();                       // sRed, sM and O are read
+        }
+        if (!ok && lane == 0) raise_abort(sFlag);
+    }
+    // groups without entries
+    if (warp != kWarpsSoft + kWarpsProd)
+        for (int g = pair; g < p.ng; g += p.pairs) {
+            const Group gr = group_of(p, g);
+            if (!gr.bad && gr.n == 0)
+                empty_rows(p, gr, (int)rank * 32 * (kWarpsSoft + kWarpsProd) + tid, 2 * 32 * (kWarpsSoft + kWarpsProd));
+        }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort_flag) count_event(p.counters, CSA2_CNT_TIMEOUT);
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// Joins the pieces of the row tiles that lie in several pairs' runs, in the
+// pairs' order, and the caller's partial result.  Pair c >= 1 answers for a
+// tile when it is the first to begin inside it; its pieces are the second slot
+// of pair c - 1 and the first of c, c + 1, ...  A thread takes 4 channels of a
+// row; the pieces of a tile are dealt to `parts` threads each (1, 2 or 4), whose
+// sums are added in order.  A block's item is 4 / parts whole rows, so that lse
+// may be prev_lse itself.
+__global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
+{
+    __shared__ int sPair[kDensePairsMax], sItem[kDensePairsMax], sWarp[kJoinThreads / 32];
+    __shared__ float sW[4][kDensePairsMax];
+    __shared__ float4 sO[kJoinThreads];
+    __shared__ Joined sJ[4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    pdl_trigger();
+    // the tiles to join (in order) and their work items; every thread looks at one pair
+    auto ends = [&](int c, const DenseBegin &d) {
+        // pairs c .. that begin before d.last: run_begin(x) = x U / P < last
+        const int64_t P = min((int64_t)p.pairs, d.total);
+        return (int)min(P, (d.last * P + d.total - 1) / d.total);
+    };
+    auto parts_of = [](int n_pieces) { return n_pieces <= 4 ? 1 : n_pieces <= 8 ? 2 : 4; };
+    int items = 0;
+    if (tid > 0 && tid < p.pairs) {
+        const DenseBegin d = p.begin[tid];
+        const int64_t b0 = run_begin(p, tid, d.total);
+        if (b0 < d.total && b0 > d.first && run_begin(p, tid - 1, d.total) <= d.first) {
+            const int parts = parts_of(ends(tid, d) - tid + 1);
+            items = (d.rows * (CSA2_D / 4) * parts + kJoinThreads - 1) / kJoinThreads;
+        }
+    }
+    const uint32_t has = __ballot_sync(0xffffffffu, items > 0);
+    int upto = items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sWarp[warp] = upto;
+    if (lane == 0) sPair[warp] = __popc(has);        // (counts, until the list is written)
+    __syncthreads();
+    int before = 0, n = 0, total = 0, tiles = 0;
+    for (int i = 0; i < kJoinThreads / 32; ++i) {
+        if (i < warp) { before += sWarp[i]; n += sPair[i]; }
+        total += sWarp[i];
+        tiles += sPair[i];
     }
     __syncthreads();
-    if (!sTile[0]) return;
-    const Group gr = group_of(p, sTile[1]);
-    const int r = 4 * (int)(blockIdx.x % (kTileR / 4)) + (tid >> 7), c = 4 * (tid & 127);
-    const int64_t in_group = (int64_t)sTile[2] * kTileR + r;
-    if (in_group >= gr.rows) return;
-    const int64_t row = gr.row0 + in_group;
-    const float *ml = p.part_ml + tile_id * p.splits * 128 + r;
-    float m = -INFINITY;
-    for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * 128]);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float *src = p.part_o + (tile_id * p.splits * 64 + r) * CSA2_D + c;
-    for (int s = 0; s < p.splits; ++s) {
-        const float ms = ml[s * 128];
-        if (ms == -INFINITY) continue;
-        const float w = fast_exp2(ms - m);
-        l = fmaf(ml[s * 128 + 64], w, l);
-        const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)s * 64 * CSA2_D);
-        o.x = fmaf(v.x, w, o.x); o.y = fmaf(v.y, w, o.y); o.z = fmaf(v.z, w, o.z); o.w = fmaf(v.w, w, o.w);
+    if (items > 0) {
+        const int at = n + __popc(has & ((1u << lane) - 1));
+        sPair[at] = tid;
+        sItem[at] = before + upto - items;
     }
-    const Joined j = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[row] : 0.f);
-    float4 pv = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (j.prev != 0.f) pv = *reinterpret_cast<const float4 *>(p.prev_out + row * CSA2_D + c);
-    const float v[4] = {fmaf(pv.x, j.prev, o.x * j.own), fmaf(pv.y, j.prev, o.y * j.own),
-                        fmaf(pv.z, j.prev, o.z * j.own), fmaf(pv.w, j.prev, o.w * j.own)};
+    __syncthreads();
+    int at = 0;
+    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+        while (at + 1 < tiles && sItem[at + 1] <= item) ++at;
+        const int c = sPair[at];
+        const DenseBegin d = p.begin[c];
+        const int n_pieces = ends(c, d) - c + 1, parts = parts_of(n_pieces);
+        const int wide = kJoinThreads / parts;            // threads (of 4 channels) side by side
+        const int part = tid / wide;
+        const int cell = (item - sItem[at]) * wide + tid % wide;
+        const int r = cell / (CSA2_D / 4), ch = 4 * (cell % (CSA2_D / 4));
+        const int r0 = (item - sItem[at]) * wide / (CSA2_D / 4);    // the item's rows: r0 .. r0 + 4 / parts - 1
+        auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c - 1 + i); };
+        __syncthreads();                              // (the last item's shared values are read)
+        if (warp < 4 / parts && r0 + warp < d.rows) {
+            const int64_t row = d.row0 + r0 + warp;
+            float m = -INFINITY, l = 0.f;
+            for (int i = lane; i < n_pieces; i += 32) m = fmaxf(m, p.part_ml[slot(i) * 2 * kRowsPair + r0 + warp]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) store_out(p.out, p.out_type, row * CSA2_D + c + i, v[i]);
-    if (p.lse && c == 0) p.lse[row] = j.lse;
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int i = lane; i < n_pieces; i += 32) {
+                const float *ml = p.part_ml + slot(i) * 2 * kRowsPair + r0 + warp;
+                const float wgt = ml[0] == -INFINITY ? 0.f : fast_exp2(ml[0] - m);
+                sW[warp][i] = wgt;
+                l = fmaf(ml[kRowsPair], wgt, l);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (lane == 0) sJ[warp] = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[row] : 0.f);
+        }
+        __syncthreads();
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < d.rows) {
+            const float *src = p.part_o + (int64_t)r * CSA2_D + ch;
+            for (int i0 = part; i0 < n_pieces; i0 += 4 * parts) {
+                float4 v[4];
+                float wgt[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = i0 + k * parts;
+                    wgt[k] = i < n_pieces ? sW[r - r0][i] : 0.f;
+                    // (a piece without weight may hold anything)
+                    v[k] = wgt[k] != 0.f ? *reinterpret_cast<const float4 *>(src + slot(i) * kRowsPair * CSA2_D)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    o.x = fmaf(v[k].x, wgt[k], o.x); o.y = fmaf(v[k].y, wgt[k], o.y);
+                    o.z = fmaf(v[k].z, wgt[k], o.z); o.w = fmaf(v[k].w, wgt[k], o.w);
+                }
+            }
+        }
+        if (parts > 1) {
+            sO[tid] = o;
+            __syncthreads();
+            if (part == 0)
+                for (int i = 1; i < parts; ++i) {
+                    const float4 v = sO[i * wide + tid];
+                    o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+                }
+        }
+        if (part == 0 && r < d.rows) {
+            const int64_t row = d.row0 + r;
+            const Joined j = sJ[r - r0];
+            float4 pv = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j.prev != 0.f) pv = *reinterpret_cast<const float4 *>(p.prev_out + row * CSA2_D + ch);
+            store4(p.out, p.out_type, row * CSA2_D + ch, fmaf(pv.x, j.prev, o.x * j.own), fmaf(pv.y, j.prev, o.y * j.own),
+                   fmaf(pv.z, j.prev, o.z * j.own), fmaf(pv.w, j.prev, o.w * j.own));
+        }
+        if (p.lse && tid < 4 / parts && r0 + tid < d.rows) p.lse[d.row0 + r0 + tid] = sJ[tid].lse;
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_dense(const DenseParams &p, cudaStream_t st)
 {
-    const size_t smem = 1024 + kDV + kDQ + kDP + (4 + 5) * 64 * 4 + 8 * 8 + 8 * 4 + 16;
+    constexpr size_t smem = 1024 + kSlots * kSlot + kQBytes + kPBytes + 6 * kRowsCta * 4 + 26 * 8;
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(dense_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_k(dense_attn_kernel, dim3((unsigned)p.splits * p.tiles), dim3(kDThreads), smem, st, 0, p);
-    if (e == cudaSuccess && p.splits > 1)
-        e = launch_k(dense_join_kernel, dim3((unsigned)(kTileR / 4) * p.tiles), dim3(512), 0, st, 0, p);
+    e = launch_k(dense_attn_kernel, dim3(2 * p.pairs), dim3(kThreads), smem, st, 2, p);
+    if (e == cudaSuccess && p.pairs > 1)
+        e = launch_k(dense_join_kernel, dim3(8 * p.pairs), dim3(kJoinThreads), 0, st, 0, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

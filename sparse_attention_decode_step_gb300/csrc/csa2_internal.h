@@ -121,7 +121,12 @@ cudaError_t launch_cache_read(const csa2_cache &c, const int64_t *rows, int64_t 
                               uint32_t *counters, cudaStream_t st);
 
 // ---- dense attention of query groups
-constexpr int kDenseRows = 64;          // (query, head) rows per CTA
+constexpr int kDenseRows = 128;         // (query, head) rows of a tile, one pair of CTAs
+constexpr int kDenseEntries = 256;      // entries of a tile
+constexpr int kDensePairsMax = 512;     // pairs of CTAs of a launch
+// Where a pair's run of tiles begins: the row tile's units [first, last) of
+// `total`, and its rows.
+struct DenseBegin { int64_t first, last, total, row0; int rows, pad; };
 struct DenseParams {
     const uint8_t *codes, *scales;
     const int64_t *seq_base;
@@ -138,13 +143,13 @@ struct DenseParams {
     void *out;
     int out_type;
     float *lse;
-    int tiles;          // bound on the row tiles of all groups
-    int splits;         // CTAs per row tile
-    float *part_o;      // [tiles][splits][64][512] unnormalised sums
-    float *part_ml;     // [tiles][splits][m | l][64]
+    int pairs;          // pairs of CTAs
+    float *part_o;      // [pairs][2][128][512] unnormalised sums of the pieces of row tiles
+    float *part_ml;     // [pairs][2][m | l][128]
+    DenseBegin *begin;  // [pairs]
     uint32_t *counters;
 };
-struct DensePlan { int tiles, splits; size_t off_ml, total; };
+struct DensePlan { int pairs; size_t off_ml, off_begin, total; };
 DensePlan dense_plan(int ng, int nq, int H, int64_t max_n);
 cudaError_t launch_dense(const DenseParams &p, cudaStream_t st);
 
