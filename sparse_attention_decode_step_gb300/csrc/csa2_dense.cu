@@ -43,18 +43,18 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kWarpsSoft = 8, kWarpsProd = 8;   // (a producer warp per ring slot)
+constexpr int kWarpsSoft = 8, kWarpsProd = 8;
 constexpr int kThreads = 32 * (kWarpsSoft + kWarpsProd + 1);
 constexpr int kSoft = 32 * kWarpsSoft;
 constexpr int kRowsPair = kDenseRows;          // rows per pair of CTAs
 constexpr int kRowsCta = kRowsPair / 2;
 constexpr int kEnt = kDenseEntries;            // entries per tile
-constexpr int kSlots = 8;
-constexpr uint32_t kSlot = 16384;
+constexpr int kStages = 2;
+constexpr uint32_t kStage = 65536;
 constexpr uint32_t kQBytes = kRowsCta * CSA2_D * 2;     // 64 KB: [8 atoms][64 rows][128 B]
 constexpr uint32_t kQAtom = kRowsCta * 128;
 constexpr uint32_t kPBytes = kRowsCta * kEnt * 2;       // 32 KB: [4 atoms][64 rows][128 B]
-constexpr uint32_t kVAtom = 32 * 128;                   // V slot: [4 atoms of 64 channels][32 entries][128 B]
+constexpr uint32_t kAtom = 128 * 128;                   // stage: [4 atoms of 64 channels][128 entries][128 B]
 constexpr uint32_t kColS = 256;                // TMEM: O in columns 0 .. 255, S buffer b from 256 + 128 b
 constexpr int kJoinThreads = 512;
 constexpr float kLazy = 8.0f;                  // log2 units
@@ -259,6 +259,26 @@ __device__ __forceinline__ bool soft_any(bool v)
     return r != 0;
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b)
+{
+    uint64_t d;
+    asm("{\n"
+        ".reg .b64 ra, rb;\n"
+        "mov.b64 ra, {%1, %2};\n"
+        "mov.b64 rb, {%3, %4};\n"
+        "add.rn.f32x2 %0, ra, rb;\n"
+        "}\n"
+        : "=l"(d)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return make_float2(__uint_as_float((uint32_t)d), __uint_as_float((uint32_t)(d >> 32)));
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
 {
     float a[16], b[16];
@@ -319,21 +339,22 @@ __device__ __forceinline__ void empty_rows(const DenseParams &p, const Group &gr
 
 __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const uint32_t rank = cta_rank();
     const int pair = (int)(blockIdx.x >> 1);
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *sRing = smem;                     // [8 slots][16 KB]
-    uint8_t *sQ = sRing + kSlots * kSlot;
+    uint8_t *sRing = smem;                     // [2 stages][64 KB]
+    uint8_t *sQ = sRing + kStages * kStage;
     uint8_t *sP = sQ + kQBytes;
     float *sRed = reinterpret_cast<float *>(sP + kPBytes);   // [4 threads of a row][64 rows]
     float *sM = sRed + 4 * kRowsCta;           // reference max per row (log2 units)
     float *sAlpha = sM + kRowsCta;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sAlpha + kRowsCta);
-    uint64_t *bar_full = bars;                 // [8] (first CTA's) slot filled by both CTAs
-    uint64_t *bar_empty = bars + 8;            // [8] slot's MMAs done
+    uint64_t *bar_full = bars;                 // [2] (first CTA's) stage filled by both CTAs
+    uint64_t *bar_empty = bars + 8;            // [2] stage's MMAs done
     uint64_t *bar_s = bars + 16;               // [2] S buffer complete
     uint64_t *bar_p = bars + 18;               // (first CTA's) P stored by both CTAs
     uint64_t *bar_o = bars + 19;               // a tile's O products done
@@ -346,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     volatile int *abort_flag = sFlag;
 
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&bar_full[i], 2);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bar_full[i], 2 * kWarpsProd);
             mbar_init(&bar_empty[i], 1);
         }
         mbar_init(&bar_s[0], 1);
@@ -399,142 +420,176 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 
     if (warp == kWarpsSoft + kWarpsProd) {
         // ============================================== MMA issuer
-        if (rank == 0 && lane == 0) {
-            const uint32_t id_s = instr_desc(128, 256, 0, 0, 0, 0);
-            const uint32_t id_o = instr_desc(128, 256, 0, 0, 0, 1);
-            const uint64_t dq = smem_desc(smem_u32(sQ), 16, 1024, kLayoutSW128);
-            const uint64_t dp = smem_desc(smem_u32(sP), 16, 1024, kLayoutSW128);
-            const uint64_t dk = smem_desc(smem_u32(sRing), 16, 1024, kLayoutSW128);
-            const uint64_t dv = smem_desc(smem_u32(sRing), kVAtom, 1024, kLayoutSW128);
-            uint32_t fills = 0;                // parity of the ring's fill (8 slots at a time)
+        // The whole warp runs the loop and one elected lane issues: descriptors and
+        // waits then stay in uniform registers.  (Measured for a wait, four MMAs and
+        // a commit: 258 cycles, the MMAs' own time; with a branch on lane 0 around
+        // the loop 404 to 483.)
+        if (rank == 0) {
+            uint32_t elected;
+            asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(elected));
+            constexpr uint32_t id_s = instr_desc(128, 256, 0, 0, 0, 0);
+            constexpr uint32_t id_o = instr_desc(128, 256, 0, 0, 0, 1);
+            const uint32_t ring = __shfl_sync(0xffffffffu, smem_u32(sRing), 0);
+            const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t dq = smem_desc(ring + kStages * kStage, 16, 1024, kLayoutSW128);
+            const uint64_t dp = smem_desc(ring + kStages * kStage + kQBytes, 16, 1024, kLayoutSW128);
+            const uint64_t dk = smem_desc(ring, 16, 1024, kLayoutSW128);
+            const uint64_t dv = smem_desc(ring, kAtom, 1024, kLayoutSW128);
+            uint32_t fills = 0;                // parity of the ring's fill (all stages at a time)
             uint32_t tile = 0, pieces = 0;
             bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+                tc_fence_after();
+            };
             auto scores = [&](uint32_t buf) {
-#pragma unroll
-                for (int j = 0; j < kSlots; ++j) {
-                    ok = ok && mbar_wait<true>(&bar_full[j], fills, abort_flag);
+                const uint32_t d = t0 + kColS + 128 * buf;
+#pragma unroll 1
+                for (uint32_t j = 0; j < kStages; ++j) {
+                    wait(&bar_full[j], fills);
                     if (!ok) return;
-                    tc_fence_after();
+                    if (elected) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma2(tmem + kColS + 128 * buf, dq + ((j * kQAtom + ks * 32) >> 4), dk + ((j * kSlot + ks * 32) >> 4),
-                             id_s, (j > 0 || ks > 0) ? 1u : 0u);
-                    commit2(&bar_empty[j]);
+                        for (int ks = 0; ks < 16; ++ks)
+                            mma2(d, dq + (j * (4 * kQAtom >> 4) + (ks >> 2) * (kQAtom >> 4) + 2 * (ks & 3)),
+                                 dk + (j * (kStage >> 4) + (ks >> 2) * (kAtom >> 4) + 2 * (ks & 3)), id_s, ks > 0 ? 1u : j);
+                        commit2(&bar_empty[j]);
+                        if (j == kStages - 1) commit2(&bar_s[buf]);
+                    }
+                    __syncwarp();
                 }
-                commit2(&bar_s[buf]);
                 fills ^= 1;
             };
             for (; more && ok; more = w.next(p), ++pieces) {
                 const int n_tiles = (int)(w.k1 - w.k0);
-                ok = mbar_wait<true>(bar_q, pieces & 1, abort_flag);
+                wait(bar_q, pieces & 1);
                 if (!ok) break;
-                tc_fence_after();
                 scores(tile & 1);
                 for (int i = 0; i < n_tiles && ok; ++i, ++tile) {
                     if (i + 1 < n_tiles) scores((tile + 1) & 1);
-                    ok = ok && mbar_wait<true>(bar_p, tile & 1, abort_flag);
+                    wait(bar_p, tile & 1);
                     if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int j = 0; j < kSlots; ++j) {
-                        ok = ok && mbar_wait<true>(&bar_full[j], fills, abort_flag);
+#pragma unroll 1
+                    for (uint32_t j = 0; j < kStages; ++j) {
+                        wait(&bar_full[j], fills);
                         if (!ok) break;
-                        tc_fence_after();
+                        if (elected) {
 #pragma unroll
-                        for (int ks = 0; ks < 2; ++ks) {
-                            const uint64_t a = dp + (((j >> 1) * kQAtom + (2 * (j & 1) + ks) * 32) >> 4);
+                            for (int ks = 0; ks < 8; ++ks) {
+                                const uint64_t a = dp + (j * (2 * kQAtom >> 4) + (ks >> 2) * (kQAtom >> 4) + 2 * (ks & 3));
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                mma2(tmem + 128 * c, a, dv + ((j * kSlot + c * 2 * kVAtom + ks * 2048) >> 4), id_o,
-                                     (i > 0 || j > 0 || ks > 0) ? 1u : 0u);
+                                for (int c = 0; c < 2; ++c)
+                                    mma2(t0 + 128 * c, a, dv + (j * (kStage >> 4) + ((c * 2 * kAtom + ks * 2048) >> 4)), id_o,
+                                         ks > 0 ? 1u : (uint32_t)i | j);
+                            }
+                            commit2(&bar_empty[j]);
+                            if (j == kStages - 1) commit2(bar_o);
                         }
-                        commit2(&bar_empty[j]);
+                        __syncwarp();
                     }
-                    if (!ok) break;
-                    commit2(bar_o);
                     fills ^= 1;
                 }
             }
-            if (!ok) raise_abort(sFlag);
             // every MMA has completed before the pair gives its TMEM and shared memory back
             volatile int no_abort = 0;
-            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                             smem_u32(bar_done))
-                         : "memory");
-            if (!mbar_wait<true>(bar_done, 0, &no_abort)) raise_abort(sFlag);
+            if (elected)
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                 smem_u32(bar_done))
+                             : "memory");
+            __syncwarp();
+            if (!mbar_wait<true>(bar_done, 0, &no_abort)) ok = false;
+            if (!ok && elected) raise_abort(sFlag);
         }
     } else if (warp >= kWarpsSoft) {
         // ============================================== producers
-        // Warp j fills slot j of every block of eight, 8 units (32 channels of one
-        // entry: 16 code bytes, 2 scales) per lane; one proxy fence and one arrival
-        // per 16 KB.  The 8 lanes of a store phase hold 8 entries' same piece, so
-        // that the swizzle spreads them over all banks.  The next block's codes are
-        // loaded as soon as this block's are converted.
+        // A stage is 1,024 units of 32 channels of one entry (16 code bytes, 2
+        // scales), four per lane of the eight warps.  Eight lanes read one entry's
+        // 128 code bytes, a whole line: the L1 port serves these loads, the stores
+        // into the ring and the tensor core's operand reads alike, and is what the
+        // kernel runs out of first (with 64 or 32 bytes of an entry per eight lanes
+        // the loads took 95 us of 298 at 32 x 64 heads x 65,536 entries).  Those eight
+        // lanes write their four 16-byte pieces each in an order turned by 0 .. 3, so
+        // that they hit eight bank groups at every store.  Codes are loaded a whole
+        // ring (two stages) ahead.
         const int pw = warp - kWarpsSoft;
-        const int e8 = lane & 7, half = (lane >> 3) & 1, sub = lane >> 4;
-        const uint32_t full = in_cta(smem_u32(&bar_full[pw]), 0);
-        uint8_t *const slot = sRing + pw * kSlot;
+        const int half = lane & 1, atom = (lane >> 1) & 3, e4 = lane >> 3;
+        const bool turn1 = (atom & 1) != 0, turn2 = (atom & 2) != 0;
+        const uint32_t full0 = in_cta(smem_u32(bar_full), 0);
+        uint32_t piece[4];                     // the four stores of an entry e4 mod 8; of e4 + 4 mod 8: ^ 64
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            piece[i] = smem_u32(sRing) + atom * kAtom + (16 * pw + e4) * 128u +
+                       (uint32_t)(((4 * half + ((i + atom) & 3)) ^ e4) << 4);
         uint32_t fills = 1;                    // parity of the next wait on "empty": the first pass is free
         bool ok = true;
-        uint4 gc[8];
-        uint32_t gs[8];
+        uint4 gc[4 * kStages];
+        uint32_t gs[4 * kStages];
         for (; more && ok; more = w.next(p)) {
             const int n_tiles = (int)(w.k1 - w.k0), n_blocks = 2 * n_tiles;
-            // the blocks: S(0) S(1) O(0) S(2) O(1) ... O(last)
-            auto is_k = [&](int b) { return b == 0 || ((b & 1) != 0 && b != n_blocks - 1); };
-            auto load = [&](int b) {
-                const bool k = is_k(b);
+            // The blocks of two stages: S(0) S(1) O(0) S(2) O(1) ... O(last).  Unit u of
+            // stage s is, for S, entry 16 pw + 4 u + e4 of this CTA's 128, channels
+            // 256 s + ..; for O, that entry of the tile's s-th 128, channels 256 rank + ..
+            const uint8_t *c0 = nullptr, *s0 = nullptr;
+            int c_step = 0, s_step = 0, left = 0, left_s = 0;
+            bool inside = true;                // the whole tile lies inside the sequence
+            auto begin = [&](int b) {
+                const bool k = b == 0 || ((b & 1) != 0 && b != n_blocks - 1);
                 const int tile = b == 0 ? 0 : b == n_blocks - 1 ? n_tiles - 1 : (b & 1) ? (b + 1) >> 1 : (b >> 1) - 1;
-                // unit u: K entry 16 u + 8 sub + e8 of this CTA's 128, channels 64 pw + 32 half ..;
-                // V entry 32 pw + 8 (u & 3) + e8, channels 256 (u >> 2) + 128 rank + 64 sub + 32 half ..
-                const int64_t e = (w.k0 + tile) * kEnt + e8 + (k ? 128 * (int)rank + 8 * sub : 32 * pw);
-                const int ch = 32 * half + (k ? 64 * pw : 128 * (int)rank + 64 * sub);
-                const uint8_t *c = p.codes + (w.gr.base + e) * CSA2_CODE_BYTES + (ch >> 1);
-                const uint8_t *s = p.scales + (w.gr.base + e) * CSA2_SCALE_BYTES + (ch >> 4);
-                const int64_t left = w.gr.n - e;      // entries from this thread's first one on
-                if (k) {
+                const int64_t e = (w.k0 + tile) * kEnt;
+                const int mine = e4 + 16 * pw + (k ? 128 * (int)rank : 0);
+                const int ch = 64 * atom + 32 * half + (k ? 0 : 256 * (int)rank);
+                inside = e + kEnt <= w.gr.n;
+                left = (int)(w.gr.n - e) - mine;
+                c0 = p.codes + (w.gr.base + e + mine) * CSA2_CODE_BYTES + (ch >> 1);
+                s0 = p.scales + (w.gr.base + e + mine) * CSA2_SCALE_BYTES + (ch >> 4);
+                c_step = k ? 128 : 128 * CSA2_CODE_BYTES;
+                s_step = k ? 16 : 128 * CSA2_SCALE_BYTES;
+                left_s = k ? 0 : 128;
+            };
+            auto load = [&](int s) {
+                const uint8_t *c = c0 + s * c_step, *sc = s0 + s * s_step;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        gc[u] = make_uint4(0, 0, 0, 0);
-                        gs[u] = 0;
-                        if (16 * u < left) {
-                            gc[u] = __ldg(reinterpret_cast<const uint4 *>(c + 16 * u * CSA2_CODE_BYTES));
-                            gs[u] = __ldg(reinterpret_cast<const uint16_t *>(s + 16 * u * CSA2_SCALE_BYTES));
-                        }
+                for (int u = 0; u < 4; ++u) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    uint32_t t = 0;
+                    if (inside || left_s * s + 4 * u < left) {
+                        v = __ldg(reinterpret_cast<const uint4 *>(c + 4 * u * CSA2_CODE_BYTES));
+                        t = __ldg(reinterpret_cast<const uint16_t *>(sc + 4 * u * CSA2_SCALE_BYTES));
                     }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        gc[u] = make_uint4(0, 0, 0, 0);
-                        gs[u] = 0;
-                        if (8 * (u & 3) < left) {
-                            gc[u] = __ldg(reinterpret_cast<const uint4 *>(c + 8 * (u & 3) * CSA2_CODE_BYTES + 128 * (u >> 2)));
-                            gs[u] = __ldg(reinterpret_cast<const uint16_t *>(s + 8 * (u & 3) * CSA2_SCALE_BYTES + 16 * (u >> 2)));
-                        }
-                    }
+                    gc[4 * s + u] = v;
+                    gs[4 * s + u] = t;
                 }
             };
-            load(0);
-            for (int b = 0; b < n_blocks && ok; ++b) {
-                const bool k = is_k(b);
-                // unit u goes to dst + u * step (K: rows 16 apart; V: rows 8 apart, atoms 2 apart)
-                uint8_t *dst = slot + (k ? 8 * sub * 128 : sub * kVAtom) + e8 * 128;
-                ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_empty[pw], fills, abort_flag));
-                if (!ok) break;
+            begin(0);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const uint32_t p0 = scale_pair(gs[u] & 0xFFu), p1 = scale_pair(gs[u] >> 8);
-                    uint8_t *d = dst + (k ? 16 * u * 128 : 8 * (u & 3) * 128 + (u >> 2) * 2 * kVAtom);
-                    // (rows are a multiple of 8 past e8: the swizzle is that of row e8)
-                    *reinterpret_cast<uint4 *>(d + (((4 * half + 0) ^ e8) << 4)) = fp4x8_to_f16(gc[u].x, p0);
-                    *reinterpret_cast<uint4 *>(d + (((4 * half + 1) ^ e8) << 4)) = fp4x8_to_f16(gc[u].y, p0);
-                    *reinterpret_cast<uint4 *>(d + (((4 * half + 2) ^ e8) << 4)) = fp4x8_to_f16(gc[u].z, p1);
-                    *reinterpret_cast<uint4 *>(d + (((4 * half + 3) ^ e8) << 4)) = fp4x8_to_f16(gc[u].w, p1);
+            for (int s = 0; s < kStages; ++s) load(s);
+            for (int b = 0; b < n_blocks && ok; ++b) {
+                const bool ahead = b + 1 < n_blocks;
+                if (ahead) begin(b + 1);
+#pragma unroll
+                for (int s = 0; s < kStages; ++s) {
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(&bar_empty[s], fills, abort_flag));
+                    if (!ok) break;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t sc = e4m3x2_to_f16x2(gs[4 * s + u]);
+                        const uint32_t p0 = __byte_perm(sc, 0, 0x1010), p1 = __byte_perm(sc, 0, 0x3232);
+                        uint4 c = gc[4 * s + u];
+                        if (turn1) c = make_uint4(c.y, c.z, c.w, c.x);
+                        if (turn2) c = make_uint4(c.z, c.w, c.x, c.y);
+                        const uint32_t q0 = turn2 ? p1 : p0, q1 = turn1 != turn2 ? p1 : p0;
+                        const uint32_t q2 = turn2 ? p0 : p1, q3 = turn1 != turn2 ? p0 : p1;
+                        const uint32_t d = s * kStage + 4 * u * 128, x = (u & 1) * 64;
+                        st_shared16((piece[0] ^ x) + d, fp4x8_to_f16(c.x, q0));
+                        st_shared16((piece[1] ^ x) + d, fp4x8_to_f16(c.y, q1));
+                        st_shared16((piece[2] ^ x) + d, fp4x8_to_f16(c.z, q2));
+                        st_shared16((piece[3] ^ x) + d, fp4x8_to_f16(c.w, q3));
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_at(full0 + 8 * s);
+                    if (ahead) load(s);
                 }
-                if (b + 1 < n_blocks) load(b + 1);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_at(full);
                 fills ^= 1;
             }
         }
@@ -551,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         const uint32_t p_bar = in_cta(smem_u32(bar_p), 0), q_bar = in_cta(smem_u32(bar_q), 0);
         uint8_t *p_row = sP + which * kQAtom;
         const float l2s = p.sm_scale * kLog2e;
+        const float worst = l2s >= 0.f ? -INFINITY : INFINITY;     // a score that never is the largest logit
         uint32_t tile = 0;
         bool ok = true;
         for (; more && ok; more = w.next(p)) {
@@ -580,20 +636,28 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 bool got = mbar_wait<true>(&bar_s[tile & 1], (tile >> 1) & 1, abort_flag);
                 tc_fence_after();
                 const int64_t left = w.gr.n - (w.k0 + i) * kEnt - ent0;     // entries of this thread's 64
-                float m = sM[row], top = -INFINITY;
+                float m = sM[row];
+                // the largest logit: of the scores if sm_scale >= 0, else of their negatives
+                float hi = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float x[32];
                     tmem_ld32(tS + 32 * h, x);
                     tmem_wait_ld();
-                    if (left >= 64) {
+                    if (left < 64) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) top = fmaxf(top, x[c] * l2s);
+                        for (int c = 0; c < 32; ++c)
+                            if (32 * h + c >= left) x[c] = worst;
+                    }
+                    if (l2s >= 0.f) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) hi = fmaxf(hi, x[c]);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) top = fmaxf(top, 32 * h + c < left ? x[c] * l2s : -INFINITY);
+                        for (int c = 0; c < 32; ++c) hi = fmaxf(hi, -x[c]);
                     }
                 }
+                const float top = hi == -INFINITY ? hi : hi * fabsf(l2s);
                 // (a wait that gave up takes the same path, and the vote makes every thread
                 // leave together)
                 if (soft_any(top > m + kLazy || !got)) {
@@ -642,14 +706,24 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                     tmem_ld32(tS + 32 * h, x);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        x[c] = fast_exp2(fmaf(x[c], l2s, -mref));
-                        if (left < 64) x[c] = 32 * h + c < left ? x[c] : 0.f;
+                    for (int c = 0; c < 32; c += 2) {
+                        const float2 y = fma_f32x2(make_float2(x[c], x[c + 1]), make_float2(l2s, l2s), make_float2(-mref, -mref));
+                        x[c] = fast_exp2(y.x);
+                        x[c + 1] = fast_exp2(y.y);
                     }
-                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (left < 64) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) s4[c & 3] += x[c];
-                    l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                        for (int c = 0; c < 32; ++c)
+                            if (32 * h + c >= left) x[c] = 0.f;
+                    }
+                    float2 sum[2] = {make_float2(x[0], x[1]), make_float2(x[2], x[3])};
+#pragma unroll
+                    for (int c = 4; c < 32; c += 4) {
+                        sum[0] = add_f32x2(sum[0], make_float2(x[c], x[c + 1]));
+                        sum[1] = add_f32x2(sum[1], make_float2(x[c + 2], x[c + 3]));
+                    }
+                    const float2 s2 = add_f32x2(sum[0], sum[1]);
+                    l += s2.x + s2.y;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         *reinterpret_cast<uint4 *>(p_row + sw128((uint32_t)row, (uint32_t)(4 * h + c))) =
@@ -672,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             if (!ok) break;
             l = (sRed[row] + sRed[kRowsCta + row]) + (sRed[2 * kRowsCta + row] + sRed[3 * kRowsCta + row]);
             const float m = l != l ? 0.f : sM[row];             // (a NaN row is not an empty one)
-            const int chan = 256 * ch + 128 * (quarter >> 1);
+            const int chan = 256 * (quarter >> 1) + 128 * ch;
             const int64_t piece = 2 * (int64_t)pair + (w.k0 == 0 ? 1 : 0);
             Joined j{1.f, 0.f, 0.f};
             if (whole) {
@@ -863,7 +937,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
 
 cudaError_t launch_dense(const DenseParams &p, cudaStream_t st)
 {
-    constexpr size_t smem = 1024 + kSlots * kSlot + kQBytes + kPBytes + 6 * kRowsCta * 4 + 26 * 8;
+    constexpr size_t smem = 1024 + kStages * kStage + kQBytes + kPBytes + 6 * kRowsCta * 4 + 26 * 8;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(dense_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
