@@ -66,9 +66,9 @@ static_assert(kRowsPair == 128 && kEnt == 256, "lane and column maps below");
 // What a group asks for.  bad: its arguments are out of contract and its rows
 // are left as they are.
 struct Group {
-    int64_t base;
-    int64_t row0;        // first row (query * H)
-    int64_t rows;
+    int base;            // cache row of entry 0 (a cache has under 2^31 rows)
+    int row0;            // first row (query * H, under 2^30)
+    int rows;
     int n;
     bool bad;
 };
@@ -81,31 +81,25 @@ __device__ __forceinline__ Group group_of(const DenseParams &p, int g)
     if (r.bad) return r;
     const int64_t len = p.seq_len[b];
     const int64_t n = p.g_len ? (int64_t)p.g_len[g] : len;
-    r.base = p.seq_base[b];
-    r.bad = n < 0 || n > len || n > p.max_n || r.base < 0 || r.base + n > p.cap;
+    const int64_t base = p.seq_base[b];
+    r.bad = n < 0 || n > len || n > p.max_n || base < 0 || base + n > p.cap;
     if (r.bad) return r;
+    r.base = (int)base;
     r.n = (int)n;
-    r.row0 = (int64_t)a * p.H;
-    r.rows = (int64_t)(e - a) * p.H;
+    r.row0 = a * p.H;
+    r.rows = (e - a) * p.H;
     return r;
 }
 
-__device__ __forceinline__ int64_t row_tiles(const Group &g) { return g.bad ? 0 : (g.rows + kRowsPair - 1) / kRowsPair; }
-__device__ __forceinline__ int64_t ent_tiles(const Group &g) { return g.bad ? 0 : (g.n + kEnt - 1) / kEnt; }
+__device__ __forceinline__ int row_tiles(const Group &g) { return (g.rows + kRowsPair - 1) / kRowsPair; }
+__device__ __forceinline__ int ent_tiles(const Group &g) { return g.n / kEnt + (g.n % kEnt != 0); }
+__device__ __forceinline__ int64_t units(const Group &g) { return (int64_t)row_tiles(g) * ent_tiles(g); }   // (bad: 0)
 
-// Sum over all groups of their tiles (one warp; count_bad: counts the groups
-// that are out of contract).
-__device__ __forceinline__ int64_t total_units(const DenseParams &p, int lane, bool count_bad)
+// a / b of non-negative numbers (a 32-bit division where it serves)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
-    int64_t sum = 0;
-    for (int g = lane; g < p.ng; g += 32) {
-        const Group gr = group_of(p, g);
-        if (gr.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
-        sum += row_tiles(gr) * ent_tiles(gr);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
 }
 
 // First unit of a pair's run: equal runs, none of them empty (of U units in all,
@@ -113,73 +107,99 @@ __device__ __forceinline__ int64_t total_units(const DenseParams &p, int lane, b
 __device__ __forceinline__ int64_t run_begin(const DenseParams &p, int64_t pair, int64_t U)
 {
     const int64_t P = min((int64_t)p.pairs, U);
-    return pair < P ? pair * U / P : U;
+    return pair < P ? quotient(pair * U, P) : U;
 }
 
-// The group that unit u (< the total) belongs to, and the units before it (one warp).
-__device__ __forceinline__ void find_unit(const DenseParams &p, int64_t u, int lane, int *g_out, int64_t *before_out)
+// One pair's pieces of work in order: entries k0 .. k1 (in tiles) of a row tile.
+// find() sets up the first piece.
+struct Work {
+    Group gr;
+    int g;
+    int rt;              // row tile of the group
+    int kt;              // tiles of entries of the group
+    int k0, k1;
+    int64_t left;        // units left after this piece
+
+    __device__ __forceinline__ bool next(const DenseParams &p)
+    {
+        if (left <= 0) return false;
+        if (++rt == row_tiles(gr)) {
+            do { gr = group_of(p, ++g); } while (units(gr) == 0);
+            kt = ent_tiles(gr);
+            rt = 0;
+        }
+        k0 = 0;
+        k1 = (int)min((int64_t)kt, left);
+        left -= k1;
+        return true;
+    }
+};
+
+// What a pair works on, found by one warp in one pass over the groups (two when
+// there are more than 32).
+struct Found {
+    Work w;
+    int64_t total;       // units of all groups
+    int64_t u0, u1;      // this pair's
+    int empty;           // some group has rows but no entries
+};
+
+__device__ __forceinline__ void find(const DenseParams &p, int pair, int lane, bool count_bad, Found *out)
 {
+    Group gr{};
+    int64_t total = 0;
+    int empty = 0;
+    for (int g0 = 0; g0 < p.ng; g0 += 32) {
+        gr = Group{};
+        if (g0 + lane < p.ng) {
+            gr = group_of(p, g0 + lane);
+            if (gr.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
+            if (!gr.bad && gr.n == 0 && gr.rows > 0) empty = 1;
+        }
+        total += units(gr);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    empty = __any_sync(0xffffffffu, empty);
+    const int64_t u0 = run_begin(p, pair, total), u1 = run_begin(p, pair + 1, total);
+    if (lane == 0) {
+        out->total = total;
+        out->u0 = u0;
+        out->u1 = u1;
+        out->empty = empty;
+    }
+    if (u0 >= u1) return;
     int64_t before = 0;
     for (int g0 = 0; g0 < p.ng; g0 += 32) {
-        int64_t mine = 0;
-        if (g0 + lane < p.ng) {
-            const Group gr = group_of(p, g0 + lane);
-            mine = row_tiles(gr) * ent_tiles(gr);
+        if (p.ng > 32) {
+            gr = Group{};
+            if (g0 + lane < p.ng) gr = group_of(p, g0 + lane);
         }
+        const int64_t mine = units(gr);
         int64_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += v;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, before + upto > u);
+        const uint32_t hit = __ballot_sync(0xffffffffu, before + upto > u0);
         if (hit != 0u) {
-            const int l = __ffs(hit) - 1;
-            *g_out = g0 + l;
-            *before_out = before + __shfl_sync(0xffffffffu, upto - mine, l);
+            if (lane == __ffs(hit) - 1) {
+                const int64_t in_group = u0 - (before + upto - mine);
+                Work &w = out->w;
+                w.gr = gr;
+                w.g = g0 + lane;
+                w.kt = ent_tiles(gr);
+                w.rt = (int)quotient(in_group, w.kt);
+                w.k0 = (int)(in_group - (int64_t)w.rt * w.kt);
+                w.k1 = (int)min((int64_t)w.kt, w.k0 + (u1 - u0));
+                w.left = u1 - u0 - (w.k1 - w.k0);
+            }
             return;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    *g_out = p.ng;
-    *before_out = before;
 }
-
-// One pair's pieces of work in order: entries k0 .. k1 (in tiles) of a row tile.
-struct Work {
-    Group gr;
-    int g;
-    int64_t rt;          // row tile of the group
-    int64_t kt;          // tiles of entries of the group
-    int64_t k0, k1;
-    int64_t left;        // units left after this piece
-
-    __device__ __forceinline__ void start(const DenseParams &p, int g_, int64_t in_group, int64_t units)
-    {
-        left = units;
-        if (units <= 0) return;
-        g = g_;
-        gr = group_of(p, g);
-        kt = ent_tiles(gr);
-        rt = in_group / kt;
-        k0 = in_group - rt * kt;
-        k1 = min(kt, k0 + left);
-        left -= k1 - k0;
-    }
-    __device__ __forceinline__ bool next(const DenseParams &p)
-    {
-        if (left <= 0) return false;
-        if (++rt == row_tiles(gr)) {
-            do { gr = group_of(p, ++g); } while (row_tiles(gr) * ent_tiles(gr) == 0);
-            kt = ent_tiles(gr);
-            rt = 0;
-        }
-        k0 = 0;
-        k1 = min(kt, left);
-        left -= k1;
-        return true;
-    }
-};
 
 // ------------------------------------------------------------------ pairs of CTAs
 __device__ __forceinline__ uint32_t cta_rank()
@@ -326,7 +346,7 @@ __device__ __forceinline__ Joined join_prev(float m, float l, bool any_prev, flo
 // Rows of a group without entries: the caller's partial result, or nothing.
 __device__ __forceinline__ void empty_rows(const DenseParams &p, const Group &gr, int first, int step)
 {
-    for (int64_t i = first; i < gr.rows * (CSA2_D / 4); i += step) {
+    for (int64_t i = first; i < (int64_t)gr.rows * (CSA2_D / 4); i += step) {
         const int64_t row = gr.row0 + i / (CSA2_D / 4);
         const int c = (int)(i % (CSA2_D / 4)) * 4;
         const float pl = p.prev_out ? p.prev_lse[row] : -INFINITY;
@@ -360,10 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     uint64_t *bar_o = bars + 19;               // a tile's O products done
     uint64_t *bar_q = bars + 20;               // (first CTA's) Q stored by both CTAs
     uint64_t *bar_done = bars + 21;            // (first CTA's) every MMA done
-    int64_t *sUnit = reinterpret_cast<int64_t *>(bars + 22); // [0] total [1] units before the group
-    int *sFlag = reinterpret_cast<int *>(bars + 24);         // [0] abort
+    int *sFlag = reinterpret_cast<int *>(bars + 22);         // [0] abort
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(sFlag + 1);
-    int *sGroup = sFlag + 2;
+    Found *sFound = reinterpret_cast<Found *>(bars + 23);
     volatile int *abort_flag = sFlag;
 
     if (tid == 0) {
@@ -375,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         mbar_init(&bar_s[1], 1);
         mbar_init(bar_p, 2 * kWarpsSoft);
         mbar_init(bar_o, 1);
-        mbar_init(bar_q, 2 * kWarpsSoft);
+        mbar_init(bar_q, 2 * kWarpsProd);
         mbar_init(bar_done, 1);
         sFlag[0] = 0;
         fence_barrier_init();
@@ -385,25 +404,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    // (the other CTA's barriers are used only once it has arrived here)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_wait();
     pdl_trigger();
-    if (warp == 1) {
-        const int64_t U = total_units(p, lane, blockIdx.x == 0);
-        int g = 0;
-        int64_t before = 0;
-        const int64_t u0 = run_begin(p, pair, U);
-        if (u0 < U) find_unit(p, u0, lane, &g, &before);
-        if (lane == 0) { sUnit[0] = U; sUnit[1] = before; *sGroup = g; }
-    }
+    if (warp == 1) find(p, pair, lane, blockIdx.x == 0, sFound);
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem = *sTmem;
-    const int64_t U = sUnit[0];
-    const int64_t u0 = run_begin(p, pair, U), u1 = run_begin(p, pair + 1, U);
-    Work w;
-    w.start(p, *sGroup, u0 - sUnit[1], u1 - u0);
+    const int64_t U = sFound->total, u0 = sFound->u0, u1 = sFound->u1;
+    Work w = sFound->w;
     if (tid == 0 && rank == 0) {
         // for the join: the row tile that this pair begins in
         DenseBegin d{};
@@ -412,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             d.first = u0 - w.k0;
             d.last = d.first + w.kt;
             d.row0 = w.gr.row0 + w.rt * kRowsPair;
-            d.rows = (int)min((int64_t)kRowsPair, w.gr.rows - w.rt * kRowsPair);
+            d.rows = min(kRowsPair, w.gr.rows - w.rt * kRowsPair);
         }
         p.begin[pair] = d;
     }
@@ -461,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 fills ^= 1;
             };
             for (; more && ok; more = w.next(p), ++pieces) {
-                const int n_tiles = (int)(w.k1 - w.k0);
+                const int n_tiles = w.k1 - w.k0;
                 wait(bar_q, pieces & 1);
                 if (!ok) break;
                 scores(tile & 1);
@@ -521,11 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             piece[i] = smem_u32(sRing) + atom * kAtom + (16 * pw + e4) * 128u +
                        (uint32_t)(((4 * half + ((i + atom) & 3)) ^ e4) << 4);
         uint32_t fills = 1;                    // parity of the next wait on "empty": the first pass is free
+        const uint32_t q_full = in_cta(smem_u32(bar_q), 0);
+        uint32_t tiles = 0;                    // of the pieces before
         bool ok = true;
         uint4 gc[4 * kStages];
         uint32_t gs[4 * kStages];
         for (; more && ok; more = w.next(p)) {
-            const int n_tiles = (int)(w.k1 - w.k0), n_blocks = 2 * n_tiles;
+            const int n_tiles = w.k1 - w.k0, n_blocks = 2 * n_tiles;
+            const int n_left = w.gr.n - w.k0 * kEnt;                     // entries from the piece's first on
+            const int64_t first = (int64_t)w.gr.base + w.k0 * kEnt;
+            const uint8_t *const codes = p.codes + first * CSA2_CODE_BYTES;
+            const uint8_t *const scales = p.scales + first * CSA2_SCALE_BYTES;
             // The blocks of two stages: S(0) S(1) O(0) S(2) O(1) ... O(last).  Unit u of
             // stage s is, for S, entry 16 pw + 4 u + e4 of this CTA's 128, channels
             // 256 s + ..; for O, that entry of the tile's s-th 128, channels 256 rank + ..
@@ -535,13 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             auto begin = [&](int b) {
                 const bool k = b == 0 || ((b & 1) != 0 && b != n_blocks - 1);
                 const int tile = b == 0 ? 0 : b == n_blocks - 1 ? n_tiles - 1 : (b & 1) ? (b + 1) >> 1 : (b >> 1) - 1;
-                const int64_t e = (w.k0 + tile) * kEnt;
-                const int mine = e4 + 16 * pw + (k ? 128 * (int)rank : 0);
+                const int e = tile * kEnt + e4 + 16 * pw + (k ? 128 * (int)rank : 0);
                 const int ch = 64 * atom + 32 * half + (k ? 0 : 256 * (int)rank);
-                inside = e + kEnt <= w.gr.n;
-                left = (int)(w.gr.n - e) - mine;
-                c0 = p.codes + (w.gr.base + e + mine) * CSA2_CODE_BYTES + (ch >> 1);
-                s0 = p.scales + (w.gr.base + e + mine) * CSA2_SCALE_BYTES + (ch >> 4);
+                inside = (tile + 1) * kEnt <= n_left;
+                left = n_left - e;
+                c0 = codes + (int64_t)e * CSA2_CODE_BYTES + (ch >> 1);
+                s0 = scales + (int64_t)e * CSA2_SCALE_BYTES + (ch >> 4);
                 c_step = k ? 128 : 128 * CSA2_CODE_BYTES;
                 s_step = k ? 16 : 128 * CSA2_SCALE_BYTES;
                 left_s = k ? 0 : 128;
@@ -561,8 +578,39 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 }
             };
             begin(0);
+            load(0);
+            // ---- Q as f16 (rows past the tile's are zero), once the last piece's scores are done
+            if (tiles > 0)
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, abort_flag));
+            if (!ok) break;
+            {
+                const int r0 = w.rt * kRowsPair + kRowsCta * (int)rank;
+                const int n_rows = max(0, min(kRowsCta, w.gr.rows - r0));
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(w.gr.row0 + r0) * CSA2_D);
+                const int t = 32 * pw + lane;
 #pragma unroll
-            for (int s = 0; s < kStages; ++s) load(s);
+                for (int i0 = 0; i0 < 16; i0 += 4) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {          // 16 bytes: number t + 256 i of the 64 rows x 64
+                        const int at = t + 256 * (i0 + i);
+                        v[i] = (at >> 6) < n_rows ? __ldg(src + at) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = t + 256 * (i0 + i);
+                        if (p.q_type == CSA2_BF16)
+                            v[i] = make_uint4(bf16x2_to_f16x2(v[i].x), bf16x2_to_f16x2(v[i].y), bf16x2_to_f16x2(v[i].z),
+                                              bf16x2_to_f16x2(v[i].w));
+                        *reinterpret_cast<uint4 *>(sQ + ((at & 63) >> 3) * kQAtom + sw128(at >> 6, at & 7)) = v[i];
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_at(q_full);
+            }
+            tiles += n_tiles;
+            load(1);
             for (int b = 0; b < n_blocks && ok; ++b) {
                 const bool ahead = b + 1 < n_blocks;
                 if (ahead) begin(b + 1);
@@ -603,39 +651,26 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         const int row = 32 * (quarter & 1) + lane;
         const int ent0 = 128 * (quarter >> 1) + 64 * ch;           // its 64 entries of a tile
         const int which = 2 * (quarter >> 1) + ch;                 // of the row's four threads
-        const uint32_t p_bar = in_cta(smem_u32(bar_p), 0), q_bar = in_cta(smem_u32(bar_q), 0);
+        const uint32_t p_bar = in_cta(smem_u32(bar_p), 0);
         uint8_t *p_row = sP + which * kQAtom;
         const float l2s = p.sm_scale * kLog2e;
         const float worst = l2s >= 0.f ? -INFINITY : INFINITY;     // a score that never is the largest logit
         uint32_t tile = 0;
         bool ok = true;
         for (; more && ok; more = w.next(p)) {
-            const int64_t row0 = w.gr.row0 + w.rt * kRowsPair + kRowsCta * (int)rank;
-            const int n_rows = (int)max((int64_t)0, min((int64_t)kRowsCta, w.gr.rows - w.rt * kRowsPair - kRowsCta * (int)rank));
-            // ---- Q as f16 (rows past the tile's are zero); every earlier MMA has completed
-            for (int i = tid; i < kRowsCta * (CSA2_D / 8); i += kSoft) {
-                const int r = i / (CSA2_D / 8), c8 = i % (CSA2_D / 8);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < n_rows) {
-                    v = __ldg(reinterpret_cast<const uint4 *>(p.q + (row0 + r) * CSA2_D) + c8);
-                    if (p.q_type == CSA2_BF16)
-                        v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z),
-                                       bf16x2_to_f16x2(v.w));
-                }
-                *reinterpret_cast<uint4 *>(sQ + (c8 >> 3) * kQAtom + sw128(r, c8 & 7)) = v;
-            }
+            const int r0 = w.rt * kRowsPair + kRowsCta * (int)rank;
+            const int n_rows = max(0, min(kRowsCta, w.gr.rows - r0));
+            const int64_t row0 = w.gr.row0 + r0;
             if (tid < kRowsCta) sM[tid] = -INFINITY;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive_at(q_bar);
             soft_sync();
             float l = 0.f;
-            const int n_tiles = (int)(w.k1 - w.k0);
+            const int n_tiles = w.k1 - w.k0;
+            const int n_left = w.gr.n - w.k0 * kEnt;              // entries from the piece's first on
             for (int i = 0; i < n_tiles; ++i, ++tile) {
                 const uint32_t tS = tmem + kColS + 128 * (tile & 1) + 64 * ch + lane_q;
                 bool got = mbar_wait<true>(&bar_s[tile & 1], (tile >> 1) & 1, abort_flag);
                 tc_fence_after();
-                const int64_t left = w.gr.n - (w.k0 + i) * kEnt - ent0;     // entries of this thread's 64
+                const int left = n_left - i * kEnt - ent0;        // entries of this thread's 64
                 float m = sM[row];
                 // the largest logit: of the scores if sm_scale >= 0, else of their negatives
                 float hi = -INFINITY;
@@ -749,37 +784,56 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             const int chan = 256 * (quarter >> 1) + 128 * ch;
             const int64_t piece = 2 * (int64_t)pair + (w.k0 == 0 ? 1 : 0);
             Joined j{1.f, 0.f, 0.f};
-            if (whole) {
-                if (row < n_rows) j = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[row0 + row] : 0.f);
-                soft_sync();                   // (all four threads of a row have read prev_lse, which may be lse itself)
-                if (row < n_rows && which == 0 && p.lse) p.lse[row0 + row] = j.lse;
-            } else if (which == 0) {
-                float *ml = p.part_ml + piece * 2 * kRowsPair + kRowsCta * (int)rank + row;
-                ml[0] = m;
-                ml[kRowsPair] = l;
+            if (whole && row < n_rows)
+                j = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[row0 + row] : 0.f);
+            soft_sync();                       // (sRed is read, and prev_lse, which may be lse itself)
+            if (which == 0) {
+                sRed[row] = j.own;
+                sRed[kRowsCta + row] = j.prev;
+                if (whole) {
+                    if (row < n_rows && p.lse) p.lse[row0 + row] = j.lse;
+                } else {
+                    float *ml = p.part_ml + piece * 2 * kRowsPair + kRowsCta * (int)rank + row;
+                    ml[0] = m;
+                    ml[kRowsPair] = l;
+                }
             }
-            const float own = j.own, pw = j.prev;
+            soft_sync();
+            // O goes through the warp's 4 KB of the (now free) P buffer, so that 8 lanes
+            // read and write 32 consecutive channels of a row
+            uint8_t *turn = sP + warp * 4096;
+            const int r_base = 32 * (quarter & 1) + (lane >> 3), c_lane = chan + 4 * (lane & 7);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
+                float4 pv[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = r_base + 4 * i;
+                    pv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (whole && r < n_rows && sRed[kRowsCta + r] != 0.f)
+                        pv[i] = *reinterpret_cast<const float4 *>(p.prev_out + (row0 + r) * CSA2_D + c_lane + 32 * c);
+                }
                 float o[32];
                 tmem_ld32(tmem + 128 * ch + 32 * c + lane_q, o);
                 tmem_wait_ld();
-                if (whole && row < n_rows) {
-                    const int64_t at = (row0 + row) * CSA2_D + chan + 32 * c;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float4 v = make_float4(o[4 * k] * own, o[4 * k + 1] * own, o[4 * k + 2] * own, o[4 * k + 3] * own);
-                        if (pw != 0.f) {
-                            const float4 q4 = *reinterpret_cast<const float4 *>(p.prev_out + at + 4 * k);
-                            v = make_float4(fmaf(q4.x, pw, v.x), fmaf(q4.y, pw, v.y), fmaf(q4.z, pw, v.z), fmaf(q4.w, pw, v.w));
-                        }
-                        store4(p.out, p.out_type, at + 4 * k, v.x, v.y, v.z, v.w);
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<float4 *>(turn + sw128((uint32_t)lane, (uint32_t)k)) =
+                        make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = r_base + 4 * i;
+                    float4 v = *reinterpret_cast<const float4 *>(turn + sw128((uint32_t)(r & 31), (uint32_t)(lane & 7)));
+                    if (r >= n_rows) continue;
+                    if (whole) {
+                        const float own = sRed[r], pw = sRed[kRowsCta + r];
+                        store4(p.out, p.out_type, (row0 + r) * CSA2_D + c_lane + 32 * c, fmaf(pv[i].x, pw, v.x * own),
+                               fmaf(pv[i].y, pw, v.y * own), fmaf(pv[i].z, pw, v.z * own), fmaf(pv[i].w, pw, v.w * own));
+                    } else {
+                        *reinterpret_cast<float4 *>(p.part_o + (piece * kRowsPair + kRowsCta * (int)rank + r) * CSA2_D +
+                                                    c_lane + 32 * c) = v;
                     }
-                } else if (row < n_rows) {
-                    float *dst = p.part_o + (piece * kRowsPair + kRowsCta * (int)rank + row) * CSA2_D + chan + 32 * c;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<float4 *>(dst + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
                 __syncwarp();
             }
@@ -789,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         if (!ok && lane == 0) raise_abort(sFlag);
     }
     // groups without entries
-    if (warp != kWarpsSoft + kWarpsProd)
+    if (sFound->empty && warp != kWarpsSoft + kWarpsProd)
         for (int g = pair; g < p.ng; g += p.pairs) {
             const Group gr = group_of(p, g);
             if (!gr.bad && gr.n == 0)
@@ -937,7 +991,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
 
 cudaError_t launch_dense(const DenseParams &p, cudaStream_t st)
 {
-    constexpr size_t smem = 1024 + kStages * kStage + kQBytes + kPBytes + 6 * kRowsCta * 4 + 26 * 8;
+    constexpr size_t smem = 1024 + kStages * kStage + kQBytes + kPBytes + 6 * kRowsCta * 4 + 23 * 8 + sizeof(Found);
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     cudaError_t e = cudaFuncSetAttribute(dense_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
