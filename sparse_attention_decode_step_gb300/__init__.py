@@ -8,6 +8,7 @@ device memory and the current CUDA stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -175,17 +176,22 @@ class Cache:
         codes [cap][256], scales [cap][32], kidx [cap][d_idx] uint8, kscale [cap]
         fp32, seq_base [batch + 1] int64, seq_len [batch] int32, cap a multiple of 8.
         kidx and kscale may be None for a cache that is only attended."""
-        for t, dt in ((codes, torch.uint8), (scales, torch.uint8), (kidx, torch.uint8),
-                      (kscale, torch.float32), (seq_base, torch.int64), (seq_len, torch.int32)):
-            if t is not None and (t.dtype != dt or not t.is_contiguous()):
-                raise CsaError(f"cache tensor must be contiguous {dt}, got {t.dtype}")
         cap = codes.shape[0]
-        d_idx = kidx.shape[1] if kidx is not None else 128
-        if (tuple(codes.shape) != (cap, 256) or tuple(scales.shape) != (cap, 32)
-                or (kidx is None) != (kscale is None) or (kidx is not None and kidx.shape[0] != cap)
-                or (kscale is not None and kscale.numel() != cap)
+        u8 = torch.uint8
+        keys = kidx is not None
+        if (codes.dtype != u8 or scales.dtype != u8 or (keys and kidx.dtype != u8)
+                or (kscale is not None and kscale.dtype != torch.float32)
+                or seq_base.dtype != torch.int64 or seq_len.dtype != torch.int32):
+            raise CsaError("cache tensors: codes, scales, kidx uint8, kscale fp32, seq_base int64, seq_len int32")
+        if not (codes.is_contiguous() and scales.is_contiguous() and seq_base.is_contiguous()
+                and seq_len.is_contiguous() and (not keys or kidx.is_contiguous())
+                and (kscale is None or kscale.is_contiguous())):
+            raise CsaError("cache tensors must be contiguous")
+        if (codes.shape != (cap, 256) or scales.shape != (cap, 32) or keys != (kscale is not None)
+                or (keys and (kidx.dim() != 2 or kidx.shape[0] != cap or kscale.numel() != cap))
                 or seq_base.numel() != seq_len.numel() + 1):
             raise CsaError("cache tensors do not fit together")
+        d_idx = kidx.shape[1] if keys else 128
         c = cls.__new__(cls)
         c.batch, c.cap, c.d_idx, c.m = seq_len.numel(), cap, d_idx, m
         c.codes, c.scales, c.kidx, c.kscale = codes, scales, kidx, kscale
@@ -339,56 +345,82 @@ def sparse_attn(cache: Cache, qs: Queries, idx, cnt, q, win, n_win, out, lse=Non
                                   _ptr(counters), _stream()), "csa2_sparse_attn")
 
 
-def _on_current_device(*tensors):
-    """A call runs on the current device's stream, so its tensors live there."""
-    dev = torch.cuda.current_device()
+# The calls below are short on the GPU, so their marshalling is kept short too:
+# functions are looked up once, pointers go as integers, the stream as its handle.
+_fn = {}
+
+
+def _call(name, *args):
+    f = _fn.get(name)
+    if f is None:
+        f = _fn[name] = getattr(lib(), name)
+    status = f(*args)
+    if status != 0:
+        _check(status, name)
+
+
+def _device(*tensors) -> int:
+    """The current device, which all tensors must be on: a call runs on its stream."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != dev:
-            raise CsaError(f"tensor is on cuda:{t.get_device()}, the current device is cuda:{dev}")
-
-
-def _rows(t, width, what):
-    """Pointer and row stride of a [n][width] tensor whose rows are contiguous."""
-    if t is None:
-        return None, 0
-    if not t.is_cuda:
+        if t is not None and t.get_device() != dev:
+            raise CsaError(f"tensors on {t.device} and {tensors[0].device}")
+    if dev < 0:
         raise CsaError("tensor is not on a CUDA device")
-    if t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
-        raise CsaError(f"{what} must be [n][{width}] with contiguous rows, got {tuple(t.shape)}")
-    # (a single row's stride is arbitrary)
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else -(-width // 8) * 8
+    if dev != torch.cuda.current_device():
+        raise CsaError(f"tensors on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _at(t):
+    """Address of a contiguous tensor (None: 0)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise CsaError("tensor is not contiguous")
+    return t.data_ptr()
 
 
 def _row_args(cache, rows, x, key, key_type, what):
+    """Checked arguments of a row call: n, and address and row stride of x and key."""
     if rows.dtype != torch.int64 or rows.dim() != 1:
         raise CsaError(f"rows must be int64 [n], got {rows.dtype} {tuple(rows.shape)}")
     n = rows.shape[0]
     if x.dtype not in _DTYPES or (key is not None and key.dtype != key_type):
         raise CsaError(f"{what}: element type {x.dtype}, key {None if key is None else key.dtype}")
-    if x.shape[0] != n or (key is not None and key.shape[0] != n):
-        raise CsaError(f"{what}: rows, x and key differ in length")
-    xp, kp = _rows(x, D, "x"), _rows(key, cache.d_idx, "key")
-    _on_current_device(cache.codes, rows, x, key)
-    return n, xp, kp
+    if x.shape != (n, D) or x.stride(1) != 1:
+        raise CsaError(f"{what}: x must be [{n}][{D}] with contiguous rows, got {tuple(x.shape)}")
+    # (the stride of a single row says nothing)
+    ld_x = x.stride(0) if n > 1 else D
+    if key is None:
+        return n, x.data_ptr(), ld_x, None, 0
+    if key.shape != (n, cache.d_idx) or key.stride(1) != 1:
+        raise CsaError(f"{what}: key must be [{n}][{cache.d_idx}] with contiguous rows, got {tuple(key.shape)}")
+    return n, x.data_ptr(), ld_x, key.data_ptr(), key.stride(0) if n > 1 else cache.d_idx
 
 
 def cache_write(cache: Cache, rows, x, key=None, counters=None):
     """Quantises x [n][512] (fp32, bf16 or f16, any row stride) into the cache rows
     rows [n] (int64, distinct; negative: skipped), and key [n][d_idx] (x's type)
     into their indexer keys if it is given."""
-    n, (xp, ld_x), (kp, ld_k) = _row_args(cache, rows, x, key, x.dtype, "cache_write")
-    cs = cache.struct()
-    _check(lib().csa2_cache_write(ctypes.byref(cs), _ptr(rows), n, xp, _DTYPES[x.dtype], ld_x, kp,
-                                  ld_k, _ptr(counters), _stream()), "csa2_cache_write")
+    n, xp, ld_x, kp, ld_k = _row_args(cache, rows, x, key, x.dtype, "cache_write")
+    dev = _device(cache.codes, rows, x, key, counters)
+    _call("csa2_cache_write", ctypes.byref(cache.struct()), _at(rows), n, xp, _DTYPES[x.dtype], ld_x,
+          kp, ld_k, _at(counters), torch._C._cuda_getCurrentRawStream(dev))
 
 
 def cache_read(cache: Cache, rows, x, key=None, counters=None):
     """Reads the cache rows rows [n] (int64; negative: skipped) into x [n][512] (fp32,
     bf16 or f16: exact) and, if given, their indexer keys into key [n][d_idx] fp32."""
-    n, (xp, ld_x), (kp, ld_k) = _row_args(cache, rows, x, key, torch.float32, "cache_read")
-    cs = cache.struct()
-    _check(lib().csa2_cache_read(ctypes.byref(cs), _ptr(rows), n, xp, _DTYPES[x.dtype], ld_x, kp,
-                                 ld_k, _ptr(counters), _stream()), "csa2_cache_read")
+    n, xp, ld_x, kp, ld_k = _row_args(cache, rows, x, key, torch.float32, "cache_read")
+    dev = _device(cache.codes, rows, x, key, counters)
+    _call("csa2_cache_read", ctypes.byref(cache.struct()), _at(rows), n, xp, _DTYPES[x.dtype], ld_x,
+          kp, ld_k, _at(counters), torch._C._cuda_getCurrentRawStream(dev))
+
+
+@functools.lru_cache(maxsize=4096)
+def _dense_need(dev, ng, nq, H, max_n) -> int:
+    return dense_workspace_size(ng, nq, H, max_n)
 
 
 def dense_workspace_size(ng, nq, H, max_n) -> int:
@@ -401,26 +433,23 @@ def dense_attn(cache: Cache, groups: Groups, q, out, lse=None, *, prev=None, sm_
     entries of the group's sequence, into out [nq][H][512] (fp32, bf16 or f16) and
     lse [nq][H]; prev = (out, lse) of an earlier partial result (fp32) is merged in.
     max_n bounds the entries of any group (default: the cache's rows)."""
-    nq, H = int(q.shape[0]), int(q.shape[1])
-    po, pl = prev if prev is not None else (None, None)
-    if q.dtype not in (torch.bfloat16, torch.float16) or out.dtype not in _DTYPES:
-        raise CsaError(f"dense_attn: q {q.dtype}, out {out.dtype}")
     if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
         raise CsaError(f"dense_attn: q {tuple(q.shape)}, out {tuple(out.shape)}")
-    for t, shape in ((po, q.shape), (pl, q.shape[:2]), (lse, q.shape[:2])):
-        if t is not None and (t.dtype != torch.float32 or t.shape != shape):
-            raise CsaError(f"dense_attn: lse and prev must be fp32 {tuple(shape)}")
-    qp = _ptr(q)
-    _on_current_device(cache.codes, groups.seq, q, po, pl, out, lse, ws)
+    if q.dtype not in (torch.bfloat16, torch.float16) or out.dtype not in _DTYPES:
+        raise CsaError(f"dense_attn: q {q.dtype}, out {out.dtype}")
+    nq, H, _ = q.shape
+    po, pl = prev if prev is not None else (None, None)
+    if ((lse is not None and (lse.dtype != torch.float32 or lse.shape != (nq, H)))
+            or (po is not None and (po.dtype != torch.float32 or po.shape != q.shape))
+            or (pl is not None and (pl.dtype != torch.float32 or pl.shape != (nq, H)))):
+        raise CsaError(f"dense_attn: lse and prev must be fp32 [{nq}][{H}] and [{nq}][{H}][{D}]")
+    dev = _device(cache.codes, groups.seq, groups.off, groups.length, q, po, pl, out, lse, ws, counters)
     max_n = cache.cap if max_n is None else int(max_n)
     if ws is None:
-        ws = workspace(dense_workspace_size(groups.ng, nq, H, max_n), q.device)
-    cs, gs = cache.struct(), groups.struct(nq)
-    _check(lib().csa2_dense_attn(ctypes.byref(cs), ctypes.byref(gs), max_n, qp,
-                                 _DTYPES[q.dtype], H, float(sm_scale), _ptr(po), _ptr(pl),
-                                 _ptr(out), _DTYPES[out.dtype], _ptr(lse), _ptr(ws), ws.numel(),
-                                 _ptr(counters), _stream()),
-           "csa2_dense_attn")
+        ws = torch.empty(max(_dense_need(dev, groups.ng, nq, H, max_n), 256), dtype=torch.uint8, device=q.device)
+    _call("csa2_dense_attn", ctypes.byref(cache.struct()), ctypes.byref(groups.struct(nq)), max_n,
+          _at(q), _DTYPES[q.dtype], H, sm_scale, _at(po), _at(pl), _at(out), _DTYPES[out.dtype],
+          _at(lse), _at(ws), ws.numel(), _at(counters), torch._C._cuda_getCurrentRawStream(dev))
 
 
 class Layer:

@@ -649,14 +649,13 @@ csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, 
     p.prev_out = prev_out;
     p.prev_lse = prev_lse;
     p.out = out;
-    p.out_type = out_type;
     p.lse = lse;
     p.pairs = pl.pairs;
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + pl.off_ml);
     p.begin = reinterpret_cast<DenseBegin *>(static_cast<uint8_t *>(workspace) + pl.off_begin);
     p.counters = counters;
-    return cuda_status(launch_dense(p, static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_dense(p, out_type, static_cast<cudaStream_t>(stream)));
 }
 
 const char *csa2_status_string(csa2_status s)

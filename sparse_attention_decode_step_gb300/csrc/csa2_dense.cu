@@ -36,6 +36,8 @@
 // pieces in a fixed order, so results do not depend on timing.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "csa2_attn_device.cuh"
 #include "csa2_internal.h"
 
@@ -279,6 +281,12 @@ __device__ __forceinline__ bool soft_any(bool v)
     return r != 0;
 }
 
+// 16 bytes global -> shared, zeros when !in
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -309,11 +317,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
 }
 
 // ------------------------------------------------------------------ results
-__device__ __forceinline__ void store4(void *out, int type, int64_t at, float a, float b, float c, float d)
+template <int kOut>
+__device__ __forceinline__ void store4(void *out, int64_t at, float a, float b, float c, float d)
 {
-    if (type == CSA2_F32) {
+    if constexpr (kOut == CSA2_F32) {
         *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = make_float4(a, b, c, d);
-    } else if (type == CSA2_BF16) {
+    } else if constexpr (kOut == CSA2_BF16) {
         uint32_t lo, hi;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(b), "f"(a));
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(d), "f"(c));
@@ -344,6 +353,7 @@ __device__ __forceinline__ Joined join_prev(float m, float l, bool any_prev, flo
 }
 
 // Rows of a group without entries: the caller's partial result, or nothing.
+template <int kOut>
 __device__ __forceinline__ void empty_rows(const DenseParams &p, const Group &gr, int first, int step)
 {
     for (int64_t i = first; i < (int64_t)gr.rows * (CSA2_D / 4); i += step) {
@@ -352,11 +362,12 @@ __device__ __forceinline__ void empty_rows(const DenseParams &p, const Group &gr
         const float pl = p.prev_out ? p.prev_lse[row] : -INFINITY;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (pl > -INFINITY || pl != pl) v = *reinterpret_cast<const float4 *>(p.prev_out + row * CSA2_D + c);
-        store4(p.out, p.out_type, row * CSA2_D + c, v.x, v.y, v.z, v.w);
+        store4<kOut>(p.out, row * CSA2_D + c, v.x, v.y, v.z, v.w);
         if (c == 0 && p.lse) p.lse[row] = pl;
     }
 }
 
+template <int kOut>
 __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 {
     const int tid = threadIdx.x, lane = tid & 31;
@@ -586,23 +597,26 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             {
                 const int r0 = w.rt * kRowsPair + kRowsCta * (int)rank;
                 const int n_rows = max(0, min(kRowsCta, w.gr.rows - r0));
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t)(w.gr.row0 + r0) * CSA2_D);
-                const int t = 32 * pw + lane;
+                // 16 bytes: number t + 256 i of the 64 rows x 64, all 16 on their way at once,
+                // then converted where they lie
+                const int t = 32 * pw + lane, c8 = t & 63;
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(p.q + (int64_t)(w.gr.row0 + r0) * CSA2_D);
+                const uint32_t dst = smem_u32(sQ) + (c8 >> 3) * kQAtom;
 #pragma unroll
-                for (int i0 = 0; i0 < 16; i0 += 4) {
-                    uint4 v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {          // 16 bytes: number t + 256 i of the 64 rows x 64
-                        const int at = t + 256 * (i0 + i);
-                        v[i] = (at >> 6) < n_rows ? __ldg(src + at) : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int at = t + 256 * (i0 + i);
-                        if (p.q_type == CSA2_BF16)
-                            v[i] = make_uint4(bf16x2_to_f16x2(v[i].x), bf16x2_to_f16x2(v[i].y), bf16x2_to_f16x2(v[i].z),
-                                              bf16x2_to_f16x2(v[i].w));
-                        *reinterpret_cast<uint4 *>(sQ + ((at & 63) >> 3) * kQAtom + sw128(at >> 6, at & 7)) = v[i];
+                for (int i = 0; i < 16; ++i) {
+                    const int r = (t >> 6) + 4 * i;
+                    const bool in = r < n_rows;
+                    cp_async16(dst + sw128(r, c8 & 7), in ? src + r * 1024 + c8 * 16 : src, in);
+                }
+                load(1);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                if (p.q_type == CSA2_BF16) {
+#pragma unroll 4
+                    for (int i = 0; i < 16; ++i) {
+                        uint4 *const at = reinterpret_cast<uint4 *>(sQ + (c8 >> 3) * kQAtom + sw128((t >> 6) + 4 * i, c8 & 7));
+                        const uint4 v = *at;
+                        *at = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z),
+                                         bf16x2_to_f16x2(v.w));
                     }
                 }
                 fence_async_smem();
@@ -610,7 +624,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 if (lane == 0) arrive_at(q_full);
             }
             tiles += n_tiles;
-            load(1);
             for (int b = 0; b < n_blocks && ok; ++b) {
                 const bool ahead = b + 1 < n_blocks;
                 if (ahead) begin(b + 1);
@@ -803,16 +816,17 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             // read and write 32 consecutive channels of a row
             uint8_t *turn = sP + warp * 4096;
             const int r_base = 32 * (quarter & 1) + (lane >> 3), c_lane = chan + 4 * (lane & 7);
+            const int mine = (n_rows - r_base + 3) / 4;       // of this lane's 8 rows r_base + 4 i
+            float own[8], pw[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                own[i] = sRed[r_base + 4 * i];
+                pw[i] = i < mine ? sRed[kRowsCta + r_base + 4 * i] : 0.f;
+            }
+            const int64_t out0 = (row0 + r_base) * CSA2_D + c_lane;
+            float *const part0 = p.part_o + (piece * kRowsPair + kRowsCta * (int)rank + r_base) * CSA2_D + c_lane;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-                float4 pv[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = r_base + 4 * i;
-                    pv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (whole && r < n_rows && sRed[kRowsCta + r] != 0.f)
-                        pv[i] = *reinterpret_cast<const float4 *>(p.prev_out + (row0 + r) * CSA2_D + c_lane + 32 * c);
-                }
                 float o[32];
                 tmem_ld32(tmem + 128 * ch + 32 * c + lane_q, o);
                 tmem_wait_ld();
@@ -821,21 +835,29 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                     *reinterpret_cast<float4 *>(turn + sw128((uint32_t)lane, (uint32_t)k)) =
                         make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 __syncwarp();
+                float4 v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = r_base + 4 * i;
-                    float4 v = *reinterpret_cast<const float4 *>(turn + sw128((uint32_t)(r & 31), (uint32_t)(lane & 7)));
-                    if (r >= n_rows) continue;
-                    if (whole) {
-                        const float own = sRed[r], pw = sRed[kRowsCta + r];
-                        store4(p.out, p.out_type, (row0 + r) * CSA2_D + c_lane + 32 * c, fmaf(pv[i].x, pw, v.x * own),
-                               fmaf(pv[i].y, pw, v.y * own), fmaf(pv[i].z, pw, v.z * own), fmaf(pv[i].w, pw, v.w * own));
-                    } else {
-                        *reinterpret_cast<float4 *>(p.part_o + (piece * kRowsPair + kRowsCta * (int)rank + r) * CSA2_D +
-                                                    c_lane + 32 * c) = v;
-                    }
-                }
+                for (int i = 0; i < 8; ++i)
+                    v[i] = *reinterpret_cast<const float4 *>(
+                        turn + sw128((uint32_t)((lane >> 3) + 4 * i), (uint32_t)(lane & 7)));
                 __syncwarp();
+                if (whole) {
+                    float4 pv[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        pv[i] = pw[i] != 0.f ? *reinterpret_cast<const float4 *>(p.prev_out + out0 + 4 * i * CSA2_D + 32 * c)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < mine)
+                            store4<kOut>(p.out, out0 + 4 * i * CSA2_D + 32 * c, fmaf(pv[i].x, pw[i], v[i].x * own[i]),
+                                         fmaf(pv[i].y, pw[i], v[i].y * own[i]), fmaf(pv[i].z, pw[i], v[i].z * own[i]),
+                                         fmaf(pv[i].w, pw[i], v[i].w * own[i]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < mine) *reinterpret_cast<float4 *>(part0 + 4 * i * CSA2_D + 32 * c) = v[i];
+                }
             }
             tc_fence_before();
             soft_sync();                       // sRed, sM and O are read
@@ -847,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         for (int g = pair; g < p.ng; g += p.pairs) {
             const Group gr = group_of(p, g);
             if (!gr.bad && gr.n == 0)
-                empty_rows(p, gr, (int)rank * 32 * (kWarpsSoft + kWarpsProd) + tid, 2 * 32 * (kWarpsSoft + kWarpsProd));
+                empty_rows<kOut>(p, gr, (int)rank * 32 * (kWarpsSoft + kWarpsProd) + tid, 2 * 32 * (kWarpsSoft + kWarpsProd));
         }
     tc_fence_before();
     __syncthreads();
@@ -867,6 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 // row; the pieces of a tile are dealt to `parts` threads each (1, 2 or 4), whose
 // sums are added in order.  A block's item is 4 / parts whole rows, so that lse
 // may be prev_lse itself.
+template <int kOut>
 __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
 {
     __shared__ int sPair[kDensePairsMax], sItem[kDensePairsMax], sWarp[kJoinThreads / 32];
@@ -980,7 +1003,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
             const Joined j = sJ[r - r0];
             float4 pv = make_float4(0.f, 0.f, 0.f, 0.f);
             if (j.prev != 0.f) pv = *reinterpret_cast<const float4 *>(p.prev_out + row * CSA2_D + ch);
-            store4(p.out, p.out_type, row * CSA2_D + ch, fmaf(pv.x, j.prev, o.x * j.own), fmaf(pv.y, j.prev, o.y * j.own),
+            store4<kOut>(p.out, row * CSA2_D + ch, fmaf(pv.x, j.prev, o.x * j.own), fmaf(pv.y, j.prev, o.y * j.own),
                    fmaf(pv.z, j.prev, o.z * j.own), fmaf(pv.w, j.prev, o.w * j.own));
         }
         if (p.lse && tid < 4 / parts && r0 + tid < d.rows) p.lse[d.row0 + r0 + tid] = sJ[tid].lse;
@@ -989,16 +1012,33 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
 
 }  // namespace
 
-cudaError_t launch_dense(const DenseParams &p, cudaStream_t st)
+template <int kOut>
+static cudaError_t launch_dense_as(const DenseParams &p, cudaStream_t st)
 {
     constexpr size_t smem = 1024 + kStages * kStage + kQBytes + kPBytes + 6 * kRowsCta * 4 + 23 * 8 + sizeof(Found);
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    cudaError_t e = cudaFuncSetAttribute(dense_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the shared-memory attribute is set once per device (a bit each; setting it twice does no harm)
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = launch_k(dense_attn_kernel, dim3(2 * p.pairs), dim3(kThreads), smem, st, 2, p);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if ((done.load(std::memory_order_acquire) & bit) == 0) {
+        e = cudaFuncSetAttribute(dense_attn_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_release);
+    }
+    e = launch_k(dense_attn_kernel<kOut>, dim3(2 * p.pairs), dim3(kThreads), smem, st, 2, p);
     if (e == cudaSuccess && p.pairs > 1)
-        e = launch_k(dense_join_kernel, dim3(8 * p.pairs), dim3(kJoinThreads), 0, st, 0, p);
+        e = launch_k(dense_join_kernel<kOut>, dim3(8 * p.pairs), dim3(kJoinThreads), 0, st, 0, p);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_dense(const DenseParams &p, int out_type, cudaStream_t st)
+{
+    return out_type == CSA2_F32    ? launch_dense_as<CSA2_F32>(p, st)
+           : out_type == CSA2_BF16 ? launch_dense_as<CSA2_BF16>(p, st)
+                                   : launch_dense_as<CSA2_F16>(p, st);
 }
 
 }  // namespace csa2

@@ -141,7 +141,6 @@ struct DenseParams {
     float sm_scale;
     const float *prev_out, *prev_lse;
     void *out;
-    int out_type;
     float *lse;
     int pairs;          // pairs of CTAs
     float *part_o;      // [pairs][2][128][512] unnormalised sums of the pieces of row tiles
@@ -151,6 +150,6 @@ struct DenseParams {
 };
 struct DensePlan { int pairs; size_t off_ml, off_begin, total; };
 DensePlan dense_plan(int ng, int nq, int H, int64_t max_n);
-cudaError_t launch_dense(const DenseParams &p, cudaStream_t st);
+cudaError_t launch_dense(const DenseParams &p, int out_type, cudaStream_t st);
 
 }  // namespace csa2
