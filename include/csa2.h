@@ -322,7 +322,7 @@ csa2_status csa2_layer_step(const csa2_layer_args *args, void *stream);
  * csa2_cache_read: x[i] = the 512 values of row rows[i] (E2M1 code x E4M3
  * scale: exact in every type) and, if key is not NULL, key[i] = the indexer
  * key's values in fp32 (exact).  A row may appear any number of times.
- * Both: a negative row number is padding (nothing is read or written for it: x[i]
+ * Both: a negative row number is padding (nothing is written for it: x[i]
  * and key[i] of a read stay as they were); a row number >= cap is skipped the same way and
  * counted in CSA2_CNT_BAD_INPUT.  n == 0 is a no-op.  x, key: 16-byte aligned,
  * ld_x >= 512, ld_key >= d_idx, both a multiple of 16 bytes; rows: 8-byte

@@ -9,7 +9,10 @@
 // bf16 and f16 alike; key = E4M3 byte x scale in fp32.
 //
 // Both are bound by memory traffic: a row is 1 KB of bf16 against 288 B of
-// cache.  One warp per row.
+// cache.  One warp per row, lane l taking channels 8 l .. 8 l + 7 and 256 + 8 l ..,
+// so that every access of a warp is contiguous.  With seven comparisons per
+// value (the append's form) the write of bf16 rows was bound by its
+// instructions, at 50 us for 65,536 rows; see fp4_codes16.
 #include <cuda_fp16.h>
 
 #include "csa2_attn_device.cuh"
@@ -17,41 +20,84 @@
 
 namespace csa2 {
 
-// 16 consecutive elements of a row as fp32 (src 16-byte aligned)
-template <typename T>
-__device__ __forceinline__ void load16(const T *src, float (&x)[16])
+// N consecutive elements (a multiple of 16 bytes, 16-byte aligned; or 2 .. 4
+// elements aligned to their size together) as fp32
+template <int N, typename T>
+__device__ __forceinline__ void load_as_f32(const T *src, float (&x)[N])
 {
-    if constexpr (sizeof(T) == 4) {
+    constexpr int kBytes = N * (int)sizeof(T);
+    constexpr int kWords = kBytes / 4;
+    static_assert(kBytes % 16 == 0 || kBytes == 8 || kBytes == 4, "whole words");
+    uint32_t w[kWords];
+    if constexpr (kBytes >= 16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(src) + i);
-            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBytes / 16; ++i) {
             const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (kBytes == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+        w[0] = v.x; w[1] = v.y;
+    } else {
+        w[0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+    }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float2 f;
-                if constexpr (sizeof(T) == 2 && __is_same(T, __half))
-                    f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-                else
-                    f = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
-                x[8 * i + 2 * j] = f.x;
-                x[8 * i + 2 * j + 1] = f.y;
-            }
+    for (int i = 0; i < kWords; ++i) {
+        if constexpr (__is_same(T, float)) {
+            x[i] = __uint_as_float(w[i]);
+        } else if constexpr (__is_same(T, __half)) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            x[2 * i] = f.x; x[2 * i + 1] = f.y;
+        } else {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     }
 }
 
-template <typename T>
-__device__ __forceinline__ float as_float(T v)
+// fp4_scale_byte by the hardware's E4M3 rounding: the nearest E4M3 to amax / 6,
+// or the next one up when that is too small (6 s is exact).
+__device__ __forceinline__ uint32_t fp4_scale_near(float amax, float *s)
 {
-    if constexpr (__is_same(T, float)) return v;
-    else if constexpr (__is_same(T, __half)) return __half2float(v);
-    else return __bfloat162float(v);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(amax * (1.0f / 6.0f)));
+    uint32_t b = r & 0xFFu;
+    auto value = [](uint32_t byte) {
+        const uint32_t h = e4m3x2_to_f16x2(byte);
+        return __half2float(*reinterpret_cast<const __half *>(&h));
+    };
+    if (6.0f * value(b) < amax && b < 0x7Eu) ++b;
+    *s = value(b);
+    return b;
+}
+
+// E2M1 codes of 8 values that came from 16-bit floats, under scale s (r = 1 / s).
+// x r is within 2^-22 (relative) of x / s.  A 16-bit x has at most 11 significant
+// bits and a midpoint m s (m of .25, .75, 1.25, 1.75, 2.5, 3.5, 5) at most 7, so
+// x / s is either exactly m or at least 2^-11 away from it: rounding x r to 17
+// bits gives exactly m in the first case and stays on its side in the second,
+// and the hardware's round-to-nearest-even then decides as the exact quotient
+// would.  (fp32 values may lie within 2^-24 of a midpoint: they are compared.)
+__device__ __forceinline__ uint32_t fp4_codes16(const float (&x)[8], float r)
+{
+    uint32_t w = 0;
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        q[i] = __uint_as_float((__float_as_uint(x[i] * r) + 0x40u) & ~0x7Fu);
+    asm("{\n"
+        ".reg .b8 b0, b1, b2, b3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        "mov.b32 %0, {b0, b1, b2, b3};\n"
+        "}\n"
+        : "=r"(w)
+        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+    // a negative value that rounds to zero has code 0
+    const uint32_t mag = w & 0x77777777u;
+    return mag | (w & (((mag + 0x77777777u) & 0x88888888u)));
 }
 
 template <typename T>
@@ -66,42 +112,53 @@ __global__ void __launch_bounds__(256) cache_write_kernel(csa2_cache cache, cons
     const int lane = threadIdx.x & 31;
     if (i >= n) return;
     const int64_t row = rows[i];
+    float v[2][8];
+    load_as_f32<8>(x + i * ld_x + 8 * lane, v[0]);
+    load_as_f32<8>(x + i * ld_x + 256 + 8 * lane, v[1]);
+    float k[4] = {0.f, 0.f, 0.f, 0.f};
+    if (key != nullptr) {
+        if (cache.d_idx == 128) {
+            load_as_f32<4>(key + i * ld_key + 4 * lane, k);
+        } else {
+            float k2[2];
+            load_as_f32<2>(key + i * ld_key + 2 * lane, k2);
+            k[0] = k2[0]; k[1] = k2[1];
+        }
+    }
     if (row < 0) return;                          // padding
     if (row >= cache.cap) {
         if (lane == 0) count_event(counters, CSA2_CNT_BAD_INPUT);
         return;
     }
-    float v[16];
-    load16(x + i * ld_x + 16 * lane, v);
-    float amax = 0.f;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) amax = fmaxf(amax, fabsf(v[c]));
-    uint32_t sb = 0, packed[2] = {0u, 0u};
-    if (amax > 0.f) {
-        bool sat = false;
-        sb = fp4_scale_byte(amax, &sat);
-        if (sat) count_event(counters, CSA2_CNT_FP4_SATURATED);
-        const float s = e4m3_pos_value(sb);
+    for (int h = 0; h < 2; ++h) {
+        float amax = 0.f;                         // of the 16-channel group of lanes 2 j, 2 j + 1
 #pragma unroll
-        for (int c = 0; c < 16; ++c) packed[c >> 3] |= fp4_code(v[c], s) << (4 * (c & 7));
+        for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(v[h][c]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        uint32_t sb = 0, codes = 0;
+        if (amax > 0.f) {
+            if (amax > 2688.f && (lane & 1) == 0) count_event(counters, CSA2_CNT_FP4_SATURATED);
+            float s;
+            sb = fp4_scale_near(amax, &s);
+            if constexpr (sizeof(T) == 2) {
+                codes = fp4_codes16(v[h], 1.0f / s);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) codes |= fp4_code(v[h][c], s) << (4 * c);
+            }
+        }
+        *reinterpret_cast<uint32_t *>(cache.codes + row * CSA2_CODE_BYTES + 128 * h + 4 * lane) = codes;
+        if ((lane & 1) == 0) cache.scales[row * CSA2_SCALE_BYTES + 16 * h + (lane >> 1)] = (uint8_t)sb;
     }
-    *reinterpret_cast<uint2 *>(cache.codes + row * CSA2_CODE_BYTES + lane * 8) =
-        make_uint2(packed[0], packed[1]);
-    cache.scales[row * CSA2_SCALE_BYTES + lane] = (uint8_t)sb;
     if (key == nullptr) return;
-    const T *kr = key + i * ld_key;
-    const int per = cache.d_idx / 32;             // 2 or 4 components per lane
-    float k[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        if (c < per) k[c] = as_float(kr[per * lane + c]);
     float a = fmaxf(fmaxf(fabsf(k[0]), fabsf(k[1])), fmaxf(fabsf(k[2]), fabsf(k[3])));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float s = fp8_pow2_scale(a);
-    const uint32_t w = e4m3_byte(k[0] / s) | (e4m3_byte(k[1] / s) << 8) | (e4m3_byte(k[2] / s) << 16) |
-                       (e4m3_byte(k[3] / s) << 24);
-    if (per == 4)
+    const float s = fp8_pow2_scale(a), r = 1.0f / s;   // (a power of two: k r is k / s)
+    const uint32_t w = e4m3_byte(k[0] * r) | (e4m3_byte(k[1] * r) << 8) | (e4m3_byte(k[2] * r) << 16) |
+                       (e4m3_byte(k[3] * r) << 24);
+    if (cache.d_idx == 128)
         *reinterpret_cast<uint32_t *>(cache.kidx + row * 128 + lane * 4) = w;
     else
         *reinterpret_cast<uint16_t *>(cache.kidx + row * 64 + lane * 2) = (uint16_t)w;
@@ -132,8 +189,6 @@ __device__ __forceinline__ void store8(T *dst, uint4 h)
     }
 }
 
-// Lane l takes channels 8 l .. 8 l + 7 and 256 + 8 l ..: a warp reads 128
-// contiguous code bytes and writes 32 contiguous 16-byte words at a time.
 template <typename T>
 __global__ void __launch_bounds__(256) cache_read_kernel(csa2_cache cache, const int64_t *__restrict__ rows,
                                                          int64_t n, T *__restrict__ x, int64_t ld_x,
