@@ -9,10 +9,11 @@
 // bf16 and f16 alike; key = E4M3 byte x scale in fp32.
 //
 // Both are bound by memory traffic: a row is 1 KB of bf16 against 288 B of
-// cache.  One warp per row, lane l taking channels 8 l .. 8 l + 7 and 256 + 8 l ..,
-// so that every access of a warp is contiguous.  With seven comparisons per
-// value (the append's form) the write of bf16 rows was bound by its
-// instructions, at 50 us for 65,536 rows; see fp4_codes16.
+// cache.  One warp per row.  A write's lane takes one 16-channel group, so that a
+// scale is found once; a read's lane takes channels 8 l .. 8 l + 7 and 256 + 8 l ..,
+// so that its stores are contiguous.  With seven comparisons per value (the
+// append's form) the write of bf16 rows was bound by its instructions, at 50 us
+// for 65,536 rows; see fp4_codes16.
 #include <cuda_fp16.h>
 
 #include "csa2_attn_device.cuh"
@@ -55,49 +56,62 @@ __device__ __forceinline__ void load_as_f32(const T *src, float (&x)[N])
     }
 }
 
+// two values to E4M3 bytes (the first in the low byte), nearest even, saturating
+__device__ __forceinline__ uint32_t e4m3x2_near(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // fp4_scale_byte by the hardware's E4M3 rounding: the nearest E4M3 to amax / 6,
 // or the next one up when that is too small (6 s is exact).
 __device__ __forceinline__ uint32_t fp4_scale_near(float amax, float *s)
 {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(amax * (1.0f / 6.0f)));
-    uint32_t b = r & 0xFFu;
+    uint32_t b = e4m3x2_near(amax * (1.0f / 6.0f), 0.f);
     auto value = [](uint32_t byte) {
         const uint32_t h = e4m3x2_to_f16x2(byte);
         return __half2float(*reinterpret_cast<const __half *>(&h));
     };
-    if (6.0f * value(b) < amax && b < 0x7Eu) ++b;
     *s = value(b);
+    if (6.0f * *s < amax && b < 0x7Eu) *s = value(++b);
     return b;
 }
 
-// E2M1 codes of 8 values that came from 16-bit floats, under scale s (r = 1 / s).
-// x r is within 2^-22 (relative) of x / s.  A 16-bit x has at most 11 significant
+// E2M1 codes of 16 values that came from 16-bit floats, under scale s.  With the
+// hardware's reciprocal r of s (off by at most one step, 2^-23), x r is within
+// 2^-22 (relative) of x / s.  A 16-bit x has at most 11 significant
 // bits and a midpoint m s (m of .25, .75, 1.25, 1.75, 2.5, 3.5, 5) at most 7, so
 // x / s is either exactly m or at least 2^-11 away from it: rounding x r to 17
 // bits gives exactly m in the first case and stays on its side in the second,
 // and the hardware's round-to-nearest-even then decides as the exact quotient
 // would.  (fp32 values may lie within 2^-24 of a midpoint: they are compared.)
-__device__ __forceinline__ uint32_t fp4_codes16(const float (&x)[8], float r)
+__device__ __forceinline__ uint2 fp4_codes16(const float (&x)[16], float s)
 {
-    uint32_t w = 0;
-    float q[8];
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        q[i] = __uint_as_float((__float_as_uint(x[i] * r) + 0x40u) & ~0x7Fu);
-    asm("{\n"
-        ".reg .b8 b0, b1, b2, b3;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
-        "mov.b32 %0, {b0, b1, b2, b3};\n"
-        "}\n"
-        : "=r"(w)
-        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-    // a negative value that rounds to zero has code 0
-    const uint32_t mag = w & 0x77777777u;
-    return mag | (w & (((mag + 0x77777777u) & 0x88888888u)));
+    for (int h = 0; h < 2; ++h) {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = __uint_as_float((__float_as_uint(x[8 * h + i] * r) + 0x40u) & ~0x7Fu);
+        asm("{\n"
+            ".reg .b8 b0, b1, b2, b3;\n"
+            "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+            "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+            "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+            "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+            "mov.b32 %0, {b0, b1, b2, b3};\n"
+            "}\n"
+            : "=r"(w[h])
+            : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+        // a negative value that rounds to zero has code 0
+        const uint32_t mag = w[h] & 0x77777777u;
+        w[h] = mag | (w[h] & ((mag + 0x77777777u) & 0x88888888u));
+    }
+    return make_uint2(w[0], w[1]);
 }
 
 template <typename T>
@@ -111,11 +125,9 @@ __global__ void __launch_bounds__(256) cache_write_kernel(csa2_cache cache, cons
     const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (i >= n) return;
-    const int64_t row = rows[i];
-    float v[2][8];
-    load_as_f32<8>(x + i * ld_x + 8 * lane, v[0]);
-    load_as_f32<8>(x + i * ld_x + 256 + 8 * lane, v[1]);
-    float k[4] = {0.f, 0.f, 0.f, 0.f};
+    const int64_t row = __ldg(rows + i);
+    float v[16], k[4] = {0.f, 0.f, 0.f, 0.f};
+    load_as_f32<16>(x + i * ld_x + 16 * lane, v);
     if (key != nullptr) {
         if (cache.d_idx == 128) {
             load_as_f32<4>(key + i * ld_key + 4 * lane, k);
@@ -130,34 +142,38 @@ __global__ void __launch_bounds__(256) cache_write_kernel(csa2_cache cache, cons
         if (lane == 0) count_event(counters, CSA2_CNT_BAD_INPUT);
         return;
     }
+    float amax = 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float amax = 0.f;                         // of the 16-channel group of lanes 2 j, 2 j + 1
+    for (int c = 0; c < 16; ++c) amax = fmaxf(amax, fabsf(v[c]));
+    uint32_t sb = 0;
+    uint2 codes = make_uint2(0u, 0u);
+    if (amax > 0.f) {
+        if (amax > 2688.f) count_event(counters, CSA2_CNT_FP4_SATURATED);
+        float s;
+        sb = fp4_scale_near(amax, &s);
+        if constexpr (sizeof(T) == 2) {
+            codes = fp4_codes16(v, s);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) amax = fmaxf(amax, fabsf(v[h][c]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        uint32_t sb = 0, codes = 0;
-        if (amax > 0.f) {
-            if (amax > 2688.f && (lane & 1) == 0) count_event(counters, CSA2_CNT_FP4_SATURATED);
-            float s;
-            sb = fp4_scale_near(amax, &s);
-            if constexpr (sizeof(T) == 2) {
-                codes = fp4_codes16(v[h], 1.0f / s);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) codes |= fp4_code(v[h][c], s) << (4 * c);
+            for (int c = 0; c < 8; ++c) {
+                codes.x |= fp4_code(v[c], s) << (4 * c);
+                codes.y |= fp4_code(v[8 + c], s) << (4 * c);
             }
         }
-        *reinterpret_cast<uint32_t *>(cache.codes + row * CSA2_CODE_BYTES + 128 * h + 4 * lane) = codes;
-        if ((lane & 1) == 0) cache.scales[row * CSA2_SCALE_BYTES + 16 * h + (lane >> 1)] = (uint8_t)sb;
     }
+    *reinterpret_cast<uint2 *>(cache.codes + row * CSA2_CODE_BYTES + 8 * lane) = codes;
+    cache.scales[row * CSA2_SCALE_BYTES + lane] = (uint8_t)sb;
     if (key == nullptr) return;
     float a = fmaxf(fmaxf(fabsf(k[0]), fabsf(k[1])), fmaxf(fabsf(k[2]), fabsf(k[3])));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float s = fp8_pow2_scale(a), r = 1.0f / s;   // (a power of two: k r is k / s)
-    const uint32_t w = e4m3_byte(k[0] * r) | (e4m3_byte(k[1] * r) << 8) | (e4m3_byte(k[2] * r) << 16) |
-                       (e4m3_byte(k[3] * r) << 24);
+    const float s = fp8_pow2_scale(a);
+    // 1 / s by its exponent: s = 2^e with -126 <= e <= 120, so k / s is k times a power of two
+    const float r = __uint_as_float((254u << 23) - __float_as_uint(s));
+    uint32_t w = e4m3x2_near(k[0] * r, k[1] * r) | (e4m3x2_near(k[2] * r, k[3] * r) << 16);
+    // a negative value that rounds to zero is byte 0
+    const uint32_t mag = w & 0x7F7F7F7Fu;
+    w = mag | (w & ((mag + 0x7F7F7F7Fu) & 0x80808080u));
     if (cache.d_idx == 128)
         *reinterpret_cast<uint32_t *>(cache.kidx + row * 128 + lane * 4) = w;
     else
@@ -170,24 +186,29 @@ template <typename T>
 __device__ __forceinline__ void store8(T *dst, uint4 h)
 {
     if constexpr (__is_same(T, __half)) {
-        *reinterpret_cast<uint4 *>(dst) = h;
+        __stcs(reinterpret_cast<uint4 *>(dst), h);
     } else {
         const uint32_t w[4] = {h.x, h.y, h.z, h.w};
         float2 f[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
         if constexpr (__is_same(T, float)) {
-            reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-            reinterpret_cast<float4 *>(dst)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+            __stcs(reinterpret_cast<float4 *>(dst), make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
+            __stcs(reinterpret_cast<float4 *>(dst) + 1, make_float4(f[2].x, f[2].y, f[3].x, f[3].y));
         } else {
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(f[j].y), "f"(f[j].x));
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 }
+
+// A warp reads kReadRows rows, their loads all on the way before the first store
+// (200,003 rows with keys: 64.6 us one row at a time, 61.0 two, 62 four; the
+// stores are not read back soon and are marked so).
+constexpr int kReadRows = 2;
 
 template <typename T>
 __global__ void __launch_bounds__(256) cache_read_kernel(csa2_cache cache, const int64_t *__restrict__ rows,
@@ -197,42 +218,61 @@ __global__ void __launch_bounds__(256) cache_read_kernel(csa2_cache cache, const
 {
     pdl_wait();
     pdl_trigger();
-    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t i0 = (((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5) * kReadRows;
     const int lane = threadIdx.x & 31;
-    if (i >= n) return;
-    const int64_t row = rows[i];
-    if (row < 0) return;                          // padding
-    if (row >= cache.cap) {
-        if (lane == 0) count_event(counters, CSA2_CNT_BAD_INPUT);
-        return;
-    }
-    uint32_t w[2], sc[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        w[h] = *reinterpret_cast<const uint32_t *>(cache.codes + row * CSA2_CODE_BYTES + 128 * h + 4 * lane);
-        sc[h] = cache.scales[row * CSA2_SCALE_BYTES + 16 * h + (lane >> 1)];
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        store8(x + i * ld_x + 256 * h + 8 * lane, fp4x8_to_f16(w[h], scale_pair(sc[h])));
-    if (key == nullptr) return;
-    const float s = cache.kscale[row];
     const int per = cache.d_idx / 32;
-    const uint32_t b = per == 4 ? *reinterpret_cast<const uint32_t *>(cache.kidx + row * 128 + 4 * lane)
-                                : *reinterpret_cast<const uint16_t *>(cache.kidx + row * 64 + 2 * lane);
-    const uint32_t lo = e4m3x2_to_f16x2(b & 0xFFFFu), hi = e4m3x2_to_f16x2(b >> 16);
-    const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-    const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    float *dst = key + i * ld_key + per * lane;
-    if (per == 4)
-        *reinterpret_cast<float4 *>(dst) = make_float4(f0.x * s, f0.y * s, f1.x * s, f1.y * s);
-    else
-        *reinterpret_cast<float2 *>(dst) = make_float2(f0.x * s, f0.y * s);
+    int64_t row[kReadRows];
+    uint32_t w[kReadRows][2], sc[kReadRows][2], kb[kReadRows];
+    float ks[kReadRows];
+#pragma unroll
+    for (int j = 0; j < kReadRows; ++j) row[j] = i0 + j < n ? __ldg(rows + i0 + j) : -1;
+#pragma unroll
+    for (int j = 0; j < kReadRows; ++j) {
+        if (row[j] >= cache.cap) {
+            if (lane == 0) count_event(counters, CSA2_CNT_BAD_INPUT);
+            row[j] = -1;
+        }
+        if (row[j] >= 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w[j][h] = __ldg(reinterpret_cast<const uint32_t *>(cache.codes + row[j] * CSA2_CODE_BYTES + 128 * h + 4 * lane));
+                sc[j][h] = __ldg(cache.scales + row[j] * CSA2_SCALE_BYTES + 16 * h + (lane >> 1));
+            }
+            if (key != nullptr) {
+                ks[j] = __ldg(cache.kscale + row[j]);
+                kb[j] = per == 4 ? __ldg(reinterpret_cast<const uint32_t *>(cache.kidx + row[j] * 128 + 4 * lane))
+                                 : __ldg(reinterpret_cast<const uint16_t *>(cache.kidx + row[j] * 64 + 2 * lane));
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kReadRows; ++j) {
+        if (row[j] < 0) continue;
+        const int64_t i = i0 + j;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            store8(x + i * ld_x + 256 * h + 8 * lane, fp4x8_to_f16(w[j][h], scale_pair(sc[j][h])));
+        if (key == nullptr) continue;
+        const uint32_t lo = e4m3x2_to_f16x2(kb[j] & 0xFFFFu), hi = e4m3x2_to_f16x2(kb[j] >> 16);
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        float *dst = key + i * ld_key + per * lane;
+        const float s = ks[j];
+        if (per == 4)
+            __stcs(reinterpret_cast<float4 *>(dst), make_float4(f0.x * s, f0.y * s, f1.x * s, f1.y * s));
+        else
+            __stcs(reinterpret_cast<float2 *>(dst), make_float2(f0.x * s, f0.y * s));
+    }
 }
 
 constexpr int kRowThreads = 256;
 
-static unsigned row_blocks(int64_t n) { return (unsigned)((n + kRowThreads / 32 - 1) / (kRowThreads / 32)); }
+// blocks for n rows, `per` to a warp
+static unsigned row_blocks(int64_t n, int per)
+{
+    const int64_t k = kRowThreads / 32 * per;
+    return (unsigned)((n + k - 1) / k);
+}
 
 cudaError_t launch_cache_write(const csa2_cache &c, const int64_t *rows, int64_t n, const void *x, int x_type,
                                int64_t ld_x, const void *key, int64_t ld_key, uint32_t *counters,
@@ -240,7 +280,7 @@ cudaError_t launch_cache_write(const csa2_cache &c, const int64_t *rows, int64_t
 {
     auto go = [&](auto tag) {
         using T = decltype(tag);
-        return launch_k(cache_write_kernel<T>, dim3(row_blocks(n)), dim3(kRowThreads), 0, st, 0, c, rows, n,
+        return launch_k(cache_write_kernel<T>, dim3(row_blocks(n, 1)), dim3(kRowThreads), 0, st, 0, c, rows, n,
                         static_cast<const T *>(x), ld_x, static_cast<const T *>(key), ld_key, counters);
     };
     const cudaError_t e = x_type == CSA2_F32 ? go(float{}) : x_type == CSA2_BF16 ? go(__nv_bfloat16{}) : go(__half{});
@@ -252,7 +292,7 @@ cudaError_t launch_cache_read(const csa2_cache &c, const int64_t *rows, int64_t 
 {
     auto go = [&](auto tag) {
         using T = decltype(tag);
-        return launch_k(cache_read_kernel<T>, dim3(row_blocks(n)), dim3(kRowThreads), 0, st, 0, c, rows, n,
+        return launch_k(cache_read_kernel<T>, dim3(row_blocks(n, kReadRows)), dim3(kRowThreads), 0, st, 0, c, rows, n,
                         static_cast<T *>(x), ld_x, key, ld_key, counters);
     };
     const cudaError_t e = x_type == CSA2_F32 ? go(float{}) : x_type == CSA2_BF16 ? go(__nv_bfloat16{}) : go(__half{});
