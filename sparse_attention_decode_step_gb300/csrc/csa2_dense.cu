@@ -104,13 +104,9 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
     return a / b;
 }
 
-// First unit of a pair's run: equal runs, none of them empty (of U units in all,
-// pairs past U have none).
-__device__ __forceinline__ int64_t run_begin(const DenseParams &p, int64_t pair, int64_t U)
-{
-    const int64_t P = min((int64_t)p.pairs, U);
-    return pair < P ? quotient(pair * U, P) : U;
-}
+// Units in a pair's run: ceil(U / pairs) each, so that the last pairs may have
+// none (no more pairs, and no more split row tiles, than the longest run needs).
+__device__ __forceinline__ int64_t run_units(const DenseParams &p, int64_t U) { return quotient(U + p.pairs - 1, p.pairs); }
 
 // One pair's pieces of work in order: entries k0 .. k1 (in tiles) of a row tile.
 // find() sets up the first piece.
@@ -141,7 +137,7 @@ struct Work {
 // there are more than 32).
 struct Found {
     Work w;
-    int64_t total;       // units of all groups
+    int64_t run;         // units of a pair's run
     int64_t u0, u1;      // this pair's
     int empty;           // some group has rows but no entries
 };
@@ -149,8 +145,16 @@ struct Found {
 __device__ __forceinline__ void find(const DenseParams &p, int pair, int lane, bool count_bad, Found *out)
 {
     Group gr{};
-    int64_t total = 0;
+    int64_t total = 0, upto = 0;
     int empty = 0;
+    auto scan = [&](int64_t mine) {            // inclusive sums over the warp
+        upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+    };
     for (int g0 = 0; g0 < p.ng; g0 += 32) {
         gr = Group{};
         if (g0 + lane < p.ng) {
@@ -158,14 +162,13 @@ __device__ __forceinline__ void find(const DenseParams &p, int pair, int lane, b
             if (gr.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
             if (!gr.bad && gr.n == 0 && gr.rows > 0) empty = 1;
         }
-        total += units(gr);
+        scan(units(gr));
+        total += __shfl_sync(0xffffffffu, upto, 31);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     empty = __any_sync(0xffffffffu, empty);
-    const int64_t u0 = run_begin(p, pair, total), u1 = run_begin(p, pair + 1, total);
+    const int64_t run = run_units(p, total), u0 = min(pair * run, total), u1 = min(u0 + run, total);
     if (lane == 0) {
-        out->total = total;
+        out->run = run;
         out->u0 = u0;
         out->u1 = u1;
         out->empty = empty;
@@ -176,18 +179,12 @@ __device__ __forceinline__ void find(const DenseParams &p, int pair, int lane, b
         if (p.ng > 32) {
             gr = Group{};
             if (g0 + lane < p.ng) gr = group_of(p, g0 + lane);
-        }
-        const int64_t mine = units(gr);
-        int64_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+            scan(units(gr));
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, before + upto > u0);
         if (hit != 0u) {
             if (lane == __ffs(hit) - 1) {
-                const int64_t in_group = u0 - (before + upto - mine);
+                const int64_t in_group = u0 - (before + upto - units(gr));
                 Work &w = out->w;
                 w.gr = gr;
                 w.g = g0 + lane;
@@ -352,6 +349,37 @@ __device__ __forceinline__ Joined join_prev(float m, float l, bool any_prev, flo
     return j;
 }
 
+// 64 rows of Q as f16 into the swizzled sQ (rows from n_rows on are zero), by
+// the 256 threads t of eight warps: thread t takes the 16 bytes number t + 256 i,
+// all 16 of them on their way at once, and converts them where they lie.
+__device__ __forceinline__ void issue_q(const DenseParams &p, uint8_t *sQ, int64_t row0, int n_rows, int t)
+{
+    const int c8 = t & 63;
+    const uint8_t *src = reinterpret_cast<const uint8_t *>(p.q + row0 * CSA2_D);
+    const uint32_t dst = smem_u32(sQ) + (c8 >> 3) * kQAtom;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = (t >> 6) + 4 * i;
+        cp_async16(dst + sw128(r, c8 & 7), r < n_rows ? src + r * 1024 + c8 * 16 : src, r < n_rows);
+    }
+}
+
+__device__ __forceinline__ void finish_q(const DenseParams &p, uint8_t *sQ, int t)
+{
+    const int c8 = t & 63;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (p.q_type == CSA2_BF16) {
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+            uint4 *const at = reinterpret_cast<uint4 *>(sQ + (c8 >> 3) * kQAtom + sw128((t >> 6) + 4 * i, c8 & 7));
+            const uint4 v = *at;
+            *at = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+        }
+    }
+    fence_async_smem();
+    __syncwarp();
+}
+
 // Rows of a group without entries: the caller's partial result, or nothing.
 template <int kOut>
 __device__ __forceinline__ void empty_rows(const DenseParams &p, const Group &gr, int first, int step)
@@ -405,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         mbar_init(&bar_s[1], 1);
         mbar_init(bar_p, 2 * kWarpsSoft);
         mbar_init(bar_o, 1);
-        mbar_init(bar_q, 2 * kWarpsProd);
+        mbar_init(bar_q, 2 * 8);               // eight warps of each CTA, of either kind
         mbar_init(bar_done, 1);
         sFlag[0] = 0;
         fence_barrier_init();
@@ -425,15 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem = *sTmem;
-    const int64_t U = sFound->total, u0 = sFound->u0, u1 = sFound->u1;
+    const int64_t u0 = sFound->u0, u1 = sFound->u1;
     Work w = sFound->w;
     if (tid == 0 && rank == 0) {
         // for the join: the row tile that this pair begins in
         DenseBegin d{};
-        d.total = U;
         if (u1 > u0) {
             d.first = u0 - w.k0;
             d.last = d.first + w.kt;
+            d.run = sFound->run;
             d.row0 = w.gr.row0 + w.rt * kRowsPair;
             d.rows = min(kRowsPair, w.gr.rows - w.rt * kRowsPair);
         }
@@ -590,38 +618,19 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             };
             begin(0);
             load(0);
-            // ---- Q as f16 (rows past the tile's are zero), once the last piece's scores are done
-            if (tiles > 0)
+            // ---- Q, once the last piece's scores are done (the first piece's comes from
+            // the softmax warps, which have nothing else to do then)
+            if (tiles > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, abort_flag));
-            if (!ok) break;
-            {
+                if (!ok) break;
                 const int r0 = w.rt * kRowsPair + kRowsCta * (int)rank;
                 const int n_rows = max(0, min(kRowsCta, w.gr.rows - r0));
-                // 16 bytes: number t + 256 i of the 64 rows x 64, all 16 on their way at once,
-                // then converted where they lie
-                const int t = 32 * pw + lane, c8 = t & 63;
-                const uint8_t *src = reinterpret_cast<const uint8_t *>(p.q + (int64_t)(w.gr.row0 + r0) * CSA2_D);
-                const uint32_t dst = smem_u32(sQ) + (c8 >> 3) * kQAtom;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = (t >> 6) + 4 * i;
-                    const bool in = r < n_rows;
-                    cp_async16(dst + sw128(r, c8 & 7), in ? src + r * 1024 + c8 * 16 : src, in);
-                }
+                issue_q(p, sQ, (int64_t)(w.gr.row0 + r0), n_rows, 32 * pw + lane);
                 load(1);
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                if (p.q_type == CSA2_BF16) {
-#pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        uint4 *const at = reinterpret_cast<uint4 *>(sQ + (c8 >> 3) * kQAtom + sw128((t >> 6) + 4 * i, c8 & 7));
-                        const uint4 v = *at;
-                        *at = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z),
-                                         bf16x2_to_f16x2(v.w));
-                    }
-                }
-                fence_async_smem();
-                __syncwarp();
+                finish_q(p, sQ, 32 * pw + lane);
                 if (lane == 0) arrive_at(q_full);
+            } else {
+                load(1);
             }
             tiles += n_tiles;
             for (int b = 0; b < n_blocks && ok; ++b) {
@@ -674,6 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             const int r0 = w.rt * kRowsPair + kRowsCta * (int)rank;
             const int n_rows = max(0, min(kRowsCta, w.gr.rows - r0));
             const int64_t row0 = w.gr.row0 + r0;
+            if (tile == 0) {
+                issue_q(p, sQ, row0, n_rows, tid);
+                finish_q(p, sQ, tid);
+                if (lane == 0) arrive_at(in_cta(smem_u32(bar_q), 0));
+            }
             if (tid < kRowsCta) sM[tid] = -INFINITY;
             soft_sync();
             float l = 0.f;
@@ -890,30 +904,30 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 // sums are added in order.  A block's item is 4 / parts whole rows, so that lse
 // may be prev_lse itself.
 template <int kOut>
-__global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
+__global__ void __launch_bounds__(kJoinThreads, 2) dense_join_kernel(DenseParams p)
 {
-    __shared__ int sPair[kDensePairsMax], sItem[kDensePairsMax], sWarp[kJoinThreads / 32];
+    __shared__ DenseBegin sTile[kDensePairsMax];
+    __shared__ int sPair[kDensePairsMax], sItem[kDensePairsMax], sWarp[2][kJoinThreads / 32];
     __shared__ float sW[4][kDensePairsMax];
     __shared__ float4 sO[kJoinThreads];
     __shared__ Joined sJ[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (the next kernel of the stream is let in only as these blocks finish: one of
+    // this library's attention CTAs takes a whole SM, and waiting there it would
+    // keep the SM from the blocks it waits for)
     pdl_wait();
-    pdl_trigger();
     // the tiles to join (in order) and their work items; every thread looks at one pair
-    auto ends = [&](int c, const DenseBegin &d) {
-        // pairs c .. that begin before d.last: run_begin(x) = x U / P < last
-        const int64_t P = min((int64_t)p.pairs, d.total);
-        return (int)min(P, (d.last * P + d.total - 1) / d.total);
+    auto pieces_of = [&](int c, const DenseBegin &d) {     // pair c - 1's, and those of the pairs that begin before d.last
+        return (int)quotient(d.last + d.run - 1, d.run) - c + 1;
     };
     auto parts_of = [](int n_pieces) { return n_pieces <= 4 ? 1 : n_pieces <= 8 ? 2 : 4; };
     int items = 0;
+    DenseBegin mine{};
     if (tid > 0 && tid < p.pairs) {
-        const DenseBegin d = p.begin[tid];
-        const int64_t b0 = run_begin(p, tid, d.total);
-        if (b0 < d.total && b0 > d.first && run_begin(p, tid - 1, d.total) <= d.first) {
-            const int parts = parts_of(ends(tid, d) - tid + 1);
-            items = (d.rows * (CSA2_D / 4) * parts + kJoinThreads - 1) / kJoinThreads;
-        }
+        mine = p.begin[tid];
+        const int64_t b0 = tid * mine.run;
+        if (mine.rows > 0 && b0 > mine.first && b0 - mine.run <= mine.first)
+            items = (mine.rows * (CSA2_D / 4) * parts_of(pieces_of(tid, mine)) + kJoinThreads - 1) / kJoinThreads;
     }
     const uint32_t has = __ballot_sync(0xffffffffu, items > 0);
     int upto = items;
@@ -922,37 +936,52 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
         const int v = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += v;
     }
-    if (lane == 31) sWarp[warp] = upto;
-    if (lane == 0) sPair[warp] = __popc(has);        // (counts, until the list is written)
+    if (lane == 31) { sWarp[0][warp] = upto; sWarp[1][warp] = __popc(has); }
     __syncthreads();
     int before = 0, n = 0, total = 0, tiles = 0;
+#pragma unroll
     for (int i = 0; i < kJoinThreads / 32; ++i) {
-        if (i < warp) { before += sWarp[i]; n += sPair[i]; }
-        total += sWarp[i];
-        tiles += sPair[i];
+        const int a = sWarp[0][i], b = sWarp[1][i];
+        if (i < warp) { before += a; n += b; }
+        total += a;
+        tiles += b;
     }
-    __syncthreads();
     if (items > 0) {
         const int at = n + __popc(has & ((1u << lane) - 1));
         sPair[at] = tid;
         sItem[at] = before + upto - items;
+        sTile[at] = mine;
     }
     __syncthreads();
     int at = 0;
     for (int item = blockIdx.x; item < total; item += gridDim.x) {
         while (at + 1 < tiles && sItem[at + 1] <= item) ++at;
         const int c = sPair[at];
-        const DenseBegin d = p.begin[c];
-        const int n_pieces = ends(c, d) - c + 1, parts = parts_of(n_pieces);
+        const DenseBegin &d = sTile[at];
+        const int n_pieces = pieces_of(c, d), parts = parts_of(n_pieces);
         const int wide = kJoinThreads / parts;            // threads (of 4 channels) side by side
         const int part = tid / wide;
         const int cell = (item - sItem[at]) * wide + tid % wide;
         const int r = cell / (CSA2_D / 4), ch = 4 * (cell % (CSA2_D / 4));
         const int r0 = (item - sItem[at]) * wide / (CSA2_D / 4);    // the item's rows: r0 .. r0 + 4 / parts - 1
+        const bool in = r < d.rows;
+        const int64_t row = d.row0 + r;
         auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c - 1 + i); };
+        const float *src = p.part_o + (int64_t)r * CSA2_D + ch;
+        auto load = [&](int i) {
+            return in && i < n_pieces ? *reinterpret_cast<const float4 *>(src + slot(i) * kRowsPair * CSA2_D)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        // the first pieces and the caller's part are on their way before the weights
+        // are known (without a partial result prev_out may hold anything: weight 0)
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = load(part + k * parts);
+        float4 pv = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.prev_out != nullptr && part == 0 && in)
+            pv = *reinterpret_cast<const float4 *>(p.prev_out + row * CSA2_D + ch);
         __syncthreads();                              // (the last item's shared values are read)
         if (warp < 4 / parts && r0 + warp < d.rows) {
-            const int64_t row = d.row0 + r0 + warp;
             float m = -INFINITY, l = 0.f;
             for (int i = lane; i < n_pieces; i += 32) m = fmaxf(m, p.part_ml[slot(i) * 2 * kRowsPair + r0 + warp]);
 #pragma unroll
@@ -965,28 +994,22 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (lane == 0) sJ[warp] = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[row] : 0.f);
+            if (lane == 0)
+                sJ[warp] = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[d.row0 + r0 + warp] : 0.f);
         }
         __syncthreads();
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < d.rows) {
-            const float *src = p.part_o + (int64_t)r * CSA2_D + ch;
-            for (int i0 = part; i0 < n_pieces; i0 += 4 * parts) {
-                float4 v[4];
-                float wgt[4];
+        for (int i0 = part; i0 < n_pieces; i0 += 4 * parts) {
+            if (i0 != part) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = i0 + k * parts;
-                    wgt[k] = i < n_pieces ? sW[r - r0][i] : 0.f;
-                    // (a piece without weight may hold anything)
-                    v[k] = wgt[k] != 0.f ? *reinterpret_cast<const float4 *>(src + slot(i) * kRowsPair * CSA2_D)
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
+                for (int k = 0; k < 4; ++k) v[k] = load(i0 + k * parts);
+            }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    o.x = fmaf(v[k].x, wgt[k], o.x); o.y = fmaf(v[k].y, wgt[k], o.y);
-                    o.z = fmaf(v[k].z, wgt[k], o.z); o.w = fmaf(v[k].w, wgt[k], o.w);
-                }
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * parts;
+                const float wgt = in && i < n_pieces ? sW[r - r0][i] : 0.f;
+                o.x = fmaf(v[k].x, wgt, o.x); o.y = fmaf(v[k].y, wgt, o.y);
+                o.z = fmaf(v[k].z, wgt, o.z); o.w = fmaf(v[k].w, wgt, o.w);
             }
         }
         if (parts > 1) {
@@ -994,17 +1017,15 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseParams p)
             __syncthreads();
             if (part == 0)
                 for (int i = 1; i < parts; ++i) {
-                    const float4 v = sO[i * wide + tid];
-                    o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+                    const float4 u = sO[i * wide + tid];
+                    o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
                 }
         }
-        if (part == 0 && r < d.rows) {
-            const int64_t row = d.row0 + r;
+        if (part == 0 && in) {
             const Joined j = sJ[r - r0];
-            float4 pv = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j.prev != 0.f) pv = *reinterpret_cast<const float4 *>(p.prev_out + row * CSA2_D + ch);
+            if (j.prev == 0.f) pv = make_float4(0.f, 0.f, 0.f, 0.f);
             store4<kOut>(p.out, row * CSA2_D + ch, fmaf(pv.x, j.prev, o.x * j.own), fmaf(pv.y, j.prev, o.y * j.own),
-                   fmaf(pv.z, j.prev, o.z * j.own), fmaf(pv.w, j.prev, o.w * j.own));
+                         fmaf(pv.z, j.prev, o.z * j.own), fmaf(pv.w, j.prev, o.w * j.own));
         }
         if (p.lse && tid < 4 / parts && r0 + tid < d.rows) p.lse[d.row0 + r0 + tid] = sJ[tid].lse;
     }
@@ -1030,7 +1051,7 @@ static cudaError_t launch_dense_as(const DenseParams &p, cudaStream_t st)
     }
     e = launch_k(dense_attn_kernel<kOut>, dim3(2 * p.pairs), dim3(kThreads), smem, st, 2, p);
     if (e == cudaSuccess && p.pairs > 1)
-        e = launch_k(dense_join_kernel<kOut>, dim3(8 * p.pairs), dim3(kJoinThreads), 0, st, 0, p);
+        e = launch_k(dense_join_kernel<kOut>, dim3(4 * p.pairs), dim3(kJoinThreads), 0, st, 0, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

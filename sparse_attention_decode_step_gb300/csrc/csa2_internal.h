@@ -124,9 +124,9 @@ cudaError_t launch_cache_read(const csa2_cache &c, const int64_t *rows, int64_t 
 constexpr int kDenseRows = 128;         // (query, head) rows of a tile, one pair of CTAs
 constexpr int kDenseEntries = 256;      // entries of a tile
 constexpr int kDensePairsMax = 512;     // pairs of CTAs of a launch
-// Where a pair's run of tiles begins: the row tile's units [first, last) of
-// `total`, and its rows.
-struct DenseBegin { int64_t first, last, total, row0; int rows, pad; };
+// Where a pair's run of tiles begins: the row tile's units [first, last), its
+// rows, and the units of a run.  rows = 0: the pair has no work.
+struct DenseBegin { int64_t first, last, run; int row0, rows; };
 struct DenseParams {
     const uint8_t *codes, *scales;
     const int64_t *seq_base;
