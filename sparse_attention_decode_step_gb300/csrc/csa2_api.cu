@@ -95,18 +95,18 @@ size_t attn_workspace_bytes(int nq, int H, int k_max, int n_win)
     return 0;
 }
 
-// One pair of CTAs per two SMs, or per tile when there are fewer: at most
-// ceil(nq H / 128) + ng - 1 row tiles (each group rounds up) of ceil(max_n / 256)
-// entry tiles.
+// One pair of CTAs per two SMs, or per unit of work when there are fewer: at
+// most ceil(nq H / 128) + ng - 1 row tiles (each group rounds up) of
+// ceil(max_n / 256) entry tiles and kDenseSetup.
 DensePlan dense_plan(int ng, int nq, int H, int64_t max_n)
 {
     DensePlan d{};
     if (ng < 1 || nq < 1 || H < 1) return d;
     const int64_t rows = ((int64_t)nq * H + kDenseRows - 1) / kDenseRows + (ng < nq ? ng : nq) - 1;
-    const int64_t ents = (max_n + kDenseEntries - 1) / kDenseEntries;
+    const int64_t units = rows * ((max_n + kDenseEntries - 1) / kDenseEntries + kDenseSetup);
     int64_t pairs = device_sm_count() / 2;
     if (pairs > kDensePairsMax) pairs = kDensePairsMax;
-    if (ents < 1 || pairs > rows * ents) pairs = rows * ents;
+    if (pairs > units) pairs = units;
     if (pairs < 1) pairs = 1;
     d.pairs = (int)pairs;
     d.off_ml = (size_t)pairs * 2 * kDenseRows * CSA2_D * 4;
