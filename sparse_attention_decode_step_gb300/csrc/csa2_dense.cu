@@ -829,8 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 j = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[row0 + row] : 0.f);
             soft_sync();                       // (sRed is read, and prev_lse, which may be lse itself)
             if (which == 0) {
-                sRed[row] = j.own;
-                sRed[kRowsCta + row] = j.prev;
+                sRed[row] = j.prev;
                 if (whole) {
                     if (row < n_rows && p.lse) p.lse[row0 + row] = j.lse;
                 } else {
@@ -845,12 +844,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             uint8_t *turn = sP + warp * 4096;
             const int r_base = 32 * (quarter & 1) + (lane >> 3), c_lane = chan + 4 * (lane & 7);
             const int mine = (n_rows - r_base + 3) / 4;       // of this lane's 8 rows r_base + 4 i
-            float own[8], pw[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                own[i] = sRed[r_base + 4 * i];
-                pw[i] = i < mine ? sRed[kRowsCta + r_base + 4 * i] : 0.f;
-            }
             const int64_t out0 = (row0 + r_base) * CSA2_D + c_lane;
             float *const part0 = p.part_o + (piece * kRowsPair + kRowsCta * (int)rank + r_base) * CSA2_D + c_lane;
 #pragma unroll 1
@@ -861,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     *reinterpret_cast<float4 *>(turn + sw128((uint32_t)lane, (uint32_t)k)) =
-                        make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        make_float4(o[4 * k] * j.own, o[4 * k + 1] * j.own, o[4 * k + 2] * j.own, o[4 * k + 3] * j.own);
                 __syncwarp();
                 float4 v[8];
 #pragma unroll
@@ -870,17 +863,23 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                         turn + sw128((uint32_t)((lane >> 3) + 4 * i), (uint32_t)(lane & 7)));
                 __syncwarp();
                 if (whole) {
-                    float4 pv[8];
+                    if (p.prev_out != nullptr) {
+                        float4 pv[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)    // (a row without a partial result: weight 0, prev_out not read)
+                            pv[i] = i < mine && sRed[r_base + 4 * i] != 0.f
+                                        ? *reinterpret_cast<const float4 *>(p.prev_out + out0 + 4 * i * CSA2_D + 32 * c)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float pw = sRed[r_base + 4 * i];
+                            v[i].x = fmaf(pv[i].x, pw, v[i].x); v[i].y = fmaf(pv[i].y, pw, v[i].y);
+                            v[i].z = fmaf(pv[i].z, pw, v[i].z); v[i].w = fmaf(pv[i].w, pw, v[i].w);
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        pv[i] = pw[i] != 0.f ? *reinterpret_cast<const float4 *>(p.prev_out + out0 + 4 * i * CSA2_D + 32 * c)
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < mine)
-                            store4<kOut>(p.out, out0 + 4 * i * CSA2_D + 32 * c, fmaf(pv[i].x, pw[i], v[i].x * own[i]),
-                                         fmaf(pv[i].y, pw[i], v[i].y * own[i]), fmaf(pv[i].z, pw[i], v[i].z * own[i]),
-                                         fmaf(pv[i].w, pw[i], v[i].w * own[i]));
+                        if (i < mine) store4<kOut>(p.out, out0 + 4 * i * CSA2_D + 32 * c, v[i].x, v[i].y, v[i].z, v[i].w);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
