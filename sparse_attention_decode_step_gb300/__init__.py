@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 import threading
 
 import torch
@@ -198,6 +199,14 @@ class Cache:
         c.seq_base, c.seq_len, c.base_host = seq_base, seq_len, None
         return c
 
+    def packed(self) -> bytes:
+        """The bytes of struct()."""
+        keys = self.kidx is not None
+        return _CACHE_FMT.pack(self.codes.data_ptr(), self.scales.data_ptr(),
+                               self.kidx.data_ptr() if keys else 0, self.kscale.data_ptr() if keys else 0,
+                               self.seq_base.data_ptr(), self.seq_len.data_ptr(), self.cap, self.batch,
+                               self.d_idx, self.m)
+
     def struct(self, seq=None) -> _Cache:
         """The C struct; with seq = b, a one-sequence view of sequence b."""
         keys = (None, None) if self.kidx is None else (self.kidx.data_ptr(), self.kscale.data_ptr())
@@ -235,6 +244,11 @@ class Groups:
         self.ng = self.seq.numel()
         if self.off.numel() != self.ng + 1 or (length is not None and self.length.numel() != self.ng):
             raise CsaError("groups need seq [ng], off [ng + 1] and length [ng]")
+
+    def packed(self, nq: int) -> bytes:
+        """The bytes of struct()."""
+        return _GROUPS_FMT.pack(self.seq.data_ptr(), self.off.data_ptr(),
+                                0 if self.length is None else self.length.data_ptr(), self.ng, nq)
 
     def struct(self, nq: int) -> _Groups:
         return _Groups(self.seq.data_ptr(), self.off.data_ptr(),
@@ -346,8 +360,13 @@ def sparse_attn(cache: Cache, qs: Queries, idx, cnt, q, win, n_win, out, lse=Non
 
 
 # The calls below are short on the GPU, so their marshalling is kept short too:
-# functions are looked up once, pointers go as integers, the stream as its handle.
+# functions are looked up once, pointers go as integers, the C structures as
+# packed bytes (checked against the ctypes ones by the tests), the stream as its
+# handle.
 _fn = {}
+_CACHE_FMT = struct.Struct("6Pq3i4x")      # csa2_cache
+_GROUPS_FMT = struct.Struct("3P2i")        # csa2_groups
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _call(name, *args):
@@ -359,12 +378,12 @@ def _call(name, *args):
         _check(status, name)
 
 
-def _device(*tensors) -> int:
+def _device(first, *rest) -> int:
     """The current device, which all tensors must be on: a call runs on its stream."""
-    dev = tensors[0].get_device()
-    for t in tensors:
+    dev = first.get_device()
+    for t in rest:
         if t is not None and t.get_device() != dev:
-            raise CsaError(f"tensors on {t.device} and {tensors[0].device}")
+            raise CsaError(f"tensors on {t.device} and {first.device}")
     if dev < 0:
         raise CsaError("tensor is not on a CUDA device")
     if dev != torch.cuda.current_device():
@@ -372,19 +391,10 @@ def _device(*tensors) -> int:
     return dev
 
 
-def _at(t):
-    """Address of a contiguous tensor (None: 0)."""
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise CsaError("tensor is not contiguous")
-    return t.data_ptr()
-
-
 def _row_args(cache, rows, x, key, key_type, what):
     """Checked arguments of a row call: n, and address and row stride of x and key."""
-    if rows.dtype != torch.int64 or rows.dim() != 1:
-        raise CsaError(f"rows must be int64 [n], got {rows.dtype} {tuple(rows.shape)}")
+    if rows.dtype != torch.int64 or rows.dim() != 1 or not rows.is_contiguous():
+        raise CsaError(f"rows must be contiguous int64 [n], got {rows.dtype} {tuple(rows.shape)}")
     n = rows.shape[0]
     if x.dtype not in _DTYPES or (key is not None and key.dtype != key_type):
         raise CsaError(f"{what}: element type {x.dtype}, key {None if key is None else key.dtype}")
@@ -404,18 +414,18 @@ def cache_write(cache: Cache, rows, x, key=None, counters=None):
     rows [n] (int64, distinct; negative: skipped), and key [n][d_idx] (x's type)
     into their indexer keys if it is given."""
     n, xp, ld_x, kp, ld_k = _row_args(cache, rows, x, key, x.dtype, "cache_write")
-    dev = _device(cache.codes, rows, x, key, counters)
-    _call("csa2_cache_write", ctypes.byref(cache.struct()), _at(rows), n, xp, _DTYPES[x.dtype], ld_x,
-          kp, ld_k, _at(counters), torch._C._cuda_getCurrentRawStream(dev))
+    dev = _device(x, cache.codes, rows, key, counters)
+    _call("csa2_cache_write", cache.packed(), rows.data_ptr(), n, xp, _DTYPES[x.dtype], ld_x, kp, ld_k,
+          None if counters is None else counters.data_ptr(), _raw_stream(dev))
 
 
 def cache_read(cache: Cache, rows, x, key=None, counters=None):
     """Reads the cache rows rows [n] (int64; negative: skipped) into x [n][512] (fp32,
     bf16 or f16: exact) and, if given, their indexer keys into key [n][d_idx] fp32."""
     n, xp, ld_x, kp, ld_k = _row_args(cache, rows, x, key, torch.float32, "cache_read")
-    dev = _device(cache.codes, rows, x, key, counters)
-    _call("csa2_cache_read", ctypes.byref(cache.struct()), _at(rows), n, xp, _DTYPES[x.dtype], ld_x,
-          kp, ld_k, _at(counters), torch._C._cuda_getCurrentRawStream(dev))
+    dev = _device(x, cache.codes, rows, key, counters)
+    _call("csa2_cache_read", cache.packed(), rows.data_ptr(), n, xp, _DTYPES[x.dtype], ld_x, kp, ld_k,
+          None if counters is None else counters.data_ptr(), _raw_stream(dev))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -433,23 +443,32 @@ def dense_attn(cache: Cache, groups: Groups, q, out, lse=None, *, prev=None, sm_
     entries of the group's sequence, into out [nq][H][512] (fp32, bf16 or f16) and
     lse [nq][H]; prev = (out, lse) of an earlier partial result (fp32) is merged in.
     max_n bounds the entries of any group (default: the cache's rows)."""
-    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
-        raise CsaError(f"dense_attn: q {tuple(q.shape)}, out {tuple(out.shape)}")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D or out.shape != shape:
+        raise CsaError(f"dense_attn: q {tuple(shape)}, out {tuple(out.shape)}")
     if q.dtype not in (torch.bfloat16, torch.float16) or out.dtype not in _DTYPES:
         raise CsaError(f"dense_attn: q {q.dtype}, out {out.dtype}")
-    nq, H, _ = q.shape
-    po, pl = prev if prev is not None else (None, None)
-    if ((lse is not None and (lse.dtype != torch.float32 or lse.shape != (nq, H)))
-            or (po is not None and (po.dtype != torch.float32 or po.shape != q.shape))
-            or (pl is not None and (pl.dtype != torch.float32 or pl.shape != (nq, H)))):
-        raise CsaError(f"dense_attn: lse and prev must be fp32 [{nq}][{H}] and [{nq}][{H}][{D}]")
-    dev = _device(cache.codes, groups.seq, groups.off, groups.length, q, po, pl, out, lse, ws, counters)
+    nq, H, _ = shape
+    if not (q.is_contiguous() and out.is_contiguous()):
+        raise CsaError("dense_attn: tensor is not contiguous")
+    lp = po = pl = None
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.shape != (nq, H) or not lse.is_contiguous():
+            raise CsaError(f"dense_attn: lse must be contiguous fp32 [{nq}][{H}]")
+        lp = lse.data_ptr()
+    if prev is not None:
+        po, pl = prev
+        if (po.dtype != torch.float32 or pl.dtype != torch.float32 or po.shape != shape
+                or pl.shape != (nq, H) or not (po.is_contiguous() and pl.is_contiguous())):
+            raise CsaError(f"dense_attn: prev must be contiguous fp32 [{nq}][{H}][{D}] and [{nq}][{H}]")
+    dev = _device(q, cache.codes, groups.seq, groups.off, groups.length, po, pl, out, lse, ws, counters)
     max_n = cache.cap if max_n is None else int(max_n)
     if ws is None:
         ws = torch.empty(max(_dense_need(dev, groups.ng, nq, H, max_n), 256), dtype=torch.uint8, device=q.device)
-    _call("csa2_dense_attn", ctypes.byref(cache.struct()), ctypes.byref(groups.struct(nq)), max_n,
-          _at(q), _DTYPES[q.dtype], H, sm_scale, _at(po), _at(pl), _at(out), _DTYPES[out.dtype],
-          _at(lse), _at(ws), ws.numel(), _at(counters), torch._C._cuda_getCurrentRawStream(dev))
+    _call("csa2_dense_attn", cache.packed(), groups.packed(nq), max_n, q.data_ptr(), _DTYPES[q.dtype], H,
+          sm_scale, None if po is None else po.data_ptr(), None if pl is None else pl.data_ptr(),
+          out.data_ptr(), _DTYPES[out.dtype], lp, ws.data_ptr(), ws.numel(),
+          None if counters is None else counters.data_ptr(), _raw_stream(dev))
 
 
 class Layer:
