@@ -148,6 +148,9 @@ struct Work {
     }
 };
 
+constexpr int kMaxPieces = 96;                 // of a row tile: one more than the pairs at most, three per lane of a warp
+static_assert(kDensePairsMax < kMaxPieces && kMaxPieces == 96, "join's weights");
+
 // What a pair works on, found by one warp in one pass over the groups (two when
 // there are more than 32).
 struct Found {
@@ -921,7 +924,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) dense_join_kernel(DenseParams
 {
     __shared__ DenseBegin sTile[kDensePairsMax];
     __shared__ int sPair[kDensePairsMax], sItem[kDensePairsMax], sWarp[2][kJoinThreads / 32];
-    __shared__ float sW[4][kDensePairsMax];
+    __shared__ float sW[4][kMaxPieces];
     __shared__ float4 sO[kJoinThreads];
     __shared__ Joined sJ[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -995,20 +998,27 @@ __global__ void __launch_bounds__(kJoinThreads, 2) dense_join_kernel(DenseParams
             pv = *reinterpret_cast<const float4 *>(p.prev_out + row * CSA2_D + ch);
         __syncthreads();                              // (the last item's shared values are read)
         if (warp < 4 / parts && r0 + warp < d.rows) {
-            float m = -INFINITY, l = 0.f;
-            for (int i = lane; i < n_pieces; i += 32) m = fmaxf(m, p.part_ml[slot(i) * 2 * kRowsPair + r0 + warp]);
+            const float prev = p.prev_out != nullptr ? p.prev_lse[d.row0 + r0 + warp] : 0.f;
+            float m[3], l[3];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            for (int i = lane; i < n_pieces; i += 32) {
+            for (int k = 0; k < 3; ++k) {
+                const int i = lane + 32 * k;
                 const float *ml = p.part_ml + slot(i) * 2 * kRowsPair + r0 + warp;
-                const float wgt = ml[0] == -INFINITY ? 0.f : fast_exp2(ml[0] - m);
-                sW[warp][i] = wgt;
-                l = fmaf(ml[kRowsPair], wgt, l);
+                m[k] = i < n_pieces ? ml[0] : -INFINITY;
+                l[k] = i < n_pieces ? ml[kRowsPair] : 0.f;
+            }
+            float top = fmaxf(fmaxf(m[0], m[1]), m[2]), sum = 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const float wgt = m[k] == -INFINITY ? 0.f : fast_exp2(m[k] - top);
+                sW[warp][lane + 32 * k] = wgt;
+                sum = fmaf(l[k], wgt, sum);
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (lane == 0)
-                sJ[warp] = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[d.row0 + r0 + warp] : 0.f);
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) sJ[warp] = join_prev(top, sum, p.prev_out != nullptr, prev);
         }
         __syncthreads();
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);

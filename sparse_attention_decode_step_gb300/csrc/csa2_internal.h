@@ -124,7 +124,7 @@ cudaError_t launch_cache_read(const csa2_cache &c, const int64_t *rows, int64_t 
 constexpr int kDenseRows = 128;         // (query, head) rows of a tile, one pair of CTAs
 constexpr int kDenseEntries = 256;      // entries of a tile
 constexpr int kDenseSetup = 1;          // units of a row tile besides its entry tiles
-constexpr int kDensePairsMax = 512;     // pairs of CTAs of a launch
+constexpr int kDensePairsMax = 95;      // pairs of CTAs of a launch (one per two SMs, on up to 191)
 // Where a pair's run begins: the units [first, last) of the row tile's entries,
 // its rows, and the units of a run.  rows = 0: the pair has no work.
 struct DenseBegin { int64_t first, last, run; int row0, rows; };
