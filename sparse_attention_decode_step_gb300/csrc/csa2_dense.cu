@@ -151,8 +151,7 @@ struct Work {
 constexpr int kMaxPieces = 96;                 // of a row tile: one more than the pairs at most, three per lane of a warp
 static_assert(kDensePairsMax < kMaxPieces && kMaxPieces == 96, "join's weights");
 
-// What a pair works on, found by one warp in one pass over the groups (two when
-// there are more than 32).
+// What a pair works on.
 struct Found {
     Work w;
     int64_t run;         // units of a pair's run
@@ -161,60 +160,66 @@ struct Found {
     int empty;           // some group has rows but no entries
 };
 
-__device__ __forceinline__ void find(const DenseParams &p, int pair, int lane, bool count_bad, Found *out)
+// Found by the whole CTA: thread t < 512 takes ceil(ng / 512) groups, whose units
+// are summed over the warps (totals in `sums`, kFindWarps of them); the thread that
+// holds unit u0 sets up the work.  Up to 32 groups are one warp's alone (0.7 us
+// less than with the others waiting for it).  Ends without a barrier.
+constexpr int kFindWarps = 16;
+
+__device__ __forceinline__ void find(const DenseParams &p, int pair, int tid, bool count_bad, int64_t *sums, Found *out)
 {
+    const int lane = tid & 31, warp = tid >> 5;
+    const bool few = p.ng <= 32;
+    if (few && warp != 0) return;
+    const int each = (p.ng + 32 * kFindWarps - 1) / (32 * kFindWarps);
+    const int g0 = warp < kFindWarps ? min(tid * each, p.ng) : p.ng, g1 = min(g0 + each, p.ng);
     Group gr{};
-    int64_t total = 0, upto = 0;
+    int64_t mine = 0;
     int empty = 0;
-    auto scan = [&](int64_t mine) {            // inclusive sums over the warp
-        upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-    };
-    for (int g0 = 0; g0 < p.ng; g0 += 32) {
-        gr = Group{};
-        if (g0 + lane < p.ng) {
-            gr = group_of(p, g0 + lane);
-            if (gr.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
-            if (!gr.bad && gr.n == 0 && gr.rows > 0) empty = 1;
-        }
-        scan(units(gr));
-        total += __shfl_sync(0xffffffffu, upto, 31);
+    for (int g = g0; g < g1; ++g) {
+        gr = group_of(p, g);
+        if (gr.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
+        if (!gr.bad && gr.n == 0 && gr.rows > 0) empty = 1;
+        mine += units(gr);
     }
-    empty = __any_sync(0xffffffffu, empty);
-    const int64_t run = run_units(p, total), u0 = min(pair * run, total), u1 = min(u0 + run, total);
-    if (lane == 0) {
+    int64_t upto = mine;                       // inclusive sum over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    int64_t before = upto - mine, total = 0;
+    if (few) {
+        empty = __any_sync(0xffffffffu, empty);
+        total = __shfl_sync(0xffffffffu, upto, 31);
+    } else {
+        if (lane == 31 && warp < kFindWarps) sums[warp] = upto;
+        empty = __syncthreads_or(empty);
+#pragma unroll
+        for (int i = 0; i < kFindWarps; ++i) {
+            const int64_t v = sums[i];
+            if (i < warp) before += v;
+            total += v;
+        }
+    }
+    const int64_t run = run_units(p, total), u0 = min(pair * run, total), left = min(run, total - u0);
+    if (left > 0 ? u0 >= before && u0 < before + mine : tid == 0) {
         out->run = run;
         out->u0 = u0;
-        out->work = 0;
         out->empty = empty;
-    }
-    __syncwarp();
-    if (u0 >= u1) return;
-    int64_t before = 0;
-    for (int g0 = 0; g0 < p.ng; g0 += 32) {
-        if (p.ng > 32) {
-            gr = Group{};
-            if (g0 + lane < p.ng) gr = group_of(p, g0 + lane);
-            scan(units(gr));
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, before + upto > u0);
-        if (hit != 0u) {
-            if (lane == __ffs(hit) - 1) {
-                const int64_t in_group = u0 - (before + upto - units(gr));
-                Work &w = out->w;
-                w.gr = gr;
-                w.g = g0 + lane;
-                w.rt = (int)quotient(in_group, row_units(gr));
-                w.at = (int)(in_group - (int64_t)w.rt * row_units(gr));
-                out->work = w.take(w.at, u1 - u0);
+        out->work = 0;
+        if (left > 0) {
+            int g = g0;
+            if (each > 1) {
+                for (gr = group_of(p, g); u0 >= before + units(gr); gr = group_of(p, ++g)) before += units(gr);
             }
-            return;
+            Work &w = out->w;
+            w.gr = gr;
+            w.g = g;
+            w.rt = (int)quotient(u0 - before, row_units(gr));
+            w.at = (int)(u0 - before - (int64_t)w.rt * row_units(gr));
+            out->work = w.take(w.at, left);
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
     }
 }
 
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_wait();
     pdl_trigger();
-    if (warp == 1) find(p, pair, lane, blockIdx.x == 0, sFound);
+    find(p, pair, tid, blockIdx.x == 0, reinterpret_cast<int64_t *>(sRing), sFound);
     tc_fence_before();
     __syncthreads();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -164,7 +164,7 @@ def _reference(v, q, sm, prev):
     w = torch.exp(pl - lse[:, None]).nan_to_num(0.0)
     po = torch.where(w > 0, prev[0].double(), 0.0) if prev is not None else torch.zeros(q.shape, dtype=torch.float64, device=DEV)
     out = p @ v + w * po
-    d = 32 * 2.0 ** -23 * sm * (q.abs() @ v.abs().T) + 2.0 ** -25 * sm * v.abs().sum(1) + 2.0 ** -21
+    d = 32 * 2.0 ** -23 * abs(sm) * (q.abs() @ v.abs().T) + 2.0 ** -25 * abs(sm) * v.abs().sum(1) + 2.0 ** -21
     dmax = d.amax(1, keepdim=True) if n else torch.zeros(q.shape[0], 1, dtype=torch.float64, device=DEV)
     sums = n / 16 * 2.0 ** -23 + 2 * 152 * 2.0 ** -24 + 2.0 ** -20
     a = p @ v.abs() + (w * po.abs())
@@ -227,6 +227,8 @@ CASES = [
     (64, [(40, 1500)]),
     (16, [(100, 640), (1, 640)]),
     (8, [(1, 100)] * 45),
+    (4, [(1, 30 + i % 7) for i in range(700)]),
+    (2, [(i % 3, (i * 37) % 300) for i in range(1100)]),
 ]
 
 
@@ -264,6 +266,17 @@ def test_dense_rescales_when_the_maximum_moves_late(nq):
     csa.dense_attn(cache, csa.Groups([0], [0, nq]), q, out, lse, sm_scale=0.7)
     torch.cuda.synchronize()
     _check(cache, [0], [0, nq], [n], q, out, lse, sm=0.7)
+
+
+@pytest.mark.parametrize("sm", [-0.5, 0.0])
+def test_dense_scale_may_be_negative_or_zero(sm):
+    lens = [300, 2000]
+    cache = _random_cache(lens, 35)
+    q = _queries(4, 32, torch.bfloat16, 36, 0.3)
+    out, lse = torch.zeros(4, 32, 512, device=DEV), torch.zeros(4, 32, device=DEV)
+    csa.dense_attn(cache, csa.Groups([0, 1], [0, 1, 4]), q, out, lse, sm_scale=sm)
+    torch.cuda.synchronize()
+    _check(cache, [0, 1], [0, 1, 4], lens, q, out, lse, sm=sm)
 
 
 def test_dense_lengths_padding_and_groups_out_of_contract():
