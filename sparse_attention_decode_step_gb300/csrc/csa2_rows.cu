@@ -9,39 +9,47 @@
 // bf16 and f16 alike; key = E4M3 byte x scale in fp32.
 //
 // Both are bound by memory traffic: a row is 1 KB of bf16 against 288 B of
-// cache.  One warp per row.  A write's lane takes one 16-channel group, so that a
+// cache.  A warp takes a whole row.  A write's lane takes one 16-channel group, so that a
 // scale is found once; a read's lane takes channels 8 l .. 8 l + 7 and 256 + 8 l ..,
 // so that its stores are contiguous.  With seven comparisons per value (the
 // append's form) the write of bf16 rows was bound by its instructions, at 50 us
 // for 65,536 rows; see fp4_codes16.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "csa2_attn_device.cuh"
 #include "csa2_internal.h"
 
 namespace csa2 {
 
-// N consecutive elements (a multiple of 16 bytes, 16-byte aligned; or 2 .. 4
-// elements aligned to their size together) as fp32
-template <int N, typename T>
-__device__ __forceinline__ void load_as_f32(const T *src, float (&x)[N])
+// A call has at most 2^31 rows of strides below 2^31: 32-bit counts, so that an
+// address is one wide multiplication.
+constexpr int kRowThreads = 256;
+
+// kWords consecutive words (4 k of them 16-byte aligned, 2 or 1 aligned to their size)
+template <int kWords>
+__device__ __forceinline__ void load_words(const void *src, uint32_t (&w)[kWords])
 {
-    constexpr int kBytes = N * (int)sizeof(T);
-    constexpr int kWords = kBytes / 4;
-    static_assert(kBytes % 16 == 0 || kBytes == 8 || kBytes == 4, "whole words");
-    uint32_t w[kWords];
-    if constexpr (kBytes >= 16) {
+    if constexpr (kWords >= 4) {
 #pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+        for (int i = 0; i < kWords / 4; ++i) {
+            const uint4 v = __ldg(static_cast<const uint4 *>(src) + i);
             w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         }
-    } else if constexpr (kBytes == 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+    } else if constexpr (kWords == 2) {
+        const uint2 v = __ldg(static_cast<const uint2 *>(src));
         w[0] = v.x; w[1] = v.y;
     } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+        w[0] = __ldg(static_cast<const uint32_t *>(src));
     }
+}
+
+// words of T elements as fp32
+template <typename T, int kWords, int N>
+__device__ __forceinline__ void words_as_f32(const uint32_t (&w)[kWords], float (&x)[N])
+{
+    static_assert(N * sizeof(T) == kWords * 4, "whole words");
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
         if constexpr (__is_same(T, float)) {
@@ -114,71 +122,90 @@ __device__ __forceinline__ uint2 fp4_codes16(const float (&x)[16], float s)
     return make_uint2(w[0], w[1]);
 }
 
+// A warp goes from row to row, the next row's loads on their way while this one is
+// encoded (65,536 bf16 rows: 21.4 us with a row per warp, 19.1 so with at most ten
+// blocks per SM, five at a time).
+constexpr int kWriteBlocks = 10;
+
 template <typename T>
-__global__ void __launch_bounds__(256) cache_write_kernel(csa2_cache cache, const int64_t *__restrict__ rows,
-                                                          int64_t n, const T *__restrict__ x, int64_t ld_x,
-                                                          const T *__restrict__ key, int64_t ld_key,
+__global__ void __launch_bounds__(kRowThreads, 5) cache_write_kernel(csa2_cache cache, const int64_t *__restrict__ rows,
+                                                          uint32_t n, const T *__restrict__ x, uint32_t ld_x,
+                                                          const T *__restrict__ key, uint32_t ld_key,
                                                           uint32_t *counters)
 {
     pdl_wait();
     pdl_trigger();
-    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    constexpr int kX = 16 * sizeof(T) / 4, kK = sizeof(T);          // words of a lane's latents, of up to 4 key components
+    const uint32_t step = gridDim.x * (kRowThreads / 32);
     const int lane = threadIdx.x & 31;
-    if (i >= n) return;
-    const int64_t row = __ldg(rows + i);
-    float v[16], k[4] = {0.f, 0.f, 0.f, 0.f};
-    load_as_f32<16>(x + i * ld_x + 16 * lane, v);
-    if (key != nullptr) {
-        if (cache.d_idx == 128) {
-            load_as_f32<4>(key + i * ld_key + 4 * lane, k);
-        } else {
-            float k2[2];
-            load_as_f32<2>(key + i * ld_key + 2 * lane, k2);
-            k[0] = k2[0]; k[1] = k2[1];
-        }
-    }
-    if (row < 0) return;                          // padding
-    if (row >= cache.cap) {
-        if (lane == 0) count_event(counters, CSA2_CNT_BAD_INPUT);
-        return;
-    }
-    float amax = 0.f;
+    uint32_t next = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    uint32_t xw[kX], kw[kK] = {};
+    int64_t next_row = -1;
+    auto load = [&]() {
+        next_row = __ldg(rows + next);
+        load_words(x + (uint64_t)next * ld_x + 16 * lane, xw);
+        if (key != nullptr) {
+            if (cache.d_idx == 128) {
+                load_words(key + (uint64_t)next * ld_key + 4 * lane, kw);
+            } else {
+                uint32_t half[kK / 2];
+                load_words(key + (uint64_t)next * ld_key + 2 * lane, half);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) amax = fmaxf(amax, fabsf(v[c]));
-    uint32_t sb = 0;
-    uint2 codes = make_uint2(0u, 0u);
-    if (amax > 0.f) {
-        if (amax > 2688.f) count_event(counters, CSA2_CNT_FP4_SATURATED);
-        float s;
-        sb = fp4_scale_near(amax, &s);
-        if constexpr (sizeof(T) == 2) {
-            codes = fp4_codes16(v, s);
-        } else {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                codes.x |= fp4_code(v[c], s) << (4 * c);
-                codes.y |= fp4_code(v[8 + c], s) << (4 * c);
+                for (int c = 0; c < kK; ++c) kw[c] = c < kK / 2 ? half[c] : 0u;
             }
         }
-    }
-    *reinterpret_cast<uint2 *>(cache.codes + row * CSA2_CODE_BYTES + 8 * lane) = codes;
-    cache.scales[row * CSA2_SCALE_BYTES + lane] = (uint8_t)sb;
-    if (key == nullptr) return;
-    float a = fmaxf(fmaxf(fabsf(k[0]), fabsf(k[1])), fmaxf(fabsf(k[2]), fabsf(k[3])));
+    };
+    if (next < n) load();
+    while (next < n) {
+        const int64_t row = next_row;
+        float v[16], k[4];
+        words_as_f32<T>(xw, v);
+        words_as_f32<T>(kw, k);
+        next += step;
+        if (next < n) load();
+        if (row < 0) continue;                    // padding
+        if (row >= cache.cap) {
+            if (lane == 0) count_event(counters, CSA2_CNT_BAD_INPUT);
+            continue;
+        }
+        float amax = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float s = fp8_pow2_scale(a);
-    // 1 / s by its exponent: s = 2^e with -126 <= e <= 120, so k / s is k times a power of two
-    const float r = __uint_as_float((254u << 23) - __float_as_uint(s));
-    uint32_t w = e4m3x2_near(k[0] * r, k[1] * r) | (e4m3x2_near(k[2] * r, k[3] * r) << 16);
-    // a negative value that rounds to zero is byte 0
-    const uint32_t mag = w & 0x7F7F7F7Fu;
-    w = mag | (w & ((mag + 0x7F7F7F7Fu) & 0x80808080u));
-    if (cache.d_idx == 128)
-        *reinterpret_cast<uint32_t *>(cache.kidx + row * 128 + lane * 4) = w;
-    else
-        *reinterpret_cast<uint16_t *>(cache.kidx + row * 64 + lane * 2) = (uint16_t)w;
-    if (lane == 0) cache.kscale[row] = s;
+        for (int c = 0; c < 16; ++c) amax = fmaxf(amax, fabsf(v[c]));
+        uint32_t sb = 0;
+        uint2 codes = make_uint2(0u, 0u);
+        if (amax > 0.f) {
+            if (amax > 2688.f) count_event(counters, CSA2_CNT_FP4_SATURATED);
+            float s;
+            sb = fp4_scale_near(amax, &s);
+            if constexpr (sizeof(T) == 2) {
+                codes = fp4_codes16(v, s);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    codes.x |= fp4_code(v[c], s) << (4 * c);
+                    codes.y |= fp4_code(v[8 + c], s) << (4 * c);
+                }
+            }
+        }
+        *reinterpret_cast<uint2 *>(cache.codes + row * CSA2_CODE_BYTES + 8 * lane) = codes;
+        cache.scales[row * CSA2_SCALE_BYTES + lane] = (uint8_t)sb;
+        if (key == nullptr) continue;
+        float a = fmaxf(fmaxf(fabsf(k[0]), fabsf(k[1])), fmaxf(fabsf(k[2]), fabsf(k[3])));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        const float s = fp8_pow2_scale(a);
+        // 1 / s by its exponent: s = 2^e with -126 <= e <= 120, so k / s is k times a power of two
+        const float r = __uint_as_float((254u << 23) - __float_as_uint(s));
+        uint32_t w = e4m3x2_near(k[0] * r, k[1] * r) | (e4m3x2_near(k[2] * r, k[3] * r) << 16);
+        // a negative value that rounds to zero is byte 0
+        const uint32_t mag = w & 0x7F7F7F7Fu;
+        w = mag | (w & ((mag + 0x7F7F7F7Fu) & 0x80808080u));
+        if (cache.d_idx == 128)
+            *reinterpret_cast<uint32_t *>(cache.kidx + row * 128 + lane * 4) = w;
+        else
+            *reinterpret_cast<uint16_t *>(cache.kidx + row * 64 + lane * 2) = (uint16_t)w;
+        if (lane == 0) cache.kscale[row] = s;
+    }
 }
 
 // 8 values (4 x f16x2, exact) stored as T, 16-byte aligned
@@ -212,13 +239,13 @@ constexpr int kReadRows = 2;
 
 template <typename T>
 __global__ void __launch_bounds__(256) cache_read_kernel(csa2_cache cache, const int64_t *__restrict__ rows,
-                                                         int64_t n, T *__restrict__ x, int64_t ld_x,
-                                                         float *__restrict__ key, int64_t ld_key,
+                                                         uint32_t n, T *__restrict__ x, uint32_t ld_x,
+                                                         float *__restrict__ key, uint32_t ld_key,
                                                          uint32_t *counters)
 {
     pdl_wait();
     pdl_trigger();
-    const int64_t i0 = (((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5) * kReadRows;
+    const uint32_t i0 = (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kReadRows;
     const int lane = threadIdx.x & 31;
     const int per = cache.d_idx / 32;
     int64_t row[kReadRows];
@@ -248,15 +275,15 @@ __global__ void __launch_bounds__(256) cache_read_kernel(csa2_cache cache, const
 #pragma unroll
     for (int j = 0; j < kReadRows; ++j) {
         if (row[j] < 0) continue;
-        const int64_t i = i0 + j;
+        const uint32_t i = i0 + j;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            store8(x + i * ld_x + 256 * h + 8 * lane, fp4x8_to_f16(w[j][h], scale_pair(sc[j][h])));
+            store8(x + (uint64_t)i * ld_x + 256 * h + 8 * lane, fp4x8_to_f16(w[j][h], scale_pair(sc[j][h])));
         if (key == nullptr) continue;
         const uint32_t lo = e4m3x2_to_f16x2(kb[j] & 0xFFFFu), hi = e4m3x2_to_f16x2(kb[j] >> 16);
         const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
         const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-        float *dst = key + i * ld_key + per * lane;
+        float *dst = key + (uint64_t)i * ld_key + per * lane;
         const float s = ks[j];
         if (per == 4)
             __stcs(reinterpret_cast<float4 *>(dst), make_float4(f0.x * s, f0.y * s, f1.x * s, f1.y * s));
@@ -264,8 +291,6 @@ __global__ void __launch_bounds__(256) cache_read_kernel(csa2_cache cache, const
             __stcs(reinterpret_cast<float2 *>(dst), make_float2(f0.x * s, f0.y * s));
     }
 }
-
-constexpr int kRowThreads = 256;
 
 // blocks for n rows, `per` to a warp
 static unsigned row_blocks(int64_t n, int per)
@@ -280,8 +305,9 @@ cudaError_t launch_cache_write(const csa2_cache &c, const int64_t *rows, int64_t
 {
     auto go = [&](auto tag) {
         using T = decltype(tag);
-        return launch_k(cache_write_kernel<T>, dim3(row_blocks(n, 1)), dim3(kRowThreads), 0, st, 0, c, rows, n,
-                        static_cast<const T *>(x), ld_x, static_cast<const T *>(key), ld_key, counters);
+        return launch_k(cache_write_kernel<T>, dim3(std::min(row_blocks(n, 1), (unsigned)(device_sm_count() * kWriteBlocks))), dim3(kRowThreads), 0, st, 0, c, rows, (uint32_t)n,
+                        static_cast<const T *>(x), (uint32_t)ld_x, static_cast<const T *>(key), (uint32_t)ld_key,
+                        counters);
     };
     const cudaError_t e = x_type == CSA2_F32 ? go(float{}) : x_type == CSA2_BF16 ? go(__nv_bfloat16{}) : go(__half{});
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -292,8 +318,8 @@ cudaError_t launch_cache_read(const csa2_cache &c, const int64_t *rows, int64_t 
 {
     auto go = [&](auto tag) {
         using T = decltype(tag);
-        return launch_k(cache_read_kernel<T>, dim3(row_blocks(n, kReadRows)), dim3(kRowThreads), 0, st, 0, c, rows, n,
-                        static_cast<T *>(x), ld_x, key, ld_key, counters);
+        return launch_k(cache_read_kernel<T>, dim3(row_blocks(n, kReadRows)), dim3(kRowThreads), 0, st, 0, c, rows, (uint32_t)n,
+                        static_cast<T *>(x), (uint32_t)ld_x, key, (uint32_t)ld_key, counters);
     };
     const cudaError_t e = x_type == CSA2_F32 ? go(float{}) : x_type == CSA2_BF16 ? go(__nv_bfloat16{}) : go(__half{});
     return e != cudaSuccess ? e : cudaGetLastError();
