@@ -12,14 +12,14 @@
 //     S [128 rows x 256 entries]  = Q [128 x 512] . K^T          (M 128, N 256)
 //     O [128 rows x 512 channels] += P [128 x 256] . V           (M 128, 2 x N 256)
 // An SM then holds 64 rows' O (256 TMEM columns) and two S buffers (2 x 128),
-// and an MMA of N = 256 reads 6 KB of shared memory for 64 cycles of products
+// and an MMA reads 6 KB of its shared memory for 64 cycles of products
 // (measured: 4,056 MAC per cycle and SM; M = 128 entries x N = 64 rows, the
-// layout of the sparse attention, reads 6 KB for 32 cycles' worth and runs at
-// 2,705).  Each CTA dequantises its half of both operands (E2M1 x E4M3 is exact
-// in f16): as K, its 128 entries x all channels; as V, all 256 entries x its 256
-// channels.  The f16 operands never fit at once, so they pass through a ring of
-// eight 16 KB slots, each feeding four MMAs: a K slot is 128 entries x 64
-// channels (K-major), a V slot 32 entries x 256 channels (MN-major).
+// layout of the sparse attention, also reads 6 KB, for 32 cycles of products,
+// and runs at 2,705).  Each CTA dequantises its half of both operands (E2M1 x
+// E4M3 is exact in f16): as K, its 128 entries x all channels; as V, all 256
+// entries x its 256 channels.  Beside Q (64 KB) and P (32 KB) there is room for
+// 128 KB of them: a ring of two 64 KB stages, each 128 entries x 256 channels and
+// 16 MMAs, read as K-major K or as MN-major V.
 //
 // Warps of a CTA: 0..7 softmax (two per TMEM lane quarter), 8..15 producers, 16
 // issues the MMAs (the first CTA of the pair only).  S is double buffered: the
@@ -29,11 +29,19 @@
 // row moves whenever a logit exceeds it by 8 in log2 units, and O is then
 // rescaled in TMEM).
 //
-// Work is counted in tiles of 128 rows x 256 entries over all groups, and each
-// pair takes an equal run of them whatever the groups' sizes.  A pair whose
-// run begins or ends inside a row tile leaves that tile's sums in the
-// workspace (at most two such pieces per pair); a second kernel joins the
-// pieces in a fixed order, so results do not depend on timing.
+// Work is counted over all groups, and each pair takes an equal run of it
+// whatever the groups' sizes.  A pair whose run begins or ends inside a row tile
+// leaves that tile's sums in the workspace (at most two such pieces per pair); a
+// second kernel joins the pieces in a fixed order, so results do not depend on
+// timing.
+//
+// Measured: 32 queries x 64 heads over 65,536 entries (275 GFLOP) in 192 us,
+// 1,430 TFLOP/s.  What bounds a long run is the port that serves shared memory
+// and L1: per tile and SM the MMAs' operands take 3,072 of its cycles (384 KB),
+// the stores of the dequantised operands 2,048, the loads of codes 1,080 and P
+// 256, together 6,456; a tile takes about 6,700, the MMAs alone 4,134.  What
+// bounds a short run is the chain of a piece (first scores, softmax, O,
+// epilogue: about 8 us with a single tile) and the join (4 to 6 us).
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -242,7 +250,7 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t saddr, uint32_t rank)
 // this CTA's own shared memory or TMEM and read by this SM's tensor core (the
 // proxy fence before it orders that), so CTA scope is enough; at cluster scope
 // the release waits for the warp's outstanding loads and an acquire drops L1
-// (measured 1,900 cycles per ring slot against 300).
+// (with 16 KB stages, 823 us instead of 404 at 32 x 64 heads x 65,536 entries).
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr)
 {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
@@ -496,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         // The whole warp runs the loop and one elected lane issues: descriptors and
         // waits then stay in uniform registers.  (Measured for a wait, four MMAs and
         // a commit: 258 cycles, the MMAs' own time; with a branch on lane 0 around
-        // the loop 404 to 483.)
+        // the loop 404 to 483.)  The loop over stages stays rolled, or its
+        // descriptors are kept in registers and spilled.
         if (rank == 0) {
             uint32_t elected;
             asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(elected));
@@ -579,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         // scales), four per lane of the eight warps.  Eight lanes read one entry's
         // 128 code bytes, a whole line: the L1 port serves these loads, the stores
         // into the ring and the tensor core's operand reads alike, and is what the
-        // kernel runs out of first (with 64 or 32 bytes of an entry per eight lanes
-        // the loads took 95 us of 298 at 32 x 64 heads x 65,536 entries).  Those eight
+        // kernel runs out of first (with 64 or 32 bytes of an entry per eight lanes it
+        // took 298 and 323 us at 32 x 64 heads x 65,536 entries, so 248).  Those eight
         // lanes write their four 16-byte pieces each in an order turned by 0 .. 3, so
         // that they hit eight bank groups at every store.  Codes are loaded a whole
         // ring (two stages) ahead.
