@@ -158,6 +158,7 @@ struct Work {
 
 constexpr int kMaxPieces = 96;                 // of a row tile: one more than the pairs at most, three per lane of a warp
 static_assert(kDensePairsMax < kMaxPieces && kMaxPieces == 96, "join's weights");
+static_assert(kJoinThreads == 512 && CSA2_D == 4 * 128, "join's shifts");
 
 // What a pair works on.
 struct Found {
@@ -936,8 +937,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 template <int kOut>
 __global__ void __launch_bounds__(kJoinThreads, 2) dense_join_kernel(DenseParams p)
 {
-    __shared__ DenseBegin sTile[kDensePairsMax];
-    __shared__ int sPair[kDensePairsMax], sItem[kDensePairsMax], sWarp[2][kJoinThreads / 32];
+    struct Tile { int c, pieces, row0, rows, item; };
+    __shared__ Tile sTile[kDensePairsMax];
+    __shared__ int sWarp[2][kJoinThreads / 32];
     __shared__ float sW[4][kMaxPieces];
     __shared__ float4 sO[kJoinThreads];
     __shared__ Joined sJ[4];
@@ -947,17 +949,20 @@ __global__ void __launch_bounds__(kJoinThreads, 2) dense_join_kernel(DenseParams
     // keep the SM from the blocks it waits for)
     pdl_wait();
     // the tiles to join (in order) and their work items; every thread looks at one pair
-    auto pieces_of = [&](int c, const DenseBegin &d) {     // pair c - 1's, and those of the pairs that begin before d.last
-        return (int)quotient(d.last + d.run - 1, d.run) - c + 1;
-    };
-    auto parts_of = [](int n_pieces) { return n_pieces <= 4 ? 1 : n_pieces <= 8 ? 2 : 4; };
+    auto log_parts = [](int pieces) { return pieces <= 4 ? 0 : pieces <= 8 ? 1 : 2; };
+    Tile mine{};
     int items = 0;
-    DenseBegin mine{};
     if (tid > 0 && tid < p.pairs) {
-        mine = p.begin[tid];
-        const int64_t b0 = tid * mine.run;
-        if (mine.rows > 0 && b0 > mine.first && b0 - mine.run <= mine.first)
-            items = (mine.rows * (CSA2_D / 4) * parts_of(pieces_of(tid, mine)) + kJoinThreads - 1) / kJoinThreads;
+        const DenseBegin d = p.begin[tid];
+        const int64_t b0 = tid * d.run;
+        if (d.rows > 0 && b0 > d.first && b0 - d.run <= d.first) {
+            // pair tid - 1's piece, and one of each pair that begins before d.last
+            mine.c = tid;
+            mine.pieces = (int)quotient(d.last + d.run - 1, d.run) - tid + 1;
+            mine.row0 = d.row0;
+            mine.rows = d.rows;
+            items = ((d.rows << log_parts(mine.pieces)) + 3) >> 2;         // 4 / parts rows each
+        }
     }
     const uint32_t has = __ballot_sync(0xffffffffu, items > 0);
     int upto = items;
@@ -970,56 +975,52 @@ __global__ void __launch_bounds__(kJoinThreads, 2) dense_join_kernel(DenseParams
     __syncthreads();
     int before = 0, n = 0, total = 0, tiles = 0;
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) {
+    for (int i = 0; i < (kDensePairsMax + 31) / 32; ++i) {
         const int a = sWarp[0][i], b = sWarp[1][i];
         if (i < warp) { before += a; n += b; }
         total += a;
         tiles += b;
     }
     if (items > 0) {
-        const int at = n + __popc(has & ((1u << lane) - 1));
-        sPair[at] = tid;
-        sItem[at] = before + upto - items;
-        sTile[at] = mine;
+        mine.item = before + upto - items;
+        sTile[n + __popc(has & ((1u << lane) - 1))] = mine;
     }
     __syncthreads();
     int at = 0;
     for (int item = blockIdx.x; item < total; item += gridDim.x) {
-        while (at + 1 < tiles && sItem[at + 1] <= item) ++at;
-        const int c = sPair[at];
-        const DenseBegin &d = sTile[at];
-        const int n_pieces = pieces_of(c, d), parts = parts_of(n_pieces);
-        const int wide = kJoinThreads / parts;            // threads (of 4 channels) side by side
-        const int part = tid / wide;
-        const int cell = (item - sItem[at]) * wide + tid % wide;
-        const int r = cell / (CSA2_D / 4), ch = 4 * (cell % (CSA2_D / 4));
-        const int r0 = (item - sItem[at]) * wide / (CSA2_D / 4);    // the item's rows: r0 .. r0 + 4 / parts - 1
-        const bool in = r < d.rows;
-        const int64_t row = d.row0 + r;
-        auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c - 1 + i); };
-        const float *src = p.part_o + (int64_t)r * CSA2_D + ch;
+        while (at + 1 < tiles && sTile[at + 1].item <= item) ++at;
+        const Tile t = sTile[at];
+        const int lp = log_parts(t.pieces), parts = 1 << lp;
+        const int part = tid >> (9 - lp);             // of the 512 >> lp threads (of 4 channels) side by side
+        const int r0 = (item - t.item) << (2 - lp);   // the item's rows: r0 .. r0 + 4 / parts - 1
+        const int r = r0 + ((tid & ((512 >> lp) - 1)) >> 7), ch = 4 * (tid & 127);
+        const bool in = r < t.rows;
+        const int64_t out_at = (int64_t)(t.row0 + r) * CSA2_D + ch;
+        // piece i's slot: 2 (c - 1) + 1 for the first, 2 (c - 1 + i) for the others
+        const uint32_t slot0 = 2u * (t.c - 1);
+        auto slot = [&](int i) { return slot0 + (i == 0 ? 1u : 2u * i); };
+        const float *src = p.part_o + r * CSA2_D + ch;
         auto load = [&](int i) {
-            return in && i < n_pieces ? *reinterpret_cast<const float4 *>(src + slot(i) * kRowsPair * CSA2_D)
+            return in && i < t.pieces ? *reinterpret_cast<const float4 *>(src + slot(i) * (uint32_t)(kRowsPair * CSA2_D))
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
         };
         // the first pieces and the caller's part are on their way before the weights
         // are known (without a partial result prev_out may hold anything: weight 0)
         float4 v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = load(part + k * parts);
+        for (int k = 0; k < 4; ++k) v[k] = load(part + (k << lp));
         float4 pv = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.prev_out != nullptr && part == 0 && in)
-            pv = *reinterpret_cast<const float4 *>(p.prev_out + row * CSA2_D + ch);
+        if (p.prev_out != nullptr && part == 0 && in) pv = *reinterpret_cast<const float4 *>(p.prev_out + out_at);
         __syncthreads();                              // (the last item's shared values are read)
-        if (warp < 4 / parts && r0 + warp < d.rows) {
-            const float prev = p.prev_out != nullptr ? p.prev_lse[d.row0 + r0 + warp] : 0.f;
+        if (warp < (4 >> lp) && r0 + warp < t.rows) {
+            const float prev = p.prev_out != nullptr ? p.prev_lse[t.row0 + r0 + warp] : 0.f;
             float m[3], l[3];
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
                 const int i = lane + 32 * k;
-                const float *ml = p.part_ml + slot(i) * 2 * kRowsPair + r0 + warp;
-                m[k] = i < n_pieces ? ml[0] : -INFINITY;
-                l[k] = i < n_pieces ? ml[kRowsPair] : 0.f;
+                const float *ml = p.part_ml + slot(i) * (2u * kRowsPair) + r0 + warp;
+                m[k] = i < t.pieces ? ml[0] : -INFINITY;
+                l[k] = i < t.pieces ? ml[kRowsPair] : 0.f;
             }
             float top = fmaxf(fmaxf(m[0], m[1]), m[2]), sum = 0.f;
 #pragma unroll
@@ -1036,35 +1037,36 @@ __global__ void __launch_bounds__(kJoinThreads, 2) dense_join_kernel(DenseParams
         }
         __syncthreads();
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = part; i0 < n_pieces; i0 += 4 * parts) {
+        const float *const w = sW[r - r0];
+        for (int i0 = part; i0 < t.pieces; i0 += 4 << lp) {
             if (i0 != part) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = load(i0 + k * parts);
+                for (int k = 0; k < 4; ++k) v[k] = load(i0 + (k << lp));
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int i = i0 + k * parts;
-                const float wgt = in && i < n_pieces ? sW[r - r0][i] : 0.f;
+                const int i = i0 + (k << lp);
+                const float wgt = i < t.pieces ? w[i] : 0.f;
                 o.x = fmaf(v[k].x, wgt, o.x); o.y = fmaf(v[k].y, wgt, o.y);
                 o.z = fmaf(v[k].z, wgt, o.z); o.w = fmaf(v[k].w, wgt, o.w);
             }
         }
-        if (parts > 1) {
+        if (lp > 0) {
             sO[tid] = o;
             __syncthreads();
             if (part == 0)
                 for (int i = 1; i < parts; ++i) {
-                    const float4 u = sO[i * wide + tid];
+                    const float4 u = sO[(i << (9 - lp)) + tid];
                     o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
                 }
         }
         if (part == 0 && in) {
             const Joined j = sJ[r - r0];
             if (j.prev == 0.f) pv = make_float4(0.f, 0.f, 0.f, 0.f);
-            store4<kOut>(p.out, row * CSA2_D + ch, fmaf(pv.x, j.prev, o.x * j.own), fmaf(pv.y, j.prev, o.y * j.own),
+            store4<kOut>(p.out, out_at, fmaf(pv.x, j.prev, o.x * j.own), fmaf(pv.y, j.prev, o.y * j.own),
                          fmaf(pv.z, j.prev, o.z * j.own), fmaf(pv.w, j.prev, o.w * j.own));
         }
-        if (p.lse && tid < 4 / parts && r0 + tid < d.rows) p.lse[d.row0 + r0 + tid] = sJ[tid].lse;
+        if (p.lse && tid < (4 >> lp) && r0 + tid < t.rows) p.lse[t.row0 + r0 + tid] = sJ[tid].lse;
     }
 }
 
