@@ -349,8 +349,8 @@ csa2_status csa2_cache_read(const csa2_cache *cache, const int64_t *rows, int64_
  *   x_j = sm_scale * q[i][h] . v_j,  L = sum_j e^(x_j) + e^(prev_lse[i][h]),
  *   lse[i][h] = log L,
  * without the prev terms when prev_out is NULL or prev_lse[i][h] is -inf (its
- * prev_out is then not read).  With nothing to attend to (n_g = 0 and no prev)
- * out is 0 and lse -inf.  Rows of no group are left as they were.
+ * prev_out may then hold anything).  With nothing to attend to (n_g = 0 and no
+ * prev) out is 0 and lse -inf.  Rows of no group are left as they were.
  *   seq [ng], off [ng+1] ascending in [0, nq], len [ng]: a group outside the
  *   contract (sequence, offsets, n_g < 0, above seq_len or above max_n) is
  *   skipped and counted in CSA2_CNT_BAD_INPUT, its rows left as they were;

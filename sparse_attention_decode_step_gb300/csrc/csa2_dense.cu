@@ -35,8 +35,8 @@
 // second kernel joins the pieces in a fixed order, so results do not depend on
 // timing.
 //
-// Measured: 32 queries x 64 heads over 65,536 entries (275 GFLOP) in 192 us,
-// 1,430 TFLOP/s.  What bounds a long run is the port that serves shared memory
+// Measured: 32 queries x 64 heads over 65,536 entries (275 GFLOP) in 190 us,
+// 1,447 TFLOP/s.  What bounds a long run is the port that serves shared memory
 // and L1: per tile and SM the MMAs' operands take 3,072 of its cycles (384 KB),
 // the stores of the dequantised operands 2,048, the loads of codes 1,080 and P
 // 256, together 6,456; a tile takes about 6,700, the MMAs alone 4,134.  What
