@@ -8,9 +8,9 @@ device memory and the current CUDA stream.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 
 import torch
@@ -21,7 +21,6 @@ FULL, REINDEX, REUSE = 0, 1, 2
 D = 512
 CNT_FP4_SATURATED, CNT_CAPACITY, CNT_BAD_INPUT, CNT_TIMEOUT = 0, 1, 2, 3
 NUM_COUNTERS = 4
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 _lock = threading.Lock()
 _lib = None
@@ -177,35 +176,12 @@ class Cache:
         codes [cap][256], scales [cap][32], kidx [cap][d_idx] uint8, kscale [cap]
         fp32, seq_base [batch + 1] int64, seq_len [batch] int32, cap a multiple of 8.
         kidx and kscale may be None for a cache that is only attended."""
-        cap = codes.shape[0]
-        u8 = torch.uint8
-        keys = kidx is not None
-        if (codes.dtype != u8 or scales.dtype != u8 or (keys and kidx.dtype != u8)
-                or (kscale is not None and kscale.dtype != torch.float32)
-                or seq_base.dtype != torch.int64 or seq_len.dtype != torch.int32):
-            raise CsaError("cache tensors: codes, scales, kidx uint8, kscale fp32, seq_base int64, seq_len int32")
-        if not (codes.is_contiguous() and scales.is_contiguous() and seq_base.is_contiguous()
-                and seq_len.is_contiguous() and (not keys or kidx.is_contiguous())
-                and (kscale is None or kscale.is_contiguous())):
-            raise CsaError("cache tensors must be contiguous")
-        if (codes.shape != (cap, 256) or scales.shape != (cap, 32) or keys != (kscale is not None)
-                or (keys and (kidx.dim() != 2 or kidx.shape[0] != cap or kscale.numel() != cap))
-                or seq_base.numel() != seq_len.numel() + 1):
-            raise CsaError("cache tensors do not fit together")
-        d_idx = kidx.shape[1] if keys else 128
         c = cls.__new__(cls)
-        c.batch, c.cap, c.d_idx, c.m = seq_len.numel(), cap, d_idx, m
+        c.cap, c.batch, c.d_idx = (_ext or _load_ext()).check_cache(codes, scales, kidx, kscale, seq_base, seq_len)
+        c.m = m
         c.codes, c.scales, c.kidx, c.kscale = codes, scales, kidx, kscale
         c.seq_base, c.seq_len, c.base_host = seq_base, seq_len, None
         return c
-
-    def packed(self) -> bytes:
-        """The bytes of struct()."""
-        keys = self.kidx is not None
-        return _CACHE_FMT.pack(self.codes.data_ptr(), self.scales.data_ptr(),
-                               self.kidx.data_ptr() if keys else 0, self.kscale.data_ptr() if keys else 0,
-                               self.seq_base.data_ptr(), self.seq_len.data_ptr(), self.cap, self.batch,
-                               self.d_idx, self.m)
 
     def struct(self, seq=None) -> _Cache:
         """The C struct; with seq = b, a one-sequence view of sequence b."""
@@ -244,11 +220,6 @@ class Groups:
         self.ng = self.seq.numel()
         if self.off.numel() != self.ng + 1 or (length is not None and self.length.numel() != self.ng):
             raise CsaError("groups need seq [ng], off [ng + 1] and length [ng]")
-
-    def packed(self, nq: int) -> bytes:
-        """The bytes of struct()."""
-        return _GROUPS_FMT.pack(self.seq.data_ptr(), self.off.data_ptr(),
-                                0 if self.length is None else self.length.data_ptr(), self.ng, nq)
 
     def struct(self, nq: int) -> _Groups:
         return _Groups(self.seq.data_ptr(), self.off.data_ptr(),
@@ -359,78 +330,37 @@ def sparse_attn(cache: Cache, qs: Queries, idx, cnt, q, win, n_win, out, lse=Non
                                   _ptr(counters), _stream()), "csa2_sparse_attn")
 
 
-# The calls below are short on the GPU, so their marshalling is kept short too:
-# functions are looked up once, pointers go as integers, the C structures as
-# packed bytes (checked against the ctypes ones by the tests), the stream as its
-# handle.
-_fn = {}
-_CACHE_FMT = struct.Struct("6Pq3i4x")      # csa2_cache
-_GROUPS_FMT = struct.Struct("3P2i")        # csa2_groups
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The calls below are short on the GPU, so their tensors are checked and taken
+# apart in compiled code (csrc/csa2_torch.cpp) instead of here.
+_ext = None
 
 
-def _call(name, *args):
-    f = _fn.get(name)
-    if f is None:
-        f = _fn[name] = getattr(lib(), name)
-    status = f(*args)
-    if status != 0:
-        _check(status, name)
-
-
-def _device(first, *rest) -> int:
-    """The current device, which all tensors must be on: a call runs on its stream."""
-    dev = first.get_device()
-    for t in rest:
-        if t is not None and t.get_device() != dev:
-            raise CsaError(f"tensors on {t.device} and {first.device}")
-    if dev < 0:
-        raise CsaError("tensor is not on a CUDA device")
-    if dev != torch.cuda.current_device():
-        raise CsaError(f"tensors on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _row_args(cache, rows, x, key, key_type, what):
-    """Checked arguments of a row call: n, and address and row stride of x and key."""
-    if rows.dtype != torch.int64 or rows.dim() != 1 or not rows.is_contiguous():
-        raise CsaError(f"rows must be contiguous int64 [n], got {rows.dtype} {tuple(rows.shape)}")
-    n = rows.shape[0]
-    if x.dtype not in _DTYPES or (key is not None and key.dtype != key_type):
-        raise CsaError(f"{what}: element type {x.dtype}, key {None if key is None else key.dtype}")
-    if x.shape != (n, D) or x.stride(1) != 1:
-        raise CsaError(f"{what}: x must be [{n}][{D}] with contiguous rows, got {tuple(x.shape)}")
-    # (the stride of a single row says nothing)
-    ld_x = x.stride(0) if n > 1 else D
-    if key is None:
-        return n, x.data_ptr(), ld_x, None, 0
-    if key.shape != (n, cache.d_idx) or key.stride(1) != 1:
-        raise CsaError(f"{what}: key must be [{n}][{cache.d_idx}] with contiguous rows, got {tuple(key.shape)}")
-    return n, x.data_ptr(), ld_x, key.data_ptr(), key.stride(0) if n > 1 else cache.d_idx
+def _load_ext():
+    global _ext
+    lib()
+    with _lock:
+        if _ext is None:
+            if not os.path.exists(_build.EXT_PATH):
+                raise CsaError(f"compiled binding not found at {_build.EXT_PATH}")
+            loader = importlib.machinery.ExtensionFileLoader("csa2_torch", _build.EXT_PATH)
+            mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("csa2_torch", loader))
+            loader.exec_module(mod)
+            mod.set_error(CsaError)
+            _ext = mod
+    return _ext
 
 
 def cache_write(cache: Cache, rows, x, key=None, counters=None):
     """Quantises x [n][512] (fp32, bf16 or f16, any row stride) into the cache rows
     rows [n] (int64, distinct; negative: skipped), and key [n][d_idx] (x's type)
     into their indexer keys if it is given."""
-    n, xp, ld_x, kp, ld_k = _row_args(cache, rows, x, key, x.dtype, "cache_write")
-    dev = _device(x, cache.codes, rows, key, counters)
-    _call("csa2_cache_write", cache.packed(), rows.data_ptr(), n, xp, _DTYPES[x.dtype], ld_x, kp, ld_k,
-          None if counters is None else counters.data_ptr(), _raw_stream(dev))
+    (_ext or _load_ext()).cache_write(cache, rows, x, key, counters)
 
 
 def cache_read(cache: Cache, rows, x, key=None, counters=None):
     """Reads the cache rows rows [n] (int64; negative: skipped) into x [n][512] (fp32,
     bf16 or f16: exact) and, if given, their indexer keys into key [n][d_idx] fp32."""
-    n, xp, ld_x, kp, ld_k = _row_args(cache, rows, x, key, torch.float32, "cache_read")
-    dev = _device(x, cache.codes, rows, key, counters)
-    _call("csa2_cache_read", cache.packed(), rows.data_ptr(), n, xp, _DTYPES[x.dtype], ld_x, kp, ld_k,
-          None if counters is None else counters.data_ptr(), _raw_stream(dev))
-
-
-@functools.lru_cache(maxsize=4096)
-def _dense_need(dev, ng, nq, H, max_n) -> int:
-    return dense_workspace_size(ng, nq, H, max_n)
+    (_ext or _load_ext()).cache_read(cache, rows, x, key, counters)
 
 
 def dense_workspace_size(ng, nq, H, max_n) -> int:
@@ -443,32 +373,9 @@ def dense_attn(cache: Cache, groups: Groups, q, out, lse=None, *, prev=None, sm_
     entries of the group's sequence, into out [nq][H][512] (fp32, bf16 or f16) and
     lse [nq][H]; prev = (out, lse) of an earlier partial result (fp32) is merged in.
     max_n bounds the entries of any group (default: the cache's rows)."""
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != D or out.shape != shape:
-        raise CsaError(f"dense_attn: q {tuple(shape)}, out {tuple(out.shape)}")
-    if q.dtype not in (torch.bfloat16, torch.float16) or out.dtype not in _DTYPES:
-        raise CsaError(f"dense_attn: q {q.dtype}, out {out.dtype}")
-    nq, H, _ = shape
-    if not (q.is_contiguous() and out.is_contiguous()):
-        raise CsaError("dense_attn: tensor is not contiguous")
-    lp = po = pl = None
-    if lse is not None:
-        if lse.dtype != torch.float32 or lse.shape != (nq, H) or not lse.is_contiguous():
-            raise CsaError(f"dense_attn: lse must be contiguous fp32 [{nq}][{H}]")
-        lp = lse.data_ptr()
-    if prev is not None:
-        po, pl = prev
-        if (po.dtype != torch.float32 or pl.dtype != torch.float32 or po.shape != shape
-                or pl.shape != (nq, H) or not (po.is_contiguous() and pl.is_contiguous())):
-            raise CsaError(f"dense_attn: prev must be contiguous fp32 [{nq}][{H}][{D}] and [{nq}][{H}]")
-    dev = _device(q, cache.codes, groups.seq, groups.off, groups.length, po, pl, out, lse, ws, counters)
-    max_n = cache.cap if max_n is None else int(max_n)
-    if ws is None:
-        ws = torch.empty(max(_dense_need(dev, groups.ng, nq, H, max_n), 256), dtype=torch.uint8, device=q.device)
-    _call("csa2_dense_attn", cache.packed(), groups.packed(nq), max_n, q.data_ptr(), _DTYPES[q.dtype], H,
-          sm_scale, None if po is None else po.data_ptr(), None if pl is None else pl.data_ptr(),
-          out.data_ptr(), _DTYPES[out.dtype], lp, ws.data_ptr(), ws.numel(),
-          None if counters is None else counters.data_ptr(), _raw_stream(dev))
+    po, pl = prev if prev is not None else (None, None)
+    (_ext or _load_ext()).dense_attn(cache, groups.seq, groups.off, groups.length, q, out, lse, po, pl,
+                                     sm_scale, max_n, ws, counters)
 
 
 class Layer:

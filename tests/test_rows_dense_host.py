@@ -145,13 +145,8 @@ def test_cache_over_checks_its_tensors():
     d = csa.Cache.over(c.codes, c.scales, c.kidx, c.kscale, c.seq_base, c.seq_len, 2)
     assert (d.cap, d.batch, d.d_idx, d.m) == (24, 2, 64, 2)
     assert bytes(d.struct()) == bytes(c.struct())
-    for x in (c, d):
-        assert x.packed() == bytes(x.struct())
     bare = csa.Cache.over(c.codes, c.scales, None, None, c.seq_base, c.seq_len, 2)
-    assert bare.struct().kidx is None and bare.packed() == bytes(bare.struct())
-    for length in (None, [3, 4]):
-        g = csa.Groups([0, 1], [0, 2, 5], length, device="cpu")
-        assert g.packed(7) == bytes(g.struct(7))
+    assert bare.struct().kidx is None
     with pytest.raises(csa.CsaError):
         csa.Cache.over(c.codes, c.scales, c.kidx, None, c.seq_base, c.seq_len, 2)
     with pytest.raises(csa.CsaError):
