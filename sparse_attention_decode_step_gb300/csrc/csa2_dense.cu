@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         sFlag[0] = 0;
         fence_barrier_init();
     }
-    if (warp == 0) {
+    if (warp == kWarpsSoft + kWarpsProd) {     // (warp 0 is looking for its work)
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sTmem)), "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     tc_fence_after();
     const uint32_t tmem = *sTmem;
     Work w = sFound->w;
-    if (tid == 0 && rank == 0) {
+    if (tid == 32 * (kWarpsSoft + kWarpsProd) && rank == 0) {
         // for the join: the row tile that this pair begins in
         DenseBegin d{};
         if (sFound->work) {
@@ -930,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     // it; nothing is handed over in memory, so the arrival need not wait for the
     // stores on their way (release: 0.1 to 0.2 us more).
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-    if (warp == 0) {
+    if (warp == kWarpsSoft + kWarpsProd) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
