@@ -506,6 +506,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         p.begin[pair] = d;
     }
     bool more = sFound->work != 0;
+    // A row tile's rows are halved between the CTAs: the first of this one's, in the tile
+    auto row_split = [&](const Work &x) { return (int)rank * ((min(kRowsPair, x.gr.rows - x.rt * kRowsPair) + 1) >> 1); };
+    auto row_count = [&](const Work &x) {
+        const int n = min(kRowsPair, x.gr.rows - x.rt * kRowsPair);
+        return rank == 0 ? (n + 1) >> 1 : n >> 1;
+    };
 
     if (warp == kWarpsSoft + kWarpsProd) {
         // ============================================== MMA issuer
@@ -661,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             if (tiles > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, abort_flag));
                 if (!ok) break;
-                const int r0 = w.rt * kRowsPair + kRowsCta * (int)rank;
-                const int n_rows = max(0, min(kRowsCta, w.gr.rows - r0));
+                const int r0 = w.rt * kRowsPair + row_split(w);
+                const int n_rows = row_count(w);
                 issue_q(p, sQ, (int64_t)(w.gr.row0 + r0), n_rows, 32 * pw + lane);
                 load(1);
                 finish_q<0>(p, sQ, 32 * pw + lane, q_full);
@@ -718,8 +724,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         uint32_t tile = 0;
         bool ok = true;
         for (; more && ok; more = w.next(p)) {
-            const int r0 = w.rt * kRowsPair + kRowsCta * (int)rank;
-            const int n_rows = max(0, min(kRowsCta, w.gr.rows - r0));
+            const int r_tile = row_split(w);                     // of the tile's 128
+            const int r0 = w.rt * kRowsPair + r_tile;
+            const int n_rows = row_count(w);
             const int64_t row0 = w.gr.row0 + r0;
             if (tile == 0) {
                 issue_q(p, sQ, row0, n_rows, tid);
@@ -856,8 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 sRed[row] = j.prev;
                 if (whole) {
                     if (row < n_rows && p.lse) p.lse[row0 + row] = j.lse;
-                } else {
-                    float *ml = p.part_ml + piece * 2 * kRowsPair + kRowsCta * (int)rank + row;
+                } else if (row < n_rows) {
+                    float *ml = p.part_ml + piece * 2 * kRowsPair + r_tile + row;
                     ml[0] = m;
                     ml[kRowsPair] = l;
                 }
@@ -869,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             const int r_base = 32 * (quarter & 1) + (lane >> 3), c_lane = chan + 4 * (lane & 7);
             const int mine = (n_rows - r_base + 3) / 4;       // of this lane's 8 rows r_base + 4 i
             const int64_t out0 = (row0 + r_base) * CSA2_D + c_lane;
-            float *const part0 = p.part_o + (piece * kRowsPair + kRowsCta * (int)rank + r_base) * CSA2_D + c_lane;
+            float *const part0 = p.part_o + (piece * kRowsPair + r_tile + r_base) * CSA2_D + c_lane;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 float o[32];
