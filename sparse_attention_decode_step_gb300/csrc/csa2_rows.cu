@@ -10,13 +10,15 @@
 //
 // Both are bound by memory traffic: a row is 1 KB of bf16 against 288 B of
 // cache.  A warp takes a whole row.  A write's lane takes one 16-channel group, so that a
-// scale is found once; a read's lane takes channels 8 l .. 8 l + 7 and 256 + 8 l ..,
-// so that its stores are contiguous.  With seven comparisons per value (the
-// append's form) the write of bf16 rows was bound by its instructions, at 50 us
-// for 65,536 rows; see fp4_codes16.
+// scale is found once; a read's lane takes 16 bytes of every 512, so that a warp's
+// stores are contiguous (fp32 rows with 32 bytes a lane: 65,536 in 33.0 us instead
+// of 25.2).  With seven comparisons per value (the append's form) the write of bf16
+// rows was bound by its instructions, at 50 us for 65,536 rows, and that of fp32
+// rows at 38; see fp4_codes16.
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "csa2_attn_device.cuh"
 #include "csa2_internal.h"
@@ -86,14 +88,35 @@ __device__ __forceinline__ uint32_t fp4_scale_near(float amax, float *s)
     return b;
 }
 
-// E2M1 codes of 16 values that came from 16-bit floats, under scale s.  With the
-// hardware's reciprocal r of s (off by at most one step, 2^-23), x r is within
-// 2^-22 (relative) of x / s.  A 16-bit x has at most 11 significant
-// bits and a midpoint m s (m of .25, .75, 1.25, 1.75, 2.5, 3.5, 5) at most 7, so
-// x / s is either exactly m or at least 2^-11 away from it: rounding x r to 17
-// bits gives exactly m in the first case and stays on its side in the second,
-// and the hardware's round-to-nearest-even then decides as the exact quotient
-// would.  (fp32 values may lie within 2^-24 of a midpoint: they are compared.)
+// E2M1 codes (nearest even, saturating) of 8 values; one that rounds to zero has code 0
+__device__ __forceinline__ uint32_t e2m1x8_near(const float (&q)[8])
+{
+    uint32_t w;
+    asm("{\n"
+        ".reg .b8 b0, b1, b2, b3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        "mov.b32 %0, {b0, b1, b2, b3};\n"
+        "}\n"
+        : "=r"(w)
+        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+    const uint32_t mag = w & 0x77777777u;
+    return mag | (w & ((mag + 0x77777777u) & 0x88888888u));
+}
+
+// E2M1 codes of 16 values under scale s.  With the hardware's reciprocal r of s
+// (off by at most one step, 2^-23), x r is within 2^-22 (relative) of x / s.
+//  * 16-bit x (kSplit false): x has at most 11 significant bits and a midpoint m s (m
+//    of .25, .75, 1.25, 1.75, 2.5, 3.5, 5) at most 7, so x / s is either exactly m
+//    or at least 2^-11 away from it: rounding x r to 17 bits gives exactly m in
+//    the first case and stays on its side in the second, and the hardware's
+//    round-to-nearest-even then decides as the exact quotient would.
+//  * fp32 x: x / s lies between x r (1 - 2^-20) and x r (1 + 2^-20); where both have
+//    the same code it is that one's (rounding is monotonic), else (one value in
+//    some 2^17) the values are compared with the midpoints, which are exact.
+template <bool kSplit>
 __device__ __forceinline__ uint2 fp4_codes16(const float (&x)[16], float s)
 {
     float r;
@@ -102,33 +125,39 @@ __device__ __forceinline__ uint2 fp4_codes16(const float (&x)[16], float s)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float q[8];
+        if constexpr (kSplit) {
+            float t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            q[i] = __uint_as_float((__float_as_uint(x[8 * h + i] * r) + 0x40u) & ~0x7Fu);
-        asm("{\n"
-            ".reg .b8 b0, b1, b2, b3;\n"
-            "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
-            "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
-            "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
-            "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
-            "mov.b32 %0, {b0, b1, b2, b3};\n"
-            "}\n"
-            : "=r"(w[h])
-            : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
-        // a negative value that rounds to zero has code 0
-        const uint32_t mag = w[h] & 0x77777777u;
-        w[h] = mag | (w[h] & ((mag + 0x77777777u) & 0x88888888u));
+            for (int i = 0; i < 8; ++i) {
+                t[i] = x[8 * h + i] * r;
+                q[i] = t[i] * (1.0f - 0x1p-20f);
+                t[i] *= 1.0f + 0x1p-20f;
+            }
+            w[h] = e2m1x8_near(q);
+            if (w[h] != e2m1x8_near(t)) {
+                w[h] = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[h] |= fp4_code(x[8 * h + i], s) << (4 * i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q[i] = __uint_as_float((__float_as_uint(x[8 * h + i] * r) + 0x40u) & ~0x7Fu);
+            w[h] = e2m1x8_near(q);
+        }
     }
     return make_uint2(w[0], w[1]);
 }
 
 // A warp goes from row to row, the next row's loads on their way while this one is
-// encoded (65,536 bf16 rows: 21.4 us with a row per warp, 19.1 so with at most ten
-// blocks per SM, five at a time).
-constexpr int kWriteBlocks = 10;
+// encoded (65,536 bf16 rows: 21.4 us with a row per warp, 19.1 so).  fp32 rows hold
+// twice the words: four blocks to an SM with 64 registers a thread, not five with
+// 48 and spills (65,536 rows 32.5 -> 24.2 us).
+template <typename T>
+constexpr int kWriteResident = sizeof(T) == 4 ? 4 : 5;
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads, 5) cache_write_kernel(csa2_cache cache, const int64_t *__restrict__ rows,
+__global__ void __launch_bounds__(kRowThreads, kWriteResident<T>) cache_write_kernel(csa2_cache cache, const int64_t *__restrict__ rows,
                                                           uint32_t n, const T *__restrict__ x, uint32_t ld_x,
                                                           const T *__restrict__ key, uint32_t ld_key,
                                                           uint32_t *counters)
@@ -177,15 +206,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) cache_write_kernel(csa2_cache 
             if (amax > 2688.f) count_event(counters, CSA2_CNT_FP4_SATURATED);
             float s;
             sb = fp4_scale_near(amax, &s);
-            if constexpr (sizeof(T) == 2) {
-                codes = fp4_codes16(v, s);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    codes.x |= fp4_code(v[c], s) << (4 * c);
-                    codes.y |= fp4_code(v[8 + c], s) << (4 * c);
-                }
-            }
+            codes = fp4_codes16<sizeof(T) == 4>(v, s);
         }
         *reinterpret_cast<uint2 *>(cache.codes + row * CSA2_CODE_BYTES + 8 * lane) = codes;
         cache.scales[row * CSA2_SCALE_BYTES + lane] = (uint8_t)sb;
@@ -208,9 +229,9 @@ __global__ void __launch_bounds__(kRowThreads, 5) cache_write_kernel(csa2_cache 
     }
 }
 
-// 8 values (4 x f16x2, exact) stored as T, 16-byte aligned
+// 16 bytes of T, 16-byte aligned, from f16 values (exact): 8 of them, or for fp32 the first 4
 template <typename T>
-__device__ __forceinline__ void store8(T *dst, uint4 h)
+__device__ __forceinline__ void store16(T *dst, uint4 h)
 {
     if constexpr (__is_same(T, __half)) {
         __stcs(reinterpret_cast<uint4 *>(dst), h);
@@ -221,7 +242,6 @@ __device__ __forceinline__ void store8(T *dst, uint4 h)
         for (int j = 0; j < 4; ++j) f[j] = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
         if constexpr (__is_same(T, float)) {
             __stcs(reinterpret_cast<float4 *>(dst), make_float4(f[0].x, f[0].y, f[1].x, f[1].y));
-            __stcs(reinterpret_cast<float4 *>(dst) + 1, make_float4(f[2].x, f[2].y, f[3].x, f[3].y));
         } else {
             uint32_t o[4];
 #pragma unroll
@@ -248,8 +268,11 @@ __global__ void __launch_bounds__(256) cache_read_kernel(csa2_cache cache, const
     const uint32_t i0 = (blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kReadRows;
     const int lane = threadIdx.x & 31;
     const int per = cache.d_idx / 32;
+    // part h of a row: 32 lanes' 16 bytes, channels kE (32 h + lane) ..
+    constexpr int kE = 16 / sizeof(T), kParts = CSA2_D / (32 * kE);
+    using Codes = std::conditional_t<kE == 8, uint32_t, uint16_t>;
     int64_t row[kReadRows];
-    uint32_t w[kReadRows][2], sc[kReadRows][2], kb[kReadRows];
+    uint32_t w[kReadRows][kParts], sc[kReadRows][kParts], kb[kReadRows];
     float ks[kReadRows];
 #pragma unroll
     for (int j = 0; j < kReadRows; ++j) row[j] = i0 + j < n ? __ldg(rows + i0 + j) : -1;
@@ -261,9 +284,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(csa2_cache cache, const
         }
         if (row[j] >= 0) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                w[j][h] = __ldg(reinterpret_cast<const uint32_t *>(cache.codes + row[j] * CSA2_CODE_BYTES + 128 * h + 4 * lane));
-                sc[j][h] = __ldg(cache.scales + row[j] * CSA2_SCALE_BYTES + 16 * h + (lane >> 1));
+            for (int h = 0; h < kParts; ++h) {
+                w[j][h] = __ldg(reinterpret_cast<const Codes *>(cache.codes + row[j] * CSA2_CODE_BYTES) + 32 * h + lane);
+                sc[j][h] = __ldg(cache.scales + row[j] * CSA2_SCALE_BYTES + 2 * kE * h + lane * kE / 16);
             }
             if (key != nullptr) {
                 ks[j] = __ldg(cache.kscale + row[j]);
@@ -277,8 +300,8 @@ __global__ void __launch_bounds__(256) cache_read_kernel(csa2_cache cache, const
         if (row[j] < 0) continue;
         const uint32_t i = i0 + j;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            store8(x + (uint64_t)i * ld_x + 256 * h + 8 * lane, fp4x8_to_f16(w[j][h], scale_pair(sc[j][h])));
+        for (int h = 0; h < kParts; ++h)
+            store16(x + (uint64_t)i * ld_x + kE * (32 * h + lane), fp4x8_to_f16(w[j][h], scale_pair(sc[j][h])));
         if (key == nullptr) continue;
         const uint32_t lo = e4m3x2_to_f16x2(kb[j] & 0xFFFFu), hi = e4m3x2_to_f16x2(kb[j] >> 16);
         const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
@@ -305,7 +328,9 @@ cudaError_t launch_cache_write(const csa2_cache &c, const int64_t *rows, int64_t
 {
     auto go = [&](auto tag) {
         using T = decltype(tag);
-        return launch_k(cache_write_kernel<T>, dim3(std::min(row_blocks(n, 1), (unsigned)(device_sm_count() * kWriteBlocks))), dim3(kRowThreads), 0, st, 0, c, rows, (uint32_t)n,
+        // (twice the resident blocks: 65,536 bf16 rows with keys in 19.3 us, once: 19.7)
+        const unsigned blocks = std::min(row_blocks(n, 1), (unsigned)(device_sm_count() * 2 * kWriteResident<T>));
+        return launch_k(cache_write_kernel<T>, dim3(blocks), dim3(kRowThreads), 0, st, 0, c, rows, (uint32_t)n,
                         static_cast<const T *>(x), (uint32_t)ld_x, static_cast<const T *>(key), (uint32_t)ld_key,
                         counters);
     };
