@@ -485,7 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     // (the other CTA's barriers are used only once it has arrived here)
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_wait();
-    pdl_trigger();
     find(p, pair, tid, blockIdx.x == 0, reinterpret_cast<int64_t *>(sRing), sFound);
     tc_fence_before();
     __syncthreads();
@@ -807,8 +806,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 // P is free once the previous tile's products have completed
                 if (tile > 0 && !mbar_wait<true>(bar_o, (tile - 1) & 1, abort_flag)) raise_abort(sFlag);
                 const float mref = m == -INFINITY ? 0.f : m;    // (no finite logit yet: e^-inf = 0, a NaN stays one)
+                // (a warp whose 32 rows are all past the tile's leaves their P as it is: no row's O
+                // depends on another's P)
+                const int halves = 32 * (quarter & 1) < n_rows ? 2 : 0;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    if (h >= halves) break;
                     float x[32];
                     tmem_ld32(tS + 32 * h, x);
                     tmem_wait_ld();
@@ -877,8 +880,9 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             const int mine = (n_rows - r_base + 3) / 4;       // of this lane's 8 rows r_base + 4 i
             const int64_t out0 = (row0 + r_base) * CSA2_D + c_lane;
             float *const part0 = p.part_o + (piece * kRowsPair + r_tile + r_base) * CSA2_D + c_lane;
+            const int chunks = 32 * (quarter & 1) < n_rows ? 4 : 0;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < chunks; ++c) {
                 float o[32];
                 tmem_ld32(tmem + 128 * ch + 32 * c + lane_q, o);
                 tmem_wait_ld();
@@ -920,6 +924,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             tc_fence_before();
             soft_sync();                       // sRed, sM and O are read
         }
+        // (the join is let in this late because its blocks fill whichever SMs end first, and
+        // its first blocks would wait there two to an SM: 22.8 us instead of 21.8 for
+        // 61 queries over five prompts when let in before the epilogue)
+        pdl_trigger();
         if (!ok && lane == 0) raise_abort(sFlag);
     }
     // groups without entries
