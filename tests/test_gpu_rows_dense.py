@@ -132,27 +132,29 @@ def test_read_repeats_rows_and_infinities_saturate():
     assert (got == got[0]).all() and got[0, 0] == 2688 and got[0, 16] == -2688 and got[0, 17] == 0
 
 
-def _midpoints():
-    """fp32 rows: every scale's midpoints, and their neighbours some steps of 2^-24 away."""
+def _midpoints(t):
+    """Every scale's midpoints, and their neighbours some of the type's steps away."""
     s = torch.arange(1, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()       # 126 scales
     m = torch.tensor([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0])
-    bits = (s[:, None] * m).view(torch.int32)[:, :, None]                                # exact in fp32
-    steps = torch.tensor([-40, -17, -9, -8, -7, -4, -2, -1, 0, 1, 2, 4, 7, 8, 9, 17, 40], dtype=torch.int32)
-    v = (bits + steps).view(torch.float32).reshape(126, -1)                              # 119 a scale
+    whole = torch.int32 if t == torch.float32 else torch.int16
+    far = [-40, -17, -9, -8, -7, -4, -2, -1, 0, 1, 2, 4, 7, 8, 9, 17, 40] if t == torch.float32 else range(-8, 9)
+    bits = (s[:, None] * m).to(t).view(whole)[:, :, None]                                # exact in t
+    v = (bits + torch.tensor(list(far), dtype=whole)).view(t).float().reshape(126, -1)   # 119 a scale
     v = torch.cat([v, -v, torch.zeros(126, 2)], 1).reshape(126, 16, 15)                  # 16 groups of 15 ..
     x = torch.cat([(6 * s)[:, None, None].expand(126, 16, 1), v], 2)                     # .. and the scale's 6 s
-    return x.reshape(63, 512)
+    return x.reshape(63, 512).to(t)
 
 
-def test_write_fp32_next_to_the_midpoints():
-    x = _midpoints()
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_write_next_to_the_midpoints(t):
+    x = _midpoints(TYPES[t])
     n = x.shape[0]
     cache = csa.Cache([64], 64, 1, DEV)
     csa.cache_write(cache, torch.arange(n, device=DEV), x.to(DEV))
     torch.cuda.synchronize()
     codes, scales, _k, _s = _oracle_rows(x, None)
     assert np.array_equal(_np(cache.scales)[:n], scales) and np.array_equal(_np(cache.codes)[:n], codes)
-    assert np.array_equal(scales.reshape(126, 16)[:, 0], np.arange(1, 127))
+    assert np.array_equal(scales.reshape(126, 16), np.repeat(np.arange(1, 127)[:, None], 16, 1))
 
 
 # ================================================================ dense attention
