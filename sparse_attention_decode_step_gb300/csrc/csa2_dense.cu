@@ -35,13 +35,14 @@
 // second kernel joins the pieces in a fixed order, so results do not depend on
 // timing.
 //
-// Measured: 32 queries x 64 heads over 65,536 entries (275 GFLOP) in 190 us,
-// 1,447 TFLOP/s.  What bounds a long run is the port that serves shared memory
+// Measured: 32 queries x 64 heads over 65,536 entries (275 GFLOP) in 184 us,
+// 1,494 TFLOP/s.  What bounds a long run is the port that serves shared memory
 // and L1: per tile and SM the MMAs' operands take 3,072 of its cycles (384 KB),
 // the stores of the dequantised operands 2,048, the loads of codes 1,080 and P
-// 256, together 6,456; a tile takes about 6,700, the MMAs alone 4,134.  What
-// bounds a short run is the chain of a piece (first scores, softmax, O,
-// epilogue: about 8 us with a single tile) and the join (4 to 6 us).
+// 256, together 6,456; a tile takes about 6,500, the MMAs alone 4,134.  What
+// bounds a short run is the chain of a piece, in cycles with a single tile: work
+// found 4,700, first scores 5,900, softmax 3,400, O 2,700, epilogue 3,000 to 4,000;
+// and the join (about 4 us).
 #include <cuda_fp16.h>
 
 #include <atomic>
