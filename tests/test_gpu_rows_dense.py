@@ -10,6 +10,8 @@ Dense attention: the bound of each output is summed from its roundings --
   the sum over n entries: n / 16 fp32 additions, 2^-23 each, and the joining of
   at most 152 parts (2^-24 each, twice);
   the output type: half a step of what is stored."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -402,6 +404,86 @@ def test_dense_is_reproducible_on_streams_and_in_graphs():
         csa.dense_attn(cache, groups, q, outs[0], lses[0])
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want)
+
+
+def test_calls_from_two_threads():
+    # each thread with its stream and the call's own workspace, many calls in flight
+    cache = _random_cache([3000, 70], 81)
+    groups = csa.Groups([0, 1], [0, 3, 4])
+    q = _queries(4, 33, torch.float16, 82)
+    want = torch.zeros(4, 33, 512, device=DEV)
+    csa.dense_attn(cache, groups, q, want)
+    rows = torch.arange(3000, device=DEV)
+    values = torch.zeros(3000, 512, dtype=torch.bfloat16, device=DEV)
+    csa.cache_read(cache, rows, values)
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                o, v = torch.zeros_like(want), torch.zeros_like(values)
+                for _ in range(40):
+                    o.zero_()
+                    csa.dense_attn(cache, groups, q, o)
+                    csa.cache_read(cache, rows, v)
+                torch.cuda.current_stream().synchronize()
+                got[k] = (o, v)
+        except Exception as e:                   # (an assertion in a thread would go unseen)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for k in range(2):
+        assert torch.equal(got[k][0], want) and torch.equal(got[k][1], values)
+
+
+def test_refusals_with_tensors_on_the_device():
+    cache = _random_cache([64], 91)
+    g = csa.Groups([0], [0, 2])
+    q = _queries(2, 4, torch.bfloat16, 92)
+    out, lse = torch.full((2, 4, 512), 5.0, device=DEV), torch.full((2, 4), 5.0, device=DEV)
+    prev = (torch.zeros(2, 4, 512, device=DEV), torch.zeros(2, 4, device=DEV))
+    cnt = csa.new_counters()
+
+    def refused(f, *args, **kw):
+        with pytest.raises(csa.CsaError):
+            f(*args, **kw)
+
+    dense = lambda **kw: (lambda a: csa.dense_attn(cache, a.pop("groups"), a.pop("q"), a.pop("out"), a.pop("lse"), **a))(
+        dict(dict(groups=g, q=q, out=out, lse=lse, counters=cnt), **kw))
+    for bad in (dict(q=None), dict(q=q.cpu()), dict(q=q.float()), dict(q=q[..., :256]), dict(q=q.transpose(0, 1)),
+                dict(q=q[0]), dict(out=None), dict(out=out.cpu()), dict(out=out.double()), dict(out=out[:1]),
+                dict(out=out.transpose(0, 1).contiguous().transpose(0, 1)),
+                dict(lse=lse.cpu()), dict(lse=lse.half()), dict(lse=lse[:1]), dict(prev=(prev[0], None)),
+                dict(prev=(prev[0].half(), prev[1])), dict(prev=(prev[0], prev[1][:1])), dict(prev=(prev[0].cpu(), prev[1])),
+                dict(groups=csa.Groups([0], [0, 2], device="cpu")), dict(max_n=-1), dict(max_n=1 << 31),
+                dict(ws=csa.workspace(256)), dict(ws=csa.workspace(1 << 22)[1:]), dict(counters=cnt.cpu()),
+                dict(counters=cnt.float()), dict(counters=cnt[:3])):
+        refused(dense, **bad)
+    rows = torch.tensor([3, 1], device=DEV)
+    x, key = torch.full((2, 512), 5.0, device=DEV), torch.full((2, 64), 5.0, device=DEV)
+    bare = csa.Cache.over(cache.codes, cache.scales, None, None, cache.seq_base, cache.seq_len, 1)
+    for f in (csa.cache_write, csa.cache_read):
+        for bad in ((None, x), ([3, 1], x), (rows.cpu(), x), (rows.int(), x), (rows[:1], x), (rows[:, None], x), (rows, None),
+                    (rows, x.cpu()), (rows, x.double()), (rows, x[:, :256]), (rows, x.t().contiguous().t()),
+                    (rows, torch.zeros(2, 514, device=DEV)[:, 1:513]), (rows, x, key.cpu()), (rows, x, key[:, :32]),
+                    (rows, x, key.double()), (rows, x, None, cnt.float()), (rows, x, None, cnt.cpu())):
+            refused(f, cache, *bad)
+        refused(f, bare, rows, x, torch.zeros(2, 128, device=DEV))
+        refused(f, csa.Cache([8], 128, 1, "cpu"), rows, x)
+    torch.cuda.synchronize()
+    assert (out == 5).all() and (lse == 5).all() and (x == 5).all() and not cnt.any()
+    dense()                                      # and the call itself still works
+    csa.cache_read(bare, rows, x, counters=cnt)
+    torch.cuda.synchronize()
+    assert (out != 5).all() and not cnt.any()
+    assert np.array_equal(_np(x.double()), _values(cache, 0, 64)[[3, 1]].numpy())
 
 
 def test_rows_and_dense_past_32_bit_offsets():
