@@ -360,8 +360,10 @@ csa2_status csa2_cache_read(const csa2_cache *cache, const int64_t *rows, int64_
  *   lse [nq][H] or NULL (may be prev_lse itself);
  *   max_n: host bound on every n_g; it sets how a group's entries are divided.
  * Arithmetic as in csa2_sparse_attn: exact f16 latents, q as f16 (bf16: exact
- * for magnitudes in [2^-14, 65504]), softmax weights rounded to f16 (relative
- * 2^-11), every sum in fp32; results do not depend on the run (fixed order).
+ * for magnitudes in [2^-14, 65504]), softmax weights rounded to f16 (off by 2^-11
+ * of themselves, or by 2^-32 of the row's largest where that is more), every sum in
+ * fp32; results do not depend on the run (fixed order).  Each level of shared
+ * prompts rounds its own weights once.
  * Group arrays: 4-byte aligned; q, prev_out, out, workspace: 16-byte. */
 typedef struct {
     const int32_t *seq;        /* [ng] */

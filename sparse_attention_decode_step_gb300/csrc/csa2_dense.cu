@@ -25,9 +25,12 @@
 // issues the MMAs (the first CTA of the pair only).  S is double buffered: the
 // product of tile i + 1's scores runs while tile i's softmax does, so the order on
 // the tensor pipe is S(0) S(1) O(0) S(2) O(1) ...  All sums are fp32; P is
-// rounded to f16 (relative 2^-11; at most 2^8, since the reference maximum of a
-// row moves whenever a logit exceeds it by 8 in log2 units, and O is then
-// rescaled in TMEM).
+// rounded to f16.  A row's reference lies 7 below a maximum already seen (log2
+// units) and moves whenever a logit exceeds it by 15, O being rescaled in TMEM then:
+// P is at most 2^15, the row's largest weight so far at least 2^7, and a weight is off
+// by 2^-11 of itself or, below f16's normals, by 2^-25, which is 2^-32 of that largest
+// one (with the reference at the maximum it was 2^-25, and what lay below it, such as
+// 65,535 entries at 2^-26 of one, was lost from out but not from the sum).
 //
 // Work is counted over all groups, and each pair takes an equal run of it
 // whatever the groups' sizes.  A pair whose run begins or ends inside a row tile
@@ -70,6 +73,7 @@ constexpr uint32_t kColS = 256;                // TMEM: O in columns 0 .. 255, S
 constexpr int kJoinThreads = 512;
 constexpr int kSetup = kDenseSetup;
 constexpr float kLazy = 8.0f;                  // log2 units
+constexpr float kHead = 7.0f;                  // log2 units that a reference lies below its maximum
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 static_assert(kRowsPair == 128 && kEnt == 256, "lane and column maps below");
@@ -360,8 +364,8 @@ __device__ __forceinline__ void store4(void *out, int64_t at, float a, float b, 
     }
 }
 
-// A row's softmax (m in log2 units, l) joined with the caller's partial
-// result: the weights of the two, and the joint lse.
+// A row's softmax (its reference m in log2 units and l = sum 2^(x - m)) joined with
+// the caller's partial result: the weights of the two, and the joint lse.
 struct Joined { float own, prev, lse; };
 
 __device__ __forceinline__ Joined join_prev(float m, float l, bool any_prev, float prev_lse)
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     uint8_t *sQ = sRing + kStages * kStage;
     uint8_t *sP = sQ + kQBytes;
     float *sRed = reinterpret_cast<float *>(sP + kPBytes);   // [4 threads of a row][64 rows]
-    float *sM = sRed + 4 * kRowsCta;           // reference max per row (log2 units)
+    float *sM = sRed + 4 * kRowsCta;           // reference per row: kHead below a maximum (log2 units)
     float *sAlpha = sM + kRowsCta;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sAlpha + kRowsCta);
     uint64_t *bar_full = bars;                 // [2] (first CTA's) stage filled by both CTAs
@@ -764,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                         for (int c = 0; c < 32; ++c) hi = fmaxf(hi, -x[c]);
                     }
                 }
-                const float top = hi == -INFINITY ? hi : hi * fabsf(l2s);
+                const float top = hi == -INFINITY ? hi : fmaf(hi, fabsf(l2s), -kHead);
                 // (a wait that gave up takes the same path, and the vote makes every thread
                 // leave together)
                 if (soft_any(top > m + kLazy || !got)) {

@@ -373,6 +373,46 @@ def test_dense_nan_query_stays_in_its_row():
         assert torch.equal(out, want)
 
 
+def test_dense_keeps_a_long_tail_below_one_large_entry():
+    """One entry holds nearly all of a row's weight, 65,535 others 2^-24.3 to 2^-27.3 of it
+    each, and every pair of CTAs runs through the whole sequence, so that the reference
+    maximum is that entry's all along: the tail's weights must not vanish or be rounded
+    one way.  The bound is the module's, but with 2^-32 of the row's largest weight for
+    weights below f16's normals (half a step of 2^-24, and the largest is at least 2^7)."""
+    n, h = 65536, 64
+    nq = max(1, torch.cuda.get_device_properties(0).multi_processor_count // 2) * 128 // h
+    cache = _random_cache([n], 101)
+    g = torch.Generator().manual_seed(102)
+    # tail: channels 0 .. 15 zero, the others positive (codes 1 .. 7, scale 1); entry 0: 24 in channel 0 alone
+    codes = torch.randint(1, 8, (n, 512), generator=g, dtype=torch.uint8)
+    codes[:, :16] = 0
+    codes[0] = 0
+    codes[0, 0] = 7
+    cache.codes[:n].copy_(codes[:, 0::2] | (codes[:, 1::2] << 4))
+    scales = torch.full((n, 32), 0x38, dtype=torch.uint8)
+    scales[0] = 0x48                                          # 4
+    cache.scales[:n].copy_(scales)
+    deep = torch.tensor([24.3, 25.6, 26.6, 27.3]).repeat(h // 4)
+    q = torch.zeros(nq, h, 512)
+    q[:, :, 0] = deep * float(np.log(2)) / 24
+    q = q.to(torch.bfloat16).to(DEV)
+    out, lse = torch.zeros(nq, h, 512, device=DEV), torch.zeros(nq, h, device=DEV)
+    csa.dense_attn(cache, csa.Groups([0], [0, nq]), q, out, lse)
+    torch.cuda.synchronize()
+    v = _values(cache, 0, n).to(DEV)
+    assert v[0, 0] == 24 and not v[0, 1:].any() and not v[1:, :16].any() and (v[1:, 16:] > 0).all()
+    x = q[0].double() @ v.T                                   # (every query is the same)
+    lref = torch.logsumexp(x, 1)
+    p = torch.exp(x - lref[:, None])
+    want = p @ v
+    dmax = (32 * 2.0 ** -23 * (q[0].double().abs() @ v.abs().T) + 2.0 ** -21).amax(1, keepdim=True)
+    sums = n / 16 * 2.0 ** -23 + 2 * 152 * 2.0 ** -24 + 2.0 ** -20
+    bound = (2 * dmax + 2.0 ** -11 + 2 * sums) * want + 2.0 ** -32 * p.amax(1, keepdim=True) * v.sum(0)
+    far = (out.double() - want).abs() - bound - _storage(want, torch.float32)
+    assert far.max() <= 0, (far.amax((0, 2)).tolist()[:4], (out[0, :4, 16:].double().sum(1) / want[:4, 16:].sum(1)).tolist())
+    assert ((lse.double() - lref).abs() - dmax[:, 0] - sums - 2.0 ** -22 * (lref.abs() + 1)).max() <= 0
+
+
 def test_dense_is_reproducible_on_streams_and_in_graphs():
     cache = _random_cache([5000, 900], 71)
     groups = csa.Groups([0, 1], [0, 2, 5])
