@@ -353,7 +353,9 @@ csa2_status csa2_cache_read(const csa2_cache *cache, const int64_t *rows, int64_
  * prev) out is 0 and lse -inf.  Rows of no group are left as they were.
  *   seq [ng], off [ng+1] ascending in [0, nq], len [ng]: a group outside the
  *   contract (sequence, offsets, n_g < 0, above seq_len or above max_n) is
- *   skipped and counted in CSA2_CNT_BAD_INPUT, its rows left as they were;
+ *   skipped and counted in CSA2_CNT_BAD_INPUT, its rows left as they were; so is
+ *   every group behind one whose offsets fall, since it may share rows with those
+ *   before;
  *   q [nq][H][512] of q_type CSA2_BF16 or CSA2_F16, 1 <= H <= 128;
  *   prev_out [nq][H][512] fp32 and prev_lse [nq][H], both or neither;
  *   out [nq][H][512] of out_type (fp32: may be prev_out itself);

@@ -87,12 +87,14 @@ struct Group {
     int rows;
     int n;
     bool bad;
+    bool falls;          // its offsets do
 };
 
 __device__ __forceinline__ Group group_of(const DenseParams &p, int g)
 {
     Group r{};
     const int b = p.g_seq[g], a = p.g_off[g], e = p.g_off[g + 1];
+    r.falls = e < a;
     r.bad = b < 0 || b >= p.batch || a < 0 || e < a || e > p.nq;
     if (r.bad) return r;
     const int64_t len = p.seq_len[b];
@@ -154,7 +156,7 @@ struct Work {
     {
         if (left <= 0) return false;
         if (++rt == row_tiles(gr)) {
-            do { gr = group_of(p, ++g); } while (units(gr) == 0);
+            do { gr = group_of(p, ++g); } while (units(gr) == 0);      // (ends: units are left)
             rt = 0;
         }
         return take(0, left);
@@ -172,12 +174,14 @@ struct Found {
     int64_t u0;          // this pair's first
     int work;            // whether it has a piece
     int empty;           // some group has rows but no entries
+    int groups;          // groups before the first whose offsets fall: those behind it may share rows with them
 };
 
 // Found by the whole CTA: thread t < 512 takes ceil(ng / 512) groups, whose units
 // are summed over the warps (totals in `sums`, kFindWarps of them); the thread that
 // holds unit u0 sets up the work.  Up to 32 groups are one warp's alone (0.7 us
-// less than with the others waiting for it).  Ends without a barrier.
+// less than with the others waiting for it).  Where offsets fall, the units of the
+// groups from there on are taken out and the sums made again.  Ends without a barrier.
 constexpr int kFindWarps = 16;
 
 __device__ __forceinline__ void find(const DenseParams &p, int pair, int tid, bool count_bad, int64_t *sums, Found *out)
@@ -189,31 +193,60 @@ __device__ __forceinline__ void find(const DenseParams &p, int pair, int tid, bo
     const int g0 = warp < kFindWarps ? min(tid * each, p.ng) : p.ng, g1 = min(g0 + each, p.ng);
     Group gr{};
     int64_t mine = 0;
-    int empty = 0;
+    int empty = 0, fall = p.ng;
     for (int g = g0; g < g1; ++g) {
         gr = group_of(p, g);
+        if (gr.falls) fall = min(fall, g);
         if (gr.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
         if (!gr.bad && gr.n == 0 && gr.rows > 0) empty = 1;
         mine += units(gr);
     }
-    int64_t upto = mine;                       // inclusive sum over the warp
+    int groups = p.ng;                         // in contract as far as their offsets go
+    auto drop = [&](int from) {                // the groups from `from` on count no more
+        groups = from;
+        for (int g = max(g0, from); g < g1; ++g) {
+            const Group x = group_of(p, g);
+            if (!x.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
+            mine -= units(x);
+        }
+    };
+    auto warp_sum = [&]() {                    // inclusive
+        int64_t upto = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    int64_t before = upto - mine, total = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        return upto;
+    };
+    int64_t before, total = 0;
     if (few) {
         empty = __any_sync(0xffffffffu, empty);
+        fall = __reduce_min_sync(0xffffffffu, fall);
+        if (fall < groups) drop(fall);
+        const int64_t upto = warp_sum();
+        before = upto - mine;
         total = __shfl_sync(0xffffffffu, upto, 31);
     } else {
-        if (lane == 31 && warp < kFindWarps) sums[warp] = upto;
-        empty = __syncthreads_or(empty);
+        int *const falls = reinterpret_cast<int *>(sums + kFindWarps);
+        fall = __reduce_min_sync(0xffffffffu, fall);
+        for (;;) {                             // (twice at most)
+            const int64_t upto = warp_sum();
+            if (lane == 31 && warp < kFindWarps) { sums[warp] = upto; falls[warp] = fall; }
+            empty = __syncthreads_or(empty);
+            before = upto - mine;
+            total = 0;
+            int first = p.ng;
 #pragma unroll
-        for (int i = 0; i < kFindWarps; ++i) {
-            const int64_t v = sums[i];
-            if (i < warp) before += v;
-            total += v;
+            for (int i = 0; i < kFindWarps; ++i) {
+                const int64_t v = sums[i];
+                if (i < warp) before += v;
+                total += v;
+                first = min(first, falls[i]);
+            }
+            if (first == groups) break;
+            drop(first);
+            __syncthreads();                   // the sums are read
         }
     }
     const int64_t run = run_units(p, total), u0 = min(pair * run, total), left = min(run, total - u0);
@@ -221,6 +254,7 @@ __device__ __forceinline__ void find(const DenseParams &p, int pair, int tid, bo
         out->run = run;
         out->u0 = u0;
         out->empty = empty;
+        out->groups = groups;
         out->work = 0;
         if (left > 0) {
             int g = g0;
@@ -937,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     }
     // groups without entries
     if (sFound->empty && warp != kWarpsSoft + kWarpsProd)
-        for (int g = pair; g < p.ng; g += p.pairs) {
+        for (int g = pair; g < sFound->groups; g += p.pairs) {
             const Group gr = group_of(p, g);
             if (!gr.bad && gr.n == 0)
                 empty_rows<kOut>(p, gr, (int)rank * 32 * (kWarpsSoft + kWarpsProd) + tid, 2 * 32 * (kWarpsSoft + kWarpsProd));

@@ -340,6 +340,29 @@ def test_dense_offsets_out_of_contract_and_max_n():
     assert _np(cnt).tolist() == [0, 0, 1, 0] and (out == 7).all()    # 200 entries, at most 150 declared
 
 
+@pytest.mark.parametrize("ng,at", [(3, 1), (3, 0), (2, 1), (32, 17), (45, 20), (45, 44), (1100, 700), (1100, 1)])
+def test_dense_offsets_that_fall_end_the_groups(ng, at):
+    """Groups behind one whose offsets fall may own the same queries as those before:
+    they are skipped and counted, whatever they ask for, and what is before is computed."""
+    h, lens = 4, [(i * 37) % 300 for i in range(7)]
+    cache = _random_cache(lens, 45)
+    seqs = [g % 7 for g in range(ng)]
+    off = [2 * g for g in range(ng + 1)]
+    for g in range(at + 1, ng + 1):              # falls by one at group `at`, ascends again from there
+        off[g] = off[at] - 1 + 2 * (g - at - 1)
+    assert off[at + 1] < off[at] and all(a <= b for g, (a, b) in enumerate(zip(off, off[1:])) if g != at)
+    nq = max(off) + 5
+    q = _queries(nq, h, torch.bfloat16, 46)
+    out, lse = torch.full((nq, h, 512), 7.0, device=DEV), torch.full((nq, h), 7.0, device=DEV)
+    prev = _prev(nq, h, 47)
+    cnt = csa.new_counters()
+    csa.dense_attn(cache, csa.Groups(seqs, off), q, out, lse, prev=prev, counters=cnt)
+    torch.cuda.synchronize()
+    assert _np(cnt).tolist() == [0, 0, ng - at, 0]
+    _check(cache, seqs[:at], off[:at + 1], [lens[b] for b in seqs[:at]], q, out, lse, prev)
+    assert (out[off[at]:] == 7).all() and (lse[off[at]:] == 7).all()
+
+
 def test_dense_takes_and_leaves_its_own_partial_result():
     # three levels of shared prompts, each call in place over the last one's result
     lens = [700, 260, 1]
