@@ -345,7 +345,7 @@ def _load_ext():
             loader = importlib.machinery.ExtensionFileLoader("csa2_torch", _build.EXT_PATH)
             mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("csa2_torch", loader))
             loader.exec_module(mod)
-            mod.set_error(CsaError)
+            mod.set_errors(CsaError, torch.OutOfMemoryError)
             _ext = mod
     return _ext
 
@@ -373,9 +373,12 @@ def dense_attn(cache: Cache, groups: Groups, q, out, lse=None, *, prev=None, sm_
     entries of the group's sequence, into out [nq][H][512] (fp32, bf16 or f16) and
     lse [nq][H]; prev = (out, lse) of an earlier partial result (fp32) is merged in.
     max_n bounds the entries of any group (default: the cache's rows)."""
-    po, pl = prev if prev is not None else (None, None)
-    (_ext or _load_ext()).dense_attn(cache, groups.seq, groups.off, groups.length, q, out, lse, po, pl,
-                                     sm_scale, max_n, ws, counters)
+    try:
+        seq, off, length = groups.seq, groups.off, groups.length
+        po, pl = prev if prev is not None else (None, None)
+    except (AttributeError, TypeError, ValueError) as e:
+        raise CsaError("dense_attn: groups must be Groups, prev a pair (out, lse)") from e
+    (_ext or _load_ext()).dense_attn(cache, seq, off, length, q, out, lse, po, pl, sm_scale, max_n, ws, counters)
 
 
 class Layer:

@@ -2,8 +2,9 @@
 // attention): arguments are taken from tensors here, because on the GPU these
 // calls can be shorter than the interpreter needs for the same checks (a row
 // read of 129 rows: 1.7 us on the GPU, 8 us of checks and ctypes in Python).
-// Marshalling only, as in the rest of the binding: every refusal is a CsaError,
-// and no C++ exception leaves a function.
+// Marshalling only, as in the rest of the binding: every refusal is a CsaError
+// (with what Python raised on the way, if anything, as its cause), no memory for a
+// workspace is PyTorch's OutOfMemoryError, and no C++ exception leaves a function.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -20,6 +21,7 @@
 namespace {
 
 PyObject *g_error = nullptr;      // the package's CsaError
+PyObject *g_memory = nullptr;     // PyTorch's OutOfMemoryError
 
 struct Refusal { std::string what; };
 struct Raised {};                 // a Python exception is set already
@@ -142,19 +144,40 @@ std::string shape_of(const at::Tensor &t)
 
 bool is(const at::Tensor &t, int64_t a, int64_t b) { return t.dim() == 2 && t.size(0) == a && t.size(1) == b; }
 
+// Makes the Python exception that is set (a wrong type, a missing attribute) the
+// cause of a CsaError of the same words; an interrupt or a lack of memory stays.
+void as_refusal(PyObject *type)
+{
+    PyObject *const cause = PyErr_GetRaisedException();
+    if (!PyErr_GivenExceptionMatches(cause, PyExc_Exception) || PyErr_GivenExceptionMatches(cause, PyExc_MemoryError)) {
+        PyErr_SetRaisedException(cause);
+        return;
+    }
+    PyErr_Format(type, "%S", cause);
+    PyObject *const e = PyErr_GetRaisedException();
+    PyException_SetCause(e, cause);       // (takes the reference)
+    PyErr_SetRaisedException(e);
+}
+
 // Runs f, turning what it throws into a Python exception.
 template <typename F>
 PyObject *guarded(F f)
 {
+    PyObject *const type = g_error != nullptr ? g_error : PyExc_RuntimeError;
     try {
         return f();
     } catch (const Raised &) {
+        as_refusal(type);
     } catch (const Refusal &r) {
-        PyErr_SetString(g_error != nullptr ? g_error : PyExc_RuntimeError, r.what.c_str());
+        PyErr_SetString(type, r.what.c_str());
+    } catch (const c10::OutOfMemoryError &e) {
+        PyErr_SetString(g_memory != nullptr ? g_memory : PyExc_MemoryError, e.what_without_backtrace());
+    } catch (const c10::Error &e) {       // (a tensor without the storage or strides that a call needs)
+        PyErr_SetString(type, e.what_without_backtrace());
     } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+        PyErr_SetString(type, e.what());
     } catch (...) {
-        PyErr_SetString(PyExc_RuntimeError, "unknown error");
+        PyErr_SetString(type, "unknown error");
     }
     return nullptr;
 }
@@ -305,21 +328,20 @@ PyObject *check_cache(PyObject *, PyObject *const *a, Py_ssize_t n_args)
     });
 }
 
-// (CsaError)
-PyObject *set_error(PyObject *, PyObject *const *a, Py_ssize_t n_args)
+// (CsaError, torch.OutOfMemoryError)
+PyObject *set_errors(PyObject *, PyObject *const *a, Py_ssize_t n_args)
 {
     return guarded([&]() -> PyObject * {
-        arguments(n_args, 1);
-        Py_XINCREF(a[0]);
-        Py_XDECREF(g_error);
-        g_error = a[0];
+        arguments(n_args, 2);
+        Py_XSETREF(g_error, Py_NewRef(a[0]));
+        Py_XSETREF(g_memory, Py_NewRef(a[1]));
         Py_RETURN_NONE;
     });
 }
 
 #define CSA2_FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CSA2_FAST(cache_write), CSA2_FAST(cache_read), CSA2_FAST(dense_attn), CSA2_FAST(check_cache),
-                         CSA2_FAST(set_error), {nullptr, nullptr, 0, nullptr}};
+                         CSA2_FAST(set_errors), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "csa2_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

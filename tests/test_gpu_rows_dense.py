@@ -549,6 +549,53 @@ def test_refusals_with_tensors_on_the_device():
     assert np.array_equal(_np(x.double()), _values(cache, 0, 64)[[3, 1]].numpy())
 
 
+def test_every_refusal_is_the_packages_error():
+    cache = _random_cache([64], 93)
+    g = csa.Groups([0], [0, 2])
+    q = _queries(2, 4, torch.bfloat16, 94)
+    out, lse = torch.full((2, 4, 512), 5.0, device=DEV), torch.full((2, 4), 5.0, device=DEV)
+    rows, x = torch.tensor([3, 1], device=DEV), torch.full((2, 512), 5.0, device=DEV)
+    sparse = torch.zeros(2, 512, device=DEV).to_sparse()
+    calls = [lambda a=a, k=k: csa.dense_attn(*a, **k) for a, k in (
+        ((None, g, q, out, lse), {}), ((object(), g, q, out, lse), {}), ((cache, None, q, out, lse), {}),
+        ((cache, (0, 1), q, out, lse), {}), ((cache, g, q, out, lse), dict(max_n=1.5)),
+        ((cache, g, q, out, lse), dict(max_n=1 << 70)), ((cache, g, q, out, lse), dict(max_n="64")),
+        ((cache, g, q, out, lse), dict(sm_scale="x")), ((cache, g, q, out, lse), dict(sm_scale=None)),
+        ((cache, g, q, out, lse), dict(prev=5)), ((cache, g, q, out, lse), dict(prev=(out,))),
+        ((cache, g, q, out, lse), dict(prev=(out, lse, lse))))]
+    for f in (csa.cache_write, csa.cache_read):
+        calls += [lambda a=a, f=f: f(*a) for a in ((None, rows, x), ("cache", rows, x), (cache, rows, sparse),
+                                                   (cache, sparse, x), (cache, rows, x, sparse))]
+    for call in calls:
+        with pytest.raises(csa.CsaError):
+            call()
+    # what Python raised on the way is kept as the cause
+    with pytest.raises(csa.CsaError) as e:
+        csa.dense_attn(cache, g, q, out, lse, max_n=1.5)
+    assert isinstance(e.value.__cause__, TypeError)
+    torch.cuda.synchronize()
+    assert (out == 5).all() and (lse == 5).all() and (x == 5).all()
+
+
+def test_no_memory_for_a_workspace_is_pytorchs_error():
+    cache = _random_cache([3000], 95)
+    q = _queries(40, 64, torch.bfloat16, 96)
+    out = torch.zeros(40, 64, 512, dtype=torch.bfloat16, device=DEV)
+    groups = csa.Groups([0], [0, 40])
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(1e-4)          # 28 MB: the workspace needs 40
+    try:
+        assert csa.dense_workspace_size(1, 40, 64, cache.cap) > 30 << 20
+        with pytest.raises(torch.OutOfMemoryError):
+            csa.dense_attn(cache, groups, q, out)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    csa.dense_attn(cache, groups, q, out)
+    torch.cuda.synchronize()
+    _check(cache, [0], [0, 40], [3000], q, out, None)
+
+
 def test_rows_and_dense_past_32_bit_offsets():
     # 18 M rows: 4.6 GB of codes; the second sequence lies past 2^32 bytes
     cap0, n = 17_500_000, 700

@@ -155,3 +155,16 @@ def test_cache_over_checks_its_tensors():
         csa.Cache.over(c.codes.int(), c.scales, c.kidx, c.kscale, c.seq_base, c.seq_len, 2)
     with pytest.raises(csa.CsaError):
         csa.Cache.over(c.codes, c.scales, c.kidx, c.kscale, c.seq_base[:2], c.seq_len, 2)
+
+
+def test_refusals_of_what_is_no_tensor_or_has_no_storage():
+    c = csa.Cache([8, 16], 64, 2, "cpu")
+    rows, x = torch.zeros(4, dtype=torch.int64), torch.zeros(4, 512)
+    sparse = torch.zeros(24, 256, dtype=torch.uint8).to_sparse()
+    for call in (lambda: csa.Cache.over(sparse, c.scales, c.kidx, c.kscale, c.seq_base, c.seq_len, 2),
+                 lambda: csa.Cache.over("codes", c.scales, c.kidx, c.kscale, c.seq_base, c.seq_len, 2),
+                 lambda: csa.cache_write(c, torch.zeros(4, dtype=torch.int64).to_sparse(), x),
+                 lambda: csa.cache_read(c, rows, torch.zeros(4, 512).to_sparse()),
+                 lambda: csa.dense_attn(c, None, x, x), lambda: csa.dense_attn(c, csa.Groups([0], [0, 4], device="cpu"), x, x, prev=3)):
+        with pytest.raises(csa.CsaError):
+            call()
