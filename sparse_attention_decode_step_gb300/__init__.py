@@ -336,13 +336,13 @@ _ext = None
 
 
 def _load_ext():
+    """Loads csa2_torch.so, building it with g++ first if it is missing, stale or of
+    another PyTorch.  Only Cache.over and the calls below need it."""
     global _ext
     lib()
     with _lock:
         if _ext is None:
-            if not os.path.exists(_build.EXT_PATH):
-                raise CsaError(f"compiled binding not found at {_build.EXT_PATH}")
-            loader = importlib.machinery.ExtensionFileLoader("csa2_torch", _build.EXT_PATH)
+            loader = importlib.machinery.ExtensionFileLoader("csa2_torch", _build.build_ext())
             mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("csa2_torch", loader))
             loader.exec_module(mod)
             mod.set_errors(CsaError, torch.OutOfMemoryError)

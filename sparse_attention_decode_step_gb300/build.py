@@ -1,13 +1,15 @@
 """Builds libcsa2.so (the CUDA library behind include/csa2.h) in-tree with nvcc,
-and csa2_torch.so (the Python binding's short calls) with g++.
+and, apart from it, csa2_torch.so (the Python binding's short calls) with g++.
 
-One compiler process per translation unit, run in parallel, then a link step
-each; sm_103a only.  The output goes to sparse_attention_decode_step_gb300/_build/.
+One nvcc process per translation unit, run in parallel, then one link step;
+sm_103a only.  The library needs nothing but CUDA; the module also needs the
+headers of PyTorch and Python, and is built for the PyTorch that is installed.
+The output goes to sparse_attention_decode_step_gb300/_build/.
 """
 from __future__ import annotations
 
-import importlib.util
 import os
+import platform
 import subprocess
 import sys
 import sysconfig
@@ -20,6 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libcsa2.so")
 EXT_PATH = os.path.join(OUT_DIR, "csa2_torch.so")
+EXT_STAMP = os.path.join(OUT_DIR, "csa2_torch.for")     # what EXT_PATH was built for
 
 SOURCES = ["csa2_api.cu", "csa2_append.cu", "csa2_index.cu", "csa2_topk.cu", "csa2_attn_tc.cu",
            "csa2_rows.cu", "csa2_dense.cu"]
@@ -35,23 +38,30 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _torch_dir() -> str:
-    return importlib.util.find_spec("torch").submodule_search_locations[0]
-
-
-def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + [EXT_SOURCE]]
-    files.append(os.path.join(_torch_dir(), "version.py"))     # (the binding is built against this PyTorch)
-    files.append(os.path.join(INCLUDE, "csa2.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _fresh(out: str, inputs) -> bool:
+    if not os.path.exists(out):
+        return False
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(f) <= t for f in inputs)
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(EXT_PATH)):
+    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    return _fresh(LIB_PATH, files + [os.path.join(INCLUDE, "csa2.h"), os.path.abspath(__file__)])
+
+
+def _ext_stamp() -> str:
+    """The PyTorch (its version and C++ ABI), Python and machine that the module is good for."""
+    import torch
+    return f"torch {torch.__version__} abi {int(torch.compiled_with_cxx11_abi())} {sys.implementation.cache_tag} {platform.machine()}"
+
+
+def ext_up_to_date() -> bool:
+    files = [os.path.join(CSRC, EXT_SOURCE), os.path.join(INCLUDE, "csa2.h"), os.path.abspath(__file__)]
+    if not (_fresh(EXT_PATH, files) and os.path.exists(EXT_STAMP)):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(EXT_PATH))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    with open(EXT_STAMP) as f:
+        return f.read() == _ext_stamp()
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -69,24 +79,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    torch_dir = _torch_dir()
-    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    ext_obj = os.path.join(OUT_DIR, "csa2_torch.o")
-
-    def compile_ext():
-        inc = [INCLUDE, os.path.join(torch_dir, "include"),
-               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
-               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1",
-               *[f for d in inc for f in ("-I", d)], "-c", os.path.join(CSRC, EXT_SOURCE), "-o", ext_obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on {EXT_SOURCE}:\n{r.stderr}")
-
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext = ex.submit(compile_ext)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        ext.result()
     if verbose or ptxas_info:
         for _obj, err in results:
             if err:
@@ -97,14 +91,33 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    return LIB_PATH
+
+
+def build_ext(force: bool = False) -> str:
+    """Builds csa2_torch.so against the installed PyTorch (and the library first, if it is stale)."""
+    build()
+    if not force and ext_up_to_date():
+        return EXT_PATH
+    import torch
+    torch_dir = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [INCLUDE, os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     tmp = EXT_PATH + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, ext_obj, "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda",
-           "-ltorch_cpu", "-ltorch_python", "-L", OUT_DIR, "-l:libcsa2.so", "-Wl,-rpath,$ORIGIN"]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f for d in inc for f in ("-I", d)], os.path.join(CSRC, EXT_SOURCE), "-o", tmp,
+           "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-L", OUT_DIR, "-l:libcsa2.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ link failed:\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on {EXT_SOURCE}:\n{r.stderr}")
     os.replace(tmp, EXT_PATH)
-    return LIB_PATH
+    with open(EXT_STAMP, "w") as f:
+        f.write(_ext_stamp())
+    return EXT_PATH
 
 
 if __name__ == "__main__":

@@ -1,6 +1,10 @@
 """Host-side argument checks of the cache row calls and the dense attention:
 each call returns before it touches a device."""
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -168,3 +172,41 @@ def test_refusals_of_what_is_no_tensor_or_has_no_storage():
                  lambda: csa.dense_attn(c, None, x, x), lambda: csa.dense_attn(c, csa.Groups([0], [0, 4], device="cpu"), x, x, prev=3)):
         with pytest.raises(csa.CsaError):
             call()
+
+
+def test_the_library_does_not_need_the_compiled_module(tmp_path):
+    # a copy of the package whose module cannot be built: the C ABI and the ctypes calls work, the short calls say why not
+    csa.lib()
+    pkg = os.path.dirname(csa.__file__)
+    to = tmp_path / os.path.basename(pkg)
+    shutil.copytree(pkg, to, ignore=shutil.ignore_patterns("csa2_torch.*", "*.o", "__pycache__"))
+    shutil.copytree(os.path.join(os.path.dirname(pkg), "include"), tmp_path / "include")
+    (to / "csrc" / "csa2_torch.cpp").write_text("#error no PyTorch here\n")
+    code = f"""
+import {to.name} as csa, torch
+assert csa.library_path().startswith({str(tmp_path)!r})
+assert csa.topk_workspace_size(1, 1 << 20) > 0 and csa.dense_workspace_size(1, 1, 16, 64) > 0
+cache = csa.Cache([8], 64, 1, "cpu")
+try:
+    csa.cache_write(cache, torch.zeros(1, dtype=torch.int64), torch.zeros(1, 512))
+except RuntimeError as e:
+    assert "csa2_torch.cpp" in str(e) and "no PyTorch here" in str(e), e
+else:
+    raise AssertionError("no error")
+"""
+    env = dict(os.environ, PYTHONPATH=str(tmp_path))
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_the_compiled_module_is_rebuilt_for_another_pytorch(tmp_path, monkeypatch):
+    from sparse_attention_decode_step_gb300 import build as b
+    b.build_ext()
+    assert b.ext_up_to_date()
+    stamp = tmp_path / "for"
+    monkeypatch.setattr(b, "EXT_STAMP", str(stamp))
+    assert not b.ext_up_to_date()                                  # it is not known what it was built for
+    stamp.write_text(b._ext_stamp())
+    assert b.ext_up_to_date()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + "1")
+    assert not b.ext_up_to_date() and b.up_to_date()
