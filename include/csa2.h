@@ -382,6 +382,7 @@ csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, 
                             uint32_t *counters, void *stream);
 
 /* ---- workspace sizes (host-only, no GPU work) ------------------------------ */
+/* (0 for sizes that csa2_dense_attn refuses) */
 size_t csa2_dense_workspace_size(int32_t ng, int32_t nq, int32_t H, int64_t max_n);
 size_t csa2_index_workspace_size(int32_t nq, int32_t group, int32_t h_idx, int32_t d_idx);
 size_t csa2_topk_workspace_size(int32_t nq, int64_t max_n);

@@ -600,9 +600,19 @@ csa2_status csa2_cache_read(const csa2_cache *cache, const int64_t *rows, int64_
 }
 
 // ---------------------------------------------------------------- dense attention
+namespace {
+
+// What a call takes at most; sums of products of these stay within 64 bits.
+bool dense_sizes_ok(int64_t ng, int64_t nq, int64_t H, int64_t max_n)
+{
+    return H >= 1 && H <= 128 && nq * H < (1LL << 30) && ng < (1 << 24) && max_n >= 0 && max_n < (1LL << 31);
+}
+
+}  // namespace
+
 size_t csa2_dense_workspace_size(int32_t ng, int32_t nq, int32_t H, int64_t max_n)
 {
-    if (max_n < 0) return 0;
+    if (!dense_sizes_ok(ng, nq, H, max_n)) return 0;
     return dense_plan(ng, nq, H, max_n).total;
 }
 
@@ -620,7 +630,7 @@ csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, 
     CSA2_REQUIRE((prev_out == nullptr) == (prev_lse == nullptr), CSA2_ERR_INVALID_ARG);
     CSA2_REQUIRE(H >= 1 && H <= 128 && (q_type == CSA2_BF16 || q_type == CSA2_F16), CSA2_ERR_UNSUPPORTED);
     CSA2_REQUIRE(out_type == CSA2_F32 || out_type == CSA2_BF16 || out_type == CSA2_F16, CSA2_ERR_UNSUPPORTED);
-    CSA2_REQUIRE((int64_t)groups->nq * H < (1LL << 30) && groups->ng < (1 << 24), CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(dense_sizes_ok(groups->ng, groups->nq, H, max_n), CSA2_ERR_UNSUPPORTED);
     CSA2_REQUIRE(al4(groups->seq) && al4(groups->off) && (groups->len == nullptr || al4(groups->len)) && al16(q) &&
                      al16(out) && (prev_out == nullptr || (al16(prev_out) && al4(prev_lse))) &&
                      (lse == nullptr || al4(lse)) && (counters == nullptr || al4(counters)),

@@ -210,3 +210,14 @@ def test_the_compiled_module_is_rebuilt_for_another_pytorch(tmp_path, monkeypatc
     assert b.ext_up_to_date()
     monkeypatch.setattr(torch, "__version__", torch.__version__ + "1")
     assert not b.ext_up_to_date() and b.up_to_date()
+
+
+def test_dense_workspace_sizes_of_calls_that_are_refused():
+    for ng, nq, h, n in ((1, 1, 16, 1 << 31), (1, 1, 16, (1 << 63) - 1), (1, 1, 16, 1 << 62), (1, 1, 129, 64), (1, 1, 0, 64),
+                         (1, 1 << 30, 1, 64), (1, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1), (1 << 24, 1 << 20, 1, 64)):
+        assert csa.dense_workspace_size(ng, nq, h, n) == 0, (ng, nq, h, n)
+        assert _dense(ng=ng, nq=nq, H=h, max_n=n) in (INVALID, UNSUPPORTED)
+    # and of the largest that are not: no more than that of a full GPU
+    most = csa.dense_workspace_size(1, 1 << 20, 128, 64)
+    assert csa.dense_workspace_size((1 << 24) - 1, (1 << 30) - 1, 1, (1 << 31) - 1) == most > 0
+    assert csa.dense_workspace_size(1, 1, 16, 1 << 20) > 0
