@@ -221,10 +221,6 @@ class Groups:
         if self.off.numel() != self.ng + 1 or (length is not None and self.length.numel() != self.ng):
             raise CsaError("groups need seq [ng], off [ng + 1] and length [ng]")
 
-    def struct(self, nq: int) -> _Groups:
-        return _Groups(self.seq.data_ptr(), self.off.data_ptr(),
-                       self.length.data_ptr() if self.length is not None else None, self.ng, nq)
-
 
 def new_counters(device="cuda"):
     return torch.zeros(NUM_COUNTERS, dtype=torch.int32, device=device)
