@@ -314,6 +314,9 @@ PyObject *check_cache(PyObject *, PyObject *const *a, Py_ssize_t n_args)
             (kscale != nullptr && kscale->scalar_type() != at::kFloat) || base.scalar_type() != at::kLong ||
             len.scalar_type() != at::kInt)
             refuse("cache tensors: codes, scales, kidx uint8, kscale fp32, seq_base int64, seq_len int32");
+        for (const at::Tensor *t : {&scales, kidx, kscale, &base, &len})
+            if (t != nullptr && t->device() != codes.device())
+                refuse("cache tensors on " + codes.device().str() + " and " + t->device().str());
         if (!codes.is_contiguous() || !scales.is_contiguous() || (kidx != nullptr && !kidx->is_contiguous()) ||
             (kscale != nullptr && !kscale->is_contiguous()) || !base.is_contiguous() || !len.is_contiguous())
             refuse("cache tensors must be contiguous");

@@ -221,3 +221,13 @@ def test_dense_workspace_sizes_of_calls_that_are_refused():
     most = csa.dense_workspace_size(1, 1 << 20, 128, 64)
     assert csa.dense_workspace_size((1 << 24) - 1, (1 << 30) - 1, 1, (1 << 31) - 1) == most > 0
     assert csa.dense_workspace_size(1, 1, 16, 1 << 20) > 0
+
+
+def test_cache_over_refuses_tensors_of_two_devices():
+    # (a call takes the addresses of all of them: one of host memory would fault on the GPU)
+    c = csa.Cache([8, 16], 64, 2, "cpu")
+    six = [c.codes, c.scales, c.kidx, c.kscale, c.seq_base, c.seq_len]
+    for i in range(6):
+        with pytest.raises(csa.CsaError):
+            csa.Cache.over(*six[:i], six[i].to("meta"), *six[i + 1:], 2)
+    assert csa.Cache.over(*six, 2).cap == 24
