@@ -347,15 +347,16 @@ def _load_ext():
 
 
 def cache_write(cache: Cache, rows, x, key=None, counters=None):
-    """Quantises x [n][512] (fp32, bf16 or f16, any row stride) into the cache rows
-    rows [n] (int64, distinct; negative: skipped), and key [n][d_idx] (x's type)
-    into their indexer keys if it is given."""
+    """Quantises x [n][512] (fp32, bf16 or f16; rows 512 elements or more and a multiple
+    of 16 bytes apart) into the cache rows rows [n] (int64, distinct; negative: skipped),
+    and key [n][d_idx] (x's type, its rows likewise) into their indexer keys if it is given."""
     (_ext or _load_ext()).cache_write(cache, rows, x, key, counters)
 
 
 def cache_read(cache: Cache, rows, x, key=None, counters=None):
     """Reads the cache rows rows [n] (int64; negative: skipped) into x [n][512] (fp32,
-    bf16 or f16: exact) and, if given, their indexer keys into key [n][d_idx] fp32."""
+    bf16 or f16: exact) and, if given, their indexer keys into key [n][d_idx] fp32; rows
+    of x and key lie apart as in cache_write."""
     (_ext or _load_ext()).cache_read(cache, rows, x, key, counters)
 
 
@@ -368,7 +369,8 @@ def dense_attn(cache: Cache, groups: Groups, q, out, lse=None, *, prev=None, sm_
     """Attention of each group's queries q [nq][H][512] (bf16 or f16) over all the
     entries of the group's sequence, into out [nq][H][512] (fp32, bf16 or f16) and
     lse [nq][H]; prev = (out, lse) of an earlier partial result (fp32) is merged in.
-    max_n bounds the entries of any group (default: the cache's rows)."""
+    max_n bounds the entries of any group (default: the cache's rows).  q, out, lse and
+    prev are contiguous.  Every entry counts: this is not the selection of sparse_attn."""
     try:
         seq, off, length = groups.seq, groups.off, groups.length
         po, pl = prev if prev is not None else (None, None)

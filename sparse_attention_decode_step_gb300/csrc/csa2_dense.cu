@@ -38,12 +38,15 @@
 // second kernel joins the pieces in a fixed order, so results do not depend on
 // timing.
 //
-// Measured: 32 queries x 64 heads over 65,536 entries (275 GFLOP) in 184 us,
-// 1,494 TFLOP/s.  What bounds a long run is the port that serves shared memory
-// and L1: per tile and SM the MMAs' operands take 3,072 of its cycles (384 KB),
-// the stores of the dequantised operands 2,048, the loads of codes 1,080 and P
-// 256, together 6,456; a tile takes about 6,500, the MMAs alone 4,134.  What
-// bounds a short run is the chain of a piece, in cycles with a single tile: work
+// Measured: 32 queries x 64 heads over 65,536 entries (275 GFLOP) in 179 to 184 us
+// (in a graph), 1,494 to 1,537 TFLOP/s.  What bounds a long run is the refilling of
+// the ring.  With cycle counters around the waits (they add about a tenth to the
+// call), of 6,240 cycles a tile the issuer waits 3,890 for filled stages and 400 for P;
+// a producer waits only 700 for an empty one and takes 3,970 to convert and store, the
+// rest for its loads; a softmax warp waits 2,170.  The MMAs alone are 4,134.  No
+// counted unit is at its limit (16 queries: tensor pipe 60 %, LSU data pipe 58 % of
+// the active cycles, issue 54 %): which of the producers' steps to shorten, or whether
+// more stages would do, has not been told apart.  What bounds a short run is the chain of a piece, in cycles with a single tile: work
 // found 4,700, first scores 5,900, softmax 3,400, O 2,700, epilogue 3,000 to 4,000;
 // and the join (about 4 us).
 #include <cuda_fp16.h>
@@ -637,10 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         // ============================================== producers
         // A stage is 1,024 units of 32 channels of one entry (16 code bytes, 2
         // scales), four per lane of the eight warps.  Eight lanes read one entry's
-        // 128 code bytes, a whole line: the L1 port serves these loads, the stores
-        // into the ring and the tensor core's operand reads alike, and is what the
-        // kernel runs out of first (with 64 or 32 bytes of an entry per eight lanes it
-        // took 298 and 323 us at 32 x 64 heads x 65,536 entries, so 248).  Those eight
+        // 128 code bytes, a whole line (with 64 or 32 bytes of an entry per eight lanes
+        // it took 298 and 323 us at 32 x 64 heads x 65,536 entries, so 248).  Those eight
         // lanes write their four 16-byte pieces each in an order turned by 0 .. 3, so
         // that they hit eight bank groups at every store.  Codes are loaded a whole
         // ring (two stages) ahead.
