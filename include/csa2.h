@@ -362,7 +362,7 @@ csa2_status csa2_cache_read(const csa2_cache *cache, const int64_t *rows, int64_
  *   lse [nq][H] or NULL (may be prev_lse itself);
  *   max_n: host bound on every n_g; it sets how a group's entries are divided.
  * Arithmetic as in csa2_sparse_attn: exact f16 latents, q as f16 (bf16: exact
- * for magnitudes in [2^-14, 65504]), softmax weights rounded to f16 (off by 2^-11
+ * for magnitudes in [2^-14, 65504]), logits |x_j| below 2^27, softmax weights rounded to f16 (off by 2^-11
  * of themselves, or by 2^-32 of the row's largest where that is more), every sum in
  * fp32; results do not depend on the run (fixed order).  Each level of shared
  * prompts rounds its own weights once.

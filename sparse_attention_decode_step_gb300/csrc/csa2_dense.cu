@@ -803,10 +803,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                         for (int c = 0; c < 32; ++c) hi = fmaxf(hi, -x[c]);
                     }
                 }
-                const float top = hi == -INFINITY ? hi : fmaf(hi, fabsf(l2s), -kHead);
+                // (rounded up, and compared by its exact difference, so that P stays below 2^15
+                // however far apart fp32's values are at these logits)
+                const float top = hi == -INFINITY ? hi : __fmaf_ru(hi, fabsf(l2s), -kHead);
                 // (a wait that gave up takes the same path, and the vote makes every thread
                 // leave together)
-                if (soft_any(top > m + kLazy || !got)) {
+                if (soft_any(top - m > kLazy || !got)) {
                     sRed[which * kRowsCta + row] = top;
                     ok = !soft_any(!got || *abort_flag);
                     if (!ok) break;
@@ -814,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                         const float t = fmaxf(fmaxf(sRed[tid], sRed[kRowsCta + tid]),
                                               fmaxf(sRed[2 * kRowsCta + tid], sRed[3 * kRowsCta + tid]));
                         const float old = sM[tid];
-                        const bool moves = t > old + kLazy;
+                        const bool moves = t - old > kLazy;
                         sAlpha[tid] = !moves ? 1.f : old == -INFINITY ? 0.f : fast_exp2(old - t);
                         if (moves) sM[tid] = t;
                     }

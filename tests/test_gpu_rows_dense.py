@@ -436,6 +436,41 @@ def test_dense_keeps_a_long_tail_below_one_large_entry():
     assert ((lse.double() - lref).abs() - dmax[:, 0] - sums - 2.0 ** -22 * (lref.abs() + 1)).max() <= 0
 
 
+@pytest.mark.parametrize("queries,n,later", [(152, 600, 300), (1, 256 * 152, 300), (1, 256 * 152, 30000)])
+def test_dense_logits_where_fp32_is_coarse(queries, n, later):
+    """Two entries with logits near 6e7 (fp32 in steps of 4) that differ by one step, the
+    others far below, sums exact: the weights are 1 and e^-4, in one run of tiles and over several pieces."""
+    h = 64
+    cache = _random_cache([n], 105)
+    codes = torch.zeros(n, 512, dtype=torch.uint8)
+    scales = torch.full((n, 32), 0x38, dtype=torch.uint8)
+    for j in (0, later):                                      # 496 channels of 6 x 16, and one channel of 1 in the later entry
+        codes[j, :496], scales[j, :31] = 7, 0x58
+    codes[later, 511] = 2
+    cache.codes[:n].copy_(codes[:, 0::2] | (codes[:, 1::2] << 4))
+    cache.scales[:n].copy_(scales)
+    v = _values(cache, 0, n).to(DEV)
+    assert (v[[0, later], :496] == 96).all() and v[later, 511] == 1 and v.sum() == 2 * 496 * 96 + 1
+    q = torch.zeros(queries, h, 512)
+    q[:, :, :496] = (1032 + 8 * (torch.arange(h) % 46)).float()[None, :, None]
+    q[:, :, 511] = 4
+    q = q.to(torch.bfloat16).to(DEV)
+    out, lse = torch.zeros(queries, h, 512, device=DEV), torch.zeros(queries, h, device=DEV)
+    csa.dense_attn(cache, csa.Groups([0], [0, queries]), q, out, lse)
+    torch.cuda.synchronize()
+    x = q[0].double() @ v.T
+    assert ((x[:, later] - x[:, 0]) == 4).all() and (x.amax(1) < 2.0 ** 26).all()
+    w = 1 / (1 + float(np.exp(-4.0)))
+    want = torch.zeros(512, dtype=torch.float64, device=DEV)
+    want[:496], want[511] = 96, w
+    # each weight: half a step of f16 and 2^-20 for the exponential and sums, in numerator and denominator
+    far = (out.double() - want).abs() - 2 * (2.0 ** -11 + 2.0 ** -20) * want
+    assert far.max() <= 0, far.max().item()
+    # lse: the reference, log2 and their sum and product in fp32, four roundings
+    lref = torch.logsumexp(x, 1)
+    assert ((lse.double() - lref).abs() / lref).max() <= 4 * 2.0 ** -24
+
+
 def test_dense_is_reproducible_on_streams_and_in_graphs():
     cache = _random_cache([5000, 900], 71)
     groups = csa.Groups([0, 1], [0, 2, 5])
