@@ -39,7 +39,8 @@
  *   - Bulk arrays (cache rows, key scales, queries, scores, block maxima,
  *     window KV, outputs, workspace) must be 16-byte aligned; small index
  *     arrays (seq_base, seq_len, q_seq, q_pos, idx, cnt, n_valid, pool_blk,
- *     pool_n, win_start, lse) need only their natural alignment.  A violation
+ *     pool_n, win_start, lse) need only their natural alignment, and so does what
+ *     a section says of its own.  A violation
  *     returns CSA2_ERR_ALIGN.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = default).
  *     The returned status covers host-side argument checks and the launch
@@ -73,7 +74,7 @@ typedef enum {
 
 typedef enum { CSA2_FULL = 0, CSA2_REINDEX = 1, CSA2_REUSE = 2 } csa2_mode;
 
-/* Element types of the calls that take more than one (section 8 and 9). */
+/* Element types of the calls that take more than one (sections 8 to 13). */
 typedef enum { CSA2_F32 = 0, CSA2_BF16 = 1, CSA2_F16 = 2 } csa2_dtype;
 
 /* Device counter slots (uint32 each). */
@@ -380,6 +381,122 @@ csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, 
                             const float *prev_out, const float *prev_lse, void *out,
                             csa2_dtype out_type, float *lse, void *workspace, size_t ws_bytes,
                             uint32_t *counters, void *stream);
+
+/* ---- 10. pages -----------------------------------------------------------------
+ * A cache whose sequences are given pages as they grow: entry j of sequence b is
+ * row table[b * ld + j / page] * page + j % page.  Sequences may share pages (a
+ * common prefix) that nobody writes any more.  csa2_cache_write and
+ * csa2_cache_read take such rows by number; the calls below take the table.
+ *   page: entries per page, a power of two from 16 on; pages lie at multiples of
+ *   it, so there are cap / page (rounded down);
+ *   a sequence of n entries uses its first ceil(n / page) table entries; the
+ *   others may hold anything.  A page number outside the cache is counted in
+ *   CSA2_CNT_BAD_INPUT (once or more) and never followed: results that depend
+ *   on its entries are unspecified.
+ * The calls below take a NULL csa2_pages for sequences that lie at seq_base as
+ * everywhere else.  With pages, the cache's seq_base is not read and may be NULL.
+ * ld: 1 .. 2^31 - 1; table: 4-byte aligned. */
+typedef struct {
+    const int32_t *table;      /* [batch][ld] page numbers */
+    int64_t ld;
+    int32_t page;
+} csa2_pages;
+
+/* ---- 11. norm and rotation -------------------------------------------------------
+ * The RMS norm of every 512-wide row and the rotation of its last `rot` channels
+ * by the position of its token, in one pass: queries for the attention calls,
+ * latents for csa2_cache_write ([Notes] section 4: the cache holds values after
+ * the rotation, bounded by sqrt(512) through the norm).
+ *   y_c = x_c / sqrt(mean(x^2) + eps) * weight_c   (weight NULL: 1)
+ *   pairs (u, v) of the last rot channels, p = 0 .. rot / 2 - 1: channels 2p and
+ *   2p + 1 of them, or with halves != 0 channels p and rot / 2 + p;
+ *   a = pos[i] * inv_freq[p];  u' = u cos a - v sin a,  v' = u sin a + v cos a.
+ *   x, out [n][H][512] of type and out_type (any of the three): token i at i * ld_x
+ *   (ld_out) elements, its H heads 512 apart; out may be x itself (same type and
+ *   ld).  weight [512] fp32; pos [n] (negative: rotates back), inv_freq [rot / 2]
+ *   fp32 radians per position, both NULL allowed when rot == 0.
+ *   rot: 0 .. 512, a multiple of 16.  1 <= H <= 128, n * H < 2^31.
+ * Sums, the norm and the rotation are fp32 and rounded once at the end; the angle
+ * is reduced in turns of 64-bit fixed point, so that it is as exact at position
+ * 2^30 as near 0 (cos and sin within 2^-21).  A row of zeros gives zeros if eps > 0.
+ * x, out, weight: 16-byte aligned, ld_x and ld_out at least H * 512, below 2^31 and a
+ * multiple of 16 bytes; pos, inv_freq: 4-byte aligned; eps >= 0. */
+csa2_status csa2_norm_rope(const void *x, csa2_dtype type, int64_t ld_x, int64_t n, int32_t H,
+                           const float *weight, float eps, const int32_t *pos,
+                           const float *inv_freq, int32_t rot, int32_t halves, void *out,
+                           csa2_dtype out_type, int64_t ld_out, void *stream);
+
+/* ---- 12. attention of chunks of new tokens -----------------------------------------
+ * csa2_dense_attn with a causal limit and pages: group g is a run of consecutive
+ * tokens of sequence seq[g] (one of a decode step, a part of a prompt, a whole
+ * one), its first at token position pos[g]; their own entries are in the cache
+ * already.  Query i of the group sees the entries
+ *     j < min(n_g, floor((pos[g] + i - off[g] + 1) / m)),     (none if that is < 1)
+ * n_g and m as before (csa2_groups, csa2_cache); pos NULL: all n_g.  Positions count
+ * tokens of what the cache holds now: after csa2_cache_evict, n_g * m less the
+ * chunk's length.  Everything else, prev_out, lse, the contract of groups and the
+ * arithmetic, is csa2_dense_attn's; a query that sees nothing has prev, or 0 and
+ * lse -inf.  The size of the workspace is csa2_dense_workspace_size's.
+ *   pos [ng], 4-byte aligned, any int32. */
+csa2_status csa2_chunk_attn(const csa2_cache *cache, const csa2_pages *pages,
+                            const csa2_groups *groups, const int32_t *pos, int64_t max_n,
+                            const void *q, csa2_dtype q_type, int32_t H, float sm_scale,
+                            const float *prev_out, const float *prev_lse, void *out,
+                            csa2_dtype out_type, float *lse, void *workspace, size_t ws_bytes,
+                            uint32_t *counters, void *stream);
+
+/* ---- 13. attention weights by entry -------------------------------------------------
+ * How much weight the queries of a group give to each entry of its sequence b:
+ *   mass[b][j] = decay * prev[b][j] + sum over its queries i and heads h of
+ *                e^(sm_scale * q[i][h] . v_j - lse[i][h]),   j < n_g,
+ * over the pairs (i, j) in which i sees j (as in csa2_chunk_attn; pos NULL: all of
+ * them); prev NULL: without the first term.  lse is what an attention call gave
+ * for these queries (over the entries and whatever else was merged in), |lse| below
+ * 2^28; a row whose lse is -inf or +inf adds nothing.  Entries from n_g on and sequences of no group
+ * are left as they were.
+ *   groups as in csa2_chunk_attn, but a sequence may be in one group only: a group
+ *   whose sequence an earlier one has is skipped and counted in CSA2_CNT_BAD_INPUT;
+ *   q [nq][H][512] of q_type CSA2_BF16 or CSA2_F16, 1 <= H <= 128; lse [nq][H];
+ *   prev, mass [batch][ld_mass] fp32, ld_mass >= max_n; prev may be mass itself.
+ * Arithmetic: products of exact f16 latents and q as f16 (as in csa2_dense_attn),
+ * everything else in fp32; results do not depend on the run (fixed order).
+ * lse, prev, mass: 4-byte aligned; q, workspace: 16-byte. */
+csa2_status csa2_attn_mass(const csa2_cache *cache, const csa2_pages *pages,
+                           const csa2_groups *groups, const int32_t *pos, int64_t max_n,
+                           const void *q, csa2_dtype q_type, int32_t H, float sm_scale,
+                           const float *lse, const float *prev, float decay, float *mass,
+                           int64_t ld_mass, void *workspace, size_t ws_bytes,
+                           uint32_t *counters, void *stream);
+size_t csa2_mass_workspace_size(int32_t batch, int32_t ng, int32_t nq, int32_t H,
+                                int64_t max_n);
+
+/* ---- 14. eviction ---------------------------------------------------------------------
+ * Sequence b of `cache` (n = seq_len[b] entries) is cut to min(n, keep) entries: its
+ * first n_first, its last n_last, and of those between the ones with the largest
+ * mass[b][j] (ties to the lower entry; -0 equals 0; NaN counts as the smallest).
+ * They are copied in order, indexer keys included, to the entries 0, 1, ... of
+ * sequence b of `dst`, whose seq_len[b] becomes their number.  The old entries stay
+ * as they were: dst may be the same arrays with other pages (whose old ones are
+ * then free, or still another sequence's), and its seq_len the same array.
+ *   seq [ns]: the sequences to cut, or NULL for all (ns == cache->batch); ns at most 65535;
+ *   kept [ns][ld_kept]: the old entry numbers, ascending, ld_kept >= keep; the
+ *   places from the new length on are left as they were;
+ *   mass [batch][ld_mass], ld_mass >= max_n; mass_out [batch][ld_out] (nullable,
+ *   ld_out >= keep): the kept entries' mass, sequence by sequence;
+ *   max_n: host bound on every n; keep >= 1, n_first + n_last <= keep;
+ *   dst: as many sequences, keys if and only if `cache` has them, of the same d_idx.
+ * Sequences outside the contract (number, n < 0 or above max_n, pages or room too
+ * few on either side) are skipped, counted in CSA2_CNT_BAD_INPUT (room: in
+ * CSA2_CNT_CAPACITY), and their seq_len left.  Rows that the call writes must not be
+ * among those it reads, nor mass_out overlap mass (refused).
+ * kept, mass, mass_out: 4-byte aligned; workspace 16-byte. */
+csa2_status csa2_cache_evict(const csa2_cache *cache, const csa2_pages *pages,
+                             const csa2_cache *dst, const csa2_pages *dst_pages,
+                             const int32_t *seq, int32_t ns, const float *mass, int64_t ld_mass,
+                             int64_t max_n, int32_t keep, int32_t n_first, int32_t n_last,
+                             int32_t *kept, int64_t ld_kept, float *mass_out, int64_t ld_out,
+                             void *workspace, size_t ws_bytes, uint32_t *counters, void *stream);
+size_t csa2_evict_workspace_size(int32_t ns, int64_t max_n);
 
 /* ---- workspace sizes (host-only, no GPU work) ------------------------------ */
 /* (0 for sizes that csa2_dense_attn refuses) */

@@ -33,7 +33,8 @@ EXPORTS = ["csa2_quantize_append", "csa2_quantize_append_project", "csa2_index_f
            "csa2_topk_workspace_size", "csa2_attn_workspace_size", "csa2_layer_workspace_size",
            "csa2_status_string", "csa2_launch_count", "csa2_topk_noalloc",
            "csa2_topk_noalloc_max_scratch", "csa2_cache_write", "csa2_cache_read",
-           "csa2_dense_attn", "csa2_dense_workspace_size"]
+           "csa2_dense_attn", "csa2_dense_workspace_size", "csa2_norm_rope", "csa2_chunk_attn",
+           "csa2_attn_mass", "csa2_mass_workspace_size", "csa2_cache_evict", "csa2_evict_workspace_size"]
 
 
 class CsaError(RuntimeError):
@@ -55,6 +56,10 @@ class _Queries(ctypes.Structure):
 class _Groups(ctypes.Structure):
     _fields_ = [("seq", ctypes.c_void_p), ("off", ctypes.c_void_p), ("len", ctypes.c_void_p),
                 ("ng", ctypes.c_int32), ("nq", ctypes.c_int32)]
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("ld", ctypes.c_int64), ("page", ctypes.c_int32)]
 
 
 class _LayerArgs(ctypes.Structure):
@@ -99,6 +104,13 @@ def lib() -> ctypes.CDLL:
                 "csa2_cache_read": [vp, vp, i64, vp, i32, i64, vp, i64, vp, vp],
                 "csa2_dense_attn": [vp, vp, i64, vp, i32, i32, ctypes.c_float, vp, vp, vp, i32, vp,
                                     vp, sz, vp, vp],
+                "csa2_norm_rope": [vp, i32, i64, i64, i32, vp, ctypes.c_float, vp, vp, i32, i32, vp, i32, i64, vp],
+                "csa2_chunk_attn": [vp, vp, vp, vp, i64, vp, i32, i32, ctypes.c_float, vp, vp, vp, i32, vp,
+                                    vp, sz, vp, vp],
+                "csa2_attn_mass": [vp, vp, vp, vp, i64, vp, i32, i32, ctypes.c_float, vp, vp, ctypes.c_float, vp, i64,
+                                   vp, sz, vp, vp],
+                "csa2_cache_evict": [vp, vp, vp, vp, vp, i32, vp, i64, i64, i32, i32, i32, vp, i64, vp, i64,
+                                     vp, sz, vp, vp],
             }
             for name, args in sig.items():
                 f = getattr(L, name)
@@ -114,6 +126,10 @@ def lib() -> ctypes.CDLL:
             L.csa2_layer_workspace_size.restype = sz
             L.csa2_dense_workspace_size.argtypes = [i32, i32, i32, i64]
             L.csa2_dense_workspace_size.restype = sz
+            L.csa2_mass_workspace_size.argtypes = [i32, i32, i32, i32, i64]
+            L.csa2_mass_workspace_size.restype = sz
+            L.csa2_evict_workspace_size.argtypes = [i32, i64]
+            L.csa2_evict_workspace_size.restype = sz
             L.csa2_status_string.argtypes = [ctypes.c_int]
             L.csa2_status_string.restype = ctypes.c_char_p
             L.csa2_launch_count.argtypes = []
@@ -175,7 +191,8 @@ class Cache:
         """A cache over tensors that the caller already holds (nothing is copied):
         codes [cap][256], scales [cap][32], kidx [cap][d_idx] uint8, kscale [cap]
         fp32, seq_base [batch + 1] int64, seq_len [batch] int32, cap a multiple of 8.
-        kidx and kscale may be None for a cache that is only attended."""
+        kidx and kscale may be None for a cache that is only attended, seq_base for
+        one whose sequences lie in pages (Pages)."""
         c = cls.__new__(cls)
         c.cap, c.batch, c.d_idx = (_ext or _load_ext()).check_cache(codes, scales, kidx, kscale, seq_base, seq_len)
         c.m = m
@@ -186,6 +203,8 @@ class Cache:
     def struct(self, seq=None) -> _Cache:
         """The C struct; with seq = b, a one-sequence view of sequence b."""
         keys = (None, None) if self.kidx is None else (self.kidx.data_ptr(), self.kscale.data_ptr())
+        if self.seq_base is None:
+            raise CsaError("the cache has no seq_base: its sequences lie in pages")
         if seq is None:
             return _Cache(self.codes.data_ptr(), self.scales.data_ptr(), *keys,
                           self.seq_base.data_ptr(), self.seq_len.data_ptr(),
@@ -220,6 +239,26 @@ class Groups:
         self.ng = self.seq.numel()
         if self.off.numel() != self.ng + 1 or (length is not None and self.length.numel() != self.ng):
             raise CsaError("groups need seq [ng], off [ng + 1] and length [ng]")
+
+
+class Pages:
+    """Where the sequences of a cache lie that are given pages as they grow: entry j of
+    sequence b is row table[b][j // page] * page + j % page.  table: int32 [batch][pages]
+    (what lies behind a sequence's pages may be anything), page: a power of two from 16 on."""
+
+    def __init__(self, table, page: int, device="cuda"):
+        if not (isinstance(table, torch.Tensor) and table.dtype == torch.int32 and table.is_contiguous() and
+                (table.is_cuda or torch.device(device).type == "cpu")):
+            table = torch.as_tensor(table, dtype=torch.int32).to(device).contiguous()
+        page = int(page)
+        if table.dim() != 2 or page < 16 or page & (page - 1):
+            raise CsaError("pages need a table [sequences][pages] and a power of two of entries per page, 16 or more")
+        self.table, self.page = table, page
+
+    def rows(self, seq, entry):
+        """Cache rows of entries `entry` of sequences `seq` (integer tensors), for cache_write and cache_read."""
+        entry = entry.long()
+        return self.table[seq.long(), entry // self.page].long() * self.page + entry % self.page
 
 
 def new_counters(device="cuda"):
@@ -377,6 +416,76 @@ def dense_attn(cache: Cache, groups: Groups, q, out, lse=None, *, prev=None, sm_
     except (AttributeError, TypeError, ValueError) as e:
         raise CsaError("dense_attn: groups must be Groups, prev a pair (out, lse)") from e
     (_ext or _load_ext()).dense_attn(cache, seq, off, length, q, out, lse, po, pl, sm_scale, max_n, ws, counters)
+
+
+def norm_rope(x, out, *, weight=None, eps=1e-6, pos=None, inv_freq=None, halves=False):
+    """RMS norm of every row of x [n][H][512] or [n][512] (fp32, bf16 or f16; a token's heads
+    side by side, tokens any multiple of 16 bytes apart), times weight [512] (fp32), and the
+    rotation of its last 2 * len(inv_freq) channels (a multiple of 16) by the angles
+    pos[i] * inv_freq (int32 [n], fp32), into out, which may be x.  Pairs are neighbours, or
+    with halves=True half the rotated channels apart."""
+    (_ext or _load_ext()).norm_rope(x, out, weight, eps, pos, inv_freq, halves)
+
+
+def _of_groups(groups, pages):
+    try:
+        table, page = (None, 0) if pages is None else (pages.table, pages.page)
+        return groups.seq, groups.off, groups.length, table, page
+    except AttributeError as e:
+        raise CsaError("groups must be Groups, pages Pages") from e
+
+
+def chunk_attn(cache: Cache, groups: Groups, q, out, lse=None, *, pos=None, pages=None, prev=None,
+               sm_scale=1.0, max_n=None, ws=None, counters=None):
+    """Attention of chunks of new tokens: like dense_attn, but group g's queries are consecutive
+    tokens of its sequence from token position pos[g] (int32 [groups]) on, and each sees the
+    entries up to its own, (position + 1) // m of them; their entries are in the cache already.
+    pos=None: all see everything.  pages: a Pages, if the sequences lie in pages."""
+    seq, off, length, table, page = _of_groups(groups, pages)
+    try:
+        po, pl = prev if prev is not None else (None, None)
+    except (TypeError, ValueError) as e:
+        raise CsaError("chunk_attn: prev must be a pair (out, lse)") from e
+    (_ext or _load_ext()).chunk_attn(cache, seq, off, length, pos, table, page, q, out, lse, po, pl, sm_scale, max_n, ws,
+                                     counters)
+
+
+def mass_workspace_size(batch, ng, nq, H, max_n) -> int:
+    return int(lib().csa2_mass_workspace_size(batch, ng, nq, H, max_n))
+
+
+def attn_mass(cache: Cache, groups: Groups, q, lse, mass, *, pos=None, pages=None, prev=None, decay=1.0,
+              sm_scale=1.0, max_n=None, ws=None, counters=None):
+    """How much weight the queries of each group gave to each entry of its sequence, with the
+    log sums lse [nq][H] that the attention left: mass[b][j] = decay * prev[b][j] + the sum over
+    queries and heads (mass, prev fp32 [sequences][entries]; prev may be mass, None: nothing
+    before).  groups, pos and pages as in chunk_attn; a sequence is in one group at most."""
+    seq, off, length, table, page = _of_groups(groups, pages)
+    (_ext or _load_ext()).attn_mass(cache, seq, off, length, pos, table, page, q, lse, prev, decay, mass, sm_scale, max_n, ws,
+                                    counters)
+
+
+def evict_workspace_size(ns, max_n) -> int:
+    return int(lib().csa2_evict_workspace_size(ns, max_n))
+
+
+def cache_evict(cache: Cache, to: Cache, mass, keep, kept, mass_out=None, *, first=0, last=0, seq=None, pages=None,
+                to_pages=None, max_n=None, ws=None, counters=None):
+    """Cuts sequences (seq: int32 [ns]; None: all) to `keep` entries: the first `first`, the last
+    `last`, and the rest by mass [sequences][entries] (ties to the lower entry).  They are copied
+    in order to the entries 0, 1, .. of the same sequence of `to`, whose seq_len is set: the
+    same tensors with other pages (to_pages), or another cache.  kept int32 [ns][keep] receives
+    the old entry numbers, mass_out [sequences][keep] their mass.  max_n bounds the entries of
+    any sequence (default: mass's width)."""
+    def of(p):
+        if p is None:
+            return None, 0
+        try:
+            return p.table, p.page
+        except AttributeError as e:
+            raise CsaError("cache_evict: pages and to_pages must be Pages") from e
+    (_ext or _load_ext()).cache_evict(cache, to, mass, keep, kept, mass_out, first, last, seq, *of(pages), *of(to_pages), max_n,
+                                      ws, counters)
 
 
 class Layer:

@@ -25,7 +25,7 @@ EXT_PATH = os.path.join(OUT_DIR, "csa2_torch.so")
 EXT_STAMP = os.path.join(OUT_DIR, "csa2_torch.for")     # what EXT_PATH was built for
 
 SOURCES = ["csa2_api.cu", "csa2_append.cu", "csa2_index.cu", "csa2_topk.cu", "csa2_attn_tc.cu",
-           "csa2_rows.cu", "csa2_dense.cu"]
+           "csa2_rows.cu", "csa2_dense.cu", "csa2_mass.cu", "csa2_evict.cu", "csa2_rope.cu"]
 HEADERS = ["csa2_device.cuh", "csa2_attn_device.cuh", "csa2_internal.h"]
 EXT_SOURCE = "csa2_torch.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

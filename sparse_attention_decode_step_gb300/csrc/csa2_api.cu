@@ -131,10 +131,10 @@ inline bool al8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) ==
         if (!(cond)) return (code); \
     } while (0)
 
-csa2_status check_cache(const csa2_cache *c, bool need_keys)
+csa2_status check_cache(const csa2_cache *c, bool need_keys, bool need_base = true)
 {
     CSA2_REQUIRE(c != nullptr, CSA2_ERR_INVALID_ARG);
-    CSA2_REQUIRE(c->codes && c->scales && c->seq_base && c->seq_len, CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(c->codes && c->scales && (c->seq_base || !need_base) && c->seq_len, CSA2_ERR_INVALID_ARG);
     CSA2_REQUIRE(c->batch > 0 && c->m >= 1 && c->cap > 0, CSA2_ERR_INVALID_ARG);
     CSA2_REQUIRE(c->cap % 8 == 0 && c->cap < (1LL << 31), CSA2_ERR_INVALID_ARG);
     CSA2_REQUIRE(al16(c->codes) && al16(c->scales) && al8(c->seq_base) && al4(c->seq_len),
@@ -144,6 +144,15 @@ csa2_status check_cache(const csa2_cache *c, bool need_keys)
         CSA2_REQUIRE(al16(c->kidx) && al16(c->kscale), CSA2_ERR_ALIGN);
         CSA2_REQUIRE(c->d_idx == 64 || c->d_idx == 128, CSA2_ERR_UNSUPPORTED);
     }
+    return CSA2_OK;
+}
+
+csa2_status check_pages(const csa2_pages *p)
+{
+    if (p == nullptr) return CSA2_OK;
+    CSA2_REQUIRE(p->table && p->ld >= 1 && p->ld < (1LL << 31), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(p->page >= 16 && (p->page & (p->page - 1)) == 0, CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(al4(p->table), CSA2_ERR_ALIGN);
     return CSA2_OK;
 }
 
@@ -561,7 +570,7 @@ namespace {
 csa2_status check_rows(const csa2_cache *cache, const int64_t *rows, int64_t n, const void *x, csa2_dtype type,
                        int64_t ld_x, const void *key, int64_t ld_key, int key_bytes, const uint32_t *counters)
 {
-    csa2_status s = check_cache(cache, key != nullptr);
+    csa2_status s = check_cache(cache, key != nullptr, false);     // (rows are named by number)
     if (s != CSA2_OK) return s;
     CSA2_REQUIRE(type == CSA2_F32 || type == CSA2_BF16 || type == CSA2_F16, CSA2_ERR_UNSUPPORTED);
     CSA2_REQUIRE(n >= 0 && n <= (1LL << 31), CSA2_ERR_INVALID_ARG);
@@ -608,6 +617,17 @@ bool dense_sizes_ok(int64_t ng, int64_t nq, int64_t H, int64_t max_n)
     return H >= 1 && H <= 128 && nq * H < (1LL << 30) && ng < (1 << 24) && max_n >= 0 && max_n < (1LL << 31);
 }
 
+PageMap pages_of(const csa2_pages *p, int64_t cap)
+{
+    PageMap m{};
+    if (p == nullptr) return m;
+    m.table = p->table;
+    m.ld = p->ld;
+    m.log = __builtin_ctz((unsigned)p->page);
+    m.pages = (uint32_t)(cap >> m.log);
+    return m;
+}
+
 }  // namespace
 
 size_t csa2_dense_workspace_size(int32_t ng, int32_t nq, int32_t H, int64_t max_n)
@@ -616,24 +636,37 @@ size_t csa2_dense_workspace_size(int32_t ng, int32_t nq, int32_t H, int64_t max_
     return dense_plan(ng, nq, H, max_n).total;
 }
 
-csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, int64_t max_n, const void *q,
-                            csa2_dtype q_type, int32_t H, float sm_scale, const float *prev_out,
-                            const float *prev_lse, void *out, csa2_dtype out_type, float *lse, void *workspace,
-                            size_t ws_bytes, uint32_t *counters, void *stream)
+namespace {
+
+csa2_status check_groups(const csa2_groups *groups, int64_t max_n, const void *q, csa2_dtype q_type, int32_t H)
 {
-    csa2_status s = check_cache(cache, false);
+    CSA2_REQUIRE(groups->seq && groups->off && (q || groups->nq == 0), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(max_n >= 0 && max_n < (1LL << 31), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(H >= 1 && H <= 128 && (q_type == CSA2_BF16 || q_type == CSA2_F16), CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(dense_sizes_ok(groups->ng, groups->nq, H, max_n), CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(al4(groups->seq) && al4(groups->off) && (groups->len == nullptr || al4(groups->len)) && al16(q),
+                 CSA2_ERR_ALIGN);
+    return CSA2_OK;
+}
+
+// csa2_dense_attn and csa2_chunk_attn (`chunk`, which pages and pos belong to).
+csa2_status group_attn(const csa2_cache *cache, bool chunk, const csa2_pages *pages, const csa2_groups *groups,
+                       const int32_t *pos, int64_t max_n, const void *q, csa2_dtype q_type, int32_t H, float sm_scale,
+                       const float *prev_out, const float *prev_lse, void *out, csa2_dtype out_type, float *lse,
+                       void *workspace, size_t ws_bytes, uint32_t *counters, void *stream)
+{
+    csa2_status s = check_cache(cache, false, pages == nullptr);
+    if (s == CSA2_OK) s = check_pages(pages);
     if (s != CSA2_OK) return s;
     CSA2_REQUIRE(groups != nullptr && groups->ng >= 0 && groups->nq >= 0, CSA2_ERR_INVALID_ARG);
     if (groups->ng == 0 || groups->nq == 0) return CSA2_OK;
-    CSA2_REQUIRE(groups->seq && groups->off && q && out, CSA2_ERR_INVALID_ARG);
-    CSA2_REQUIRE(max_n >= 0 && max_n < (1LL << 31), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(out, CSA2_ERR_INVALID_ARG);
     CSA2_REQUIRE((prev_out == nullptr) == (prev_lse == nullptr), CSA2_ERR_INVALID_ARG);
-    CSA2_REQUIRE(H >= 1 && H <= 128 && (q_type == CSA2_BF16 || q_type == CSA2_F16), CSA2_ERR_UNSUPPORTED);
+    s = check_groups(groups, max_n, q, q_type, H);
+    if (s != CSA2_OK) return s;
     CSA2_REQUIRE(out_type == CSA2_F32 || out_type == CSA2_BF16 || out_type == CSA2_F16, CSA2_ERR_UNSUPPORTED);
-    CSA2_REQUIRE(dense_sizes_ok(groups->ng, groups->nq, H, max_n), CSA2_ERR_UNSUPPORTED);
-    CSA2_REQUIRE(al4(groups->seq) && al4(groups->off) && (groups->len == nullptr || al4(groups->len)) && al16(q) &&
-                     al16(out) && (prev_out == nullptr || (al16(prev_out) && al4(prev_lse))) &&
-                     (lse == nullptr || al4(lse)) && (counters == nullptr || al4(counters)),
+    CSA2_REQUIRE(al16(out) && (prev_out == nullptr || (al16(prev_out) && al4(prev_lse))) && (lse == nullptr || al4(lse)) &&
+                     (pos == nullptr || al4(pos)) && (counters == nullptr || al4(counters)),
                  CSA2_ERR_ALIGN);
     const DensePlan pl = dense_plan(groups->ng, groups->nq, H, max_n);
     CSA2_REQUIRE(workspace, CSA2_ERR_INVALID_ARG);
@@ -665,7 +698,185 @@ csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, 
     p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + pl.off_ml);
     p.begin = reinterpret_cast<DenseBegin *>(static_cast<uint8_t *>(workspace) + pl.off_begin);
     p.counters = counters;
-    return cuda_status(launch_dense(p, out_type, static_cast<cudaStream_t>(stream)));
+    if (!chunk) return cuda_status(launch_dense(p, out_type, static_cast<cudaStream_t>(stream)));
+    p.pos = pos;
+    p.m = cache->m;
+    p.pages = pages_of(pages, cache->cap);
+    return cuda_status(launch_chunk(p, out_type, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+csa2_status csa2_dense_attn(const csa2_cache *cache, const csa2_groups *groups, int64_t max_n, const void *q,
+                            csa2_dtype q_type, int32_t H, float sm_scale, const float *prev_out,
+                            const float *prev_lse, void *out, csa2_dtype out_type, float *lse, void *workspace,
+                            size_t ws_bytes, uint32_t *counters, void *stream)
+{
+    return group_attn(cache, false, nullptr, groups, nullptr, max_n, q, q_type, H, sm_scale, prev_out, prev_lse, out,
+                      out_type, lse, workspace, ws_bytes, counters, stream);
+}
+
+csa2_status csa2_chunk_attn(const csa2_cache *cache, const csa2_pages *pages, const csa2_groups *groups,
+                            const int32_t *pos, int64_t max_n, const void *q, csa2_dtype q_type, int32_t H,
+                            float sm_scale, const float *prev_out, const float *prev_lse, void *out,
+                            csa2_dtype out_type, float *lse, void *workspace, size_t ws_bytes, uint32_t *counters,
+                            void *stream)
+{
+    return group_attn(cache, true, pages, groups, pos, max_n, q, q_type, H, sm_scale, prev_out, prev_lse, out, out_type,
+                      lse, workspace, ws_bytes, counters, stream);
+}
+
+// ---------------------------------------------------------------- attention weights by entry
+size_t csa2_mass_workspace_size(int32_t batch, int32_t ng, int32_t nq, int32_t H, int64_t max_n)
+{
+    if (batch < 1 || ng < 1 || nq < 0 || !dense_sizes_ok(ng, nq, H, max_n)) return 0;
+    return mass_plan(batch, ng, nq, H, max_n).total;
+}
+
+csa2_status csa2_attn_mass(const csa2_cache *cache, const csa2_pages *pages, const csa2_groups *groups,
+                           const int32_t *pos, int64_t max_n, const void *q, csa2_dtype q_type, int32_t H,
+                           float sm_scale, const float *lse, const float *prev, float decay, float *mass,
+                           int64_t ld_mass, void *workspace, size_t ws_bytes, uint32_t *counters, void *stream)
+{
+    csa2_status s = check_cache(cache, false, pages == nullptr);
+    if (s == CSA2_OK) s = check_pages(pages);
+    if (s != CSA2_OK) return s;
+    CSA2_REQUIRE(groups != nullptr && groups->ng >= 0 && groups->nq >= 0, CSA2_ERR_INVALID_ARG);
+    if (groups->ng == 0) return CSA2_OK;
+    CSA2_REQUIRE((lse || groups->nq == 0) && mass, CSA2_ERR_INVALID_ARG);
+    s = check_groups(groups, max_n, q, q_type, H);
+    if (s != CSA2_OK) return s;
+    CSA2_REQUIRE(ld_mass >= max_n && ld_mass < (1LL << 31), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(al4(lse) && al4(mass) && (prev == nullptr || al4(prev)) && (pos == nullptr || al4(pos)) &&
+                     (counters == nullptr || al4(counters)),
+                 CSA2_ERR_ALIGN);
+    const MassPlan pl = mass_plan(cache->batch, groups->ng, groups->nq, H, max_n);
+    CSA2_REQUIRE(workspace, CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(al16(workspace), CSA2_ERR_ALIGN);
+    CSA2_REQUIRE(ws_bytes >= pl.total, CSA2_ERR_CAPACITY);
+    MassParams p{};
+    p.codes = cache->codes;
+    p.scales = cache->scales;
+    p.seq_base = cache->seq_base;
+    p.seq_len = cache->seq_len;
+    p.cap = cache->cap;
+    p.batch = cache->batch;
+    p.pages = pages_of(pages, cache->cap);
+    p.g_seq = groups->seq;
+    p.g_off = groups->off;
+    p.g_len = groups->len;
+    p.pos = pos;
+    p.m = cache->m;
+    p.ng = groups->ng;
+    p.nq = groups->nq;
+    p.H = H;
+    p.max_n = max_n;
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_type = q_type;
+    p.sm_scale = sm_scale;
+    p.lse = lse;
+    p.prev = prev;
+    p.decay = decay;
+    p.mass = mass;
+    p.ld_mass = ld_mass;
+    p.plan = pl;
+    p.ws = static_cast<uint8_t *>(workspace);
+    p.counters = counters;
+    return cuda_status(launch_mass(p, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- eviction
+size_t csa2_evict_workspace_size(int32_t ns, int64_t max_n)
+{
+    if (ns < 1 || max_n < 0 || max_n >= (1LL << 31)) return 0;
+    return evict_plan(ns, max_n).total;
+}
+
+csa2_status csa2_cache_evict(const csa2_cache *cache, const csa2_pages *pages, const csa2_cache *dst,
+                             const csa2_pages *dst_pages, const int32_t *seq, int32_t ns, const float *mass,
+                             int64_t ld_mass, int64_t max_n, int32_t keep, int32_t n_first, int32_t n_last,
+                             int32_t *kept, int64_t ld_kept, float *mass_out, int64_t ld_out, void *workspace,
+                             size_t ws_bytes, uint32_t *counters, void *stream)
+{
+    const bool keys = cache != nullptr && cache->kidx != nullptr;
+    csa2_status s = check_cache(cache, keys, pages == nullptr);
+    if (s == CSA2_OK) s = check_cache(dst, keys, dst_pages == nullptr);
+    if (s == CSA2_OK) s = check_pages(pages);
+    if (s == CSA2_OK) s = check_pages(dst_pages);
+    if (s != CSA2_OK) return s;
+    CSA2_REQUIRE(cache->batch == dst->batch && keys == (dst->kidx != nullptr) && (!keys || cache->d_idx == dst->d_idx),
+                 CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(ns <= 65535, CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(ns >= 0 && (seq != nullptr || ns == cache->batch), CSA2_ERR_INVALID_ARG);
+    if (ns == 0) return CSA2_OK;
+    CSA2_REQUIRE(mass && kept && max_n >= 0 && max_n < (1LL << 31), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(keep >= 1 && n_first >= 0 && n_last >= 0 && (int64_t)n_first + n_last <= keep, CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(ld_mass >= max_n && ld_mass < (1LL << 31) && ld_kept >= keep && ld_kept < (1LL << 31), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(al4(mass) && al4(kept) && (seq == nullptr || al4(seq)) && (mass_out == nullptr || al4(mass_out)) &&
+                     (counters == nullptr || al4(counters)),
+                 CSA2_ERR_ALIGN);
+    if (mass_out) {
+        CSA2_REQUIRE(ld_out >= keep && ld_out < (1LL << 31), CSA2_ERR_INVALID_ARG);
+        const uintptr_t a = reinterpret_cast<uintptr_t>(mass), b = reinterpret_cast<uintptr_t>(mass_out);
+        CSA2_REQUIRE(a + (size_t)cache->batch * ld_mass * 4 <= b || b + (size_t)cache->batch * ld_out * 4 <= a,
+                     CSA2_ERR_INVALID_ARG);
+    }
+    const EvictPlan pl = evict_plan(ns, max_n);
+    CSA2_REQUIRE(workspace, CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(al16(workspace), CSA2_ERR_ALIGN);
+    CSA2_REQUIRE(ws_bytes >= pl.total, CSA2_ERR_CAPACITY);
+    EvictParams p{};
+    p.src = *cache;
+    p.dst = *dst;
+    p.src_pages = pages_of(pages, cache->cap);
+    p.dst_pages = pages_of(dst_pages, dst->cap);
+    p.seq = seq;
+    p.ns = ns;
+    p.mass = mass;
+    p.ld_mass = ld_mass;
+    p.max_n = max_n;
+    p.keep = keep;
+    p.n_first = n_first;
+    p.n_last = n_last;
+    p.kept = kept;
+    p.ld_kept = ld_kept;
+    p.mass_out = mass_out;
+    p.ld_out = ld_out;
+    p.counters = counters;
+    return cuda_status(launch_evict(p, pl, static_cast<uint8_t *>(workspace), static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- norm and rotation
+csa2_status csa2_norm_rope(const void *x, csa2_dtype type, int64_t ld_x, int64_t n, int32_t H, const float *weight,
+                           float eps, const int32_t *pos, const float *inv_freq, int32_t rot, int32_t halves, void *out,
+                           csa2_dtype out_type, int64_t ld_out, void *stream)
+{
+    auto known = [](csa2_dtype t) { return t == CSA2_F32 || t == CSA2_BF16 || t == CSA2_F16; };
+    CSA2_REQUIRE(known(type) && known(out_type), CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(H >= 1 && H <= 128 && rot >= 0 && rot <= CSA2_D && rot % 16 == 0, CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(n >= 0 && n < (1LL << 31) && n * H < (1LL << 31) && eps >= 0.f, CSA2_ERR_INVALID_ARG);
+    if (n == 0) return CSA2_OK;
+    CSA2_REQUIRE(x && out && (rot == 0 || (pos && inv_freq)), CSA2_ERR_INVALID_ARG);
+    CSA2_REQUIRE(ld_x >= (int64_t)H * CSA2_D && ld_out >= (int64_t)H * CSA2_D && ld_x < (1LL << 31) && ld_out < (1LL << 31),
+                 CSA2_ERR_INVALID_ARG);
+    const int bx = type == CSA2_F32 ? 4 : 2, bo = out_type == CSA2_F32 ? 4 : 2;
+    CSA2_REQUIRE(al16(x) && al16(out) && (ld_x * bx) % 16 == 0 && (ld_out * bo) % 16 == 0 &&
+                     (weight == nullptr || al16(weight)) && (pos == nullptr || al4(pos)) && (inv_freq == nullptr || al4(inv_freq)),
+                 CSA2_ERR_ALIGN);
+    RopeParams p{};
+    p.x = x;
+    p.out = out;
+    p.ld_x = (uint32_t)ld_x;
+    p.ld_out = (uint32_t)ld_out;
+    p.n = (uint32_t)n;
+    p.H = (uint32_t)H;
+    p.weight = weight;
+    p.eps = eps;
+    p.pos = pos;
+    p.inv_freq = inv_freq;
+    p.rot = rot;
+    p.halves = halves != 0;
+    return cuda_status(launch_norm_rope(p, type, out_type, static_cast<cudaStream_t>(stream)));
 }
 
 const char *csa2_status_string(csa2_status s)

@@ -84,6 +84,9 @@ static_assert(kRowsPair == 128 && kEnt == 256, "lane and column maps below");
 // ------------------------------------------------------------------ groups and work
 // What a group asks for.  bad: its arguments are out of contract and its rows
 // are left as they are.
+// kChunk: the queries of a group are consecutive tokens, each of which sees the entries
+// up to its own (csa2_chunk_attn), and the entries may lie in pages.
+template <bool kChunk>
 struct Group {
     int base;            // cache row of entry 0 (a cache has under 2^31 rows)
     int row0;            // first row (query * H, under 2^30)
@@ -92,36 +95,114 @@ struct Group {
     bool bad;
     bool falls;          // its offsets do
 };
+template <>
+struct Group<true> : Group<false> {
+    int seq;
+    bool causal;
+    int pos;             // token position of its first query
+    int tile_n;          // (of a piece of work:) entries that some row of its row tile sees
+};
 
-__device__ __forceinline__ Group group_of(const DenseParams &p, int g)
+template <bool kChunk>
+__device__ __forceinline__ Group<kChunk> group_of(const DenseParams &p, int g)
 {
-    Group r{};
+    Group<kChunk> r{};
     const int b = p.g_seq[g], a = p.g_off[g], e = p.g_off[g + 1];
     r.falls = e < a;
     r.bad = b < 0 || b >= p.batch || a < 0 || e < a || e > p.nq;
     if (r.bad) return r;
     const int64_t len = p.seq_len[b];
     const int64_t n = p.g_len ? (int64_t)p.g_len[g] : len;
-    const int64_t base = p.seq_base[b];
-    r.bad = n < 0 || n > len || n > p.max_n || base < 0 || base + n > p.cap;
+    r.bad = n < 0 || n > len || n > p.max_n;
+    if (kChunk && p.pages.table != nullptr) {
+        r.bad = r.bad || n > p.pages.ld << p.pages.log;
+    } else {
+        const int64_t base = p.seq_base[b];
+        r.bad = r.bad || base < 0 || base + n > p.cap;
+        r.base = (int)base;
+    }
     if (r.bad) return r;
-    r.base = (int)base;
     r.n = (int)n;
     r.row0 = a * p.H;
     r.rows = (e - a) * p.H;
+    if constexpr (kChunk) {
+        r.seq = b;
+        r.causal = p.pos != nullptr;
+        if (r.causal) r.pos = p.pos[g];
+    }
     return r;
 }
 
-__device__ __forceinline__ int row_tiles(const Group &g) { return (g.rows + kRowsPair - 1) / kRowsPair; }
-__device__ __forceinline__ int ent_tiles(const Group &g) { return g.n / kEnt + (g.n % kEnt != 0); }
+template <bool kChunk>
+__device__ __forceinline__ int row_tiles(const Group<kChunk> &g) { return (g.rows + kRowsPair - 1) / kRowsPair; }
+__device__ __forceinline__ int tiles_of(int n) { return n / kEnt + (n % kEnt != 0); }
+
+// Entries that the k-th query of a group sees, and those that some row of a row tile
+// does (its last row: a later token sees no fewer).
+template <bool kChunk>
+__device__ __forceinline__ int sees(const DenseParams &p, const Group<kChunk> &g, int k)
+{
+    if constexpr (kChunk) {
+        if (g.causal) {
+            const int64_t t = (int64_t)g.pos + k + 1;              // (under 2^32)
+            if (t <= 0) return 0;
+            return (int)min((uint32_t)t / (uint32_t)p.m, (uint32_t)g.n);
+        }
+    }
+    return g.n;
+}
+
+template <bool kChunk>
+__device__ __forceinline__ int tile_sees(const DenseParams &p, const Group<kChunk> &g, int rt)
+{
+    if constexpr (kChunk) return sees(p, g, (min((rt + 1) * kRowsPair, g.rows) - 1) / p.H);
+    return g.n;
+}
+
+// The first row tile behind rt that has more than rt's kt tiles of entries: a query k sees
+// more than 256 kt entries from pos + k + 1 >= m (256 kt + 1) on.
+template <bool kChunk>
+__device__ __forceinline__ int next_longer(const DenseParams &p, const Group<kChunk> &g, int rt, int kt)
+{
+    const int tiles = row_tiles(g);
+    if constexpr (kChunk) {
+        if (tiles_of(tile_sees(p, g, tiles - 1)) > kt) {           // (so that query exists)
+            const int64_t k = (int64_t)p.m * ((int64_t)kEnt * kt + 1) - g.pos - 1;
+            return max(rt + 1, (int)(k * p.H / kRowsPair));
+        }
+    }
+    return tiles;
+}
+
+// Leading rows of a group whose tiles see nothing at all.
+template <bool kChunk>
+__device__ __forceinline__ int empty_count(const DenseParams &p, const Group<kChunk> &g)
+{
+    if (g.rows == 0 || tile_sees(p, g, 0) > 0) return 0;
+    return min(g.rows, next_longer(p, g, 0, 0) * kRowsPair);
+}
 
 // Work is counted in units: a tile of entries is one, and each row tile has
 // kSetup more in front for what a piece costs besides (queries, first scores,
 // epilogue: about as long as a tile).  A run that ends in those has no piece there.
 // (Without them 61 queries over five prompts of 1 to 20,011 entries take 36.5 us
 // instead of 26.0, four chunks of queries 49.3 instead of 37.8.)
-__device__ __forceinline__ int row_units(const Group &g) { return g.n > 0 ? ent_tiles(g) + kSetup : 0; }
-__device__ __forceinline__ int64_t units(const Group &g) { return (int64_t)row_tiles(g) * row_units(g); }   // (bad: 0)
+// Tokens see more and more: the row tiles of a group fall into stretches of equal length,
+// as many as the tiles of entries that its tokens themselves fill.
+__device__ __forceinline__ int row_units(int n) { return n > 0 ? tiles_of(n) + kSetup : 0; }
+
+template <bool kChunk>
+__device__ __forceinline__ int64_t units(const DenseParams &p, const Group<kChunk> &g)    // (bad: 0)
+{
+    if constexpr (!kChunk) return (int64_t)row_tiles(g) * row_units(g.n);
+    int64_t u = 0;
+    for (int rt = 0, next; rt < row_tiles(g); rt = next) {
+        const int n = tile_sees(p, g, rt);
+        next = next_longer(p, g, rt, tiles_of(n));
+        u += (int64_t)(next - rt) * row_units(n);
+    }
+    return u;
+}
 
 // a / b of non-negative numbers (a 32-bit division where it serves)
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
@@ -136,33 +217,40 @@ __device__ __forceinline__ int64_t run_units(const DenseParams &p, int64_t U) { 
 
 // One pair's pieces of work in order: entries k0 .. k1 (in tiles) of a row tile.
 // find() sets up the first piece.
+template <bool kChunk>
 struct Work {
-    Group gr;
+    Group<kChunk> gr;
     int g;
     int rt;              // row tile of the group
-    int kt;              // tiles of entries of the group
+    int kt;              // tiles of entries that some row of it sees
     int k0, k1;
     int at;              // the run's first unit within its row tile
     int64_t left;        // units left after this piece
 
     // From unit `at` of a row tile on, with `units` left; false: no piece.
-    __device__ __forceinline__ bool take(int at, int64_t units)
+    __device__ __forceinline__ bool take(const DenseParams &p, int at, int64_t units)
     {
-        kt = ent_tiles(gr);
+        if constexpr (kChunk) gr.tile_n = tile_sees(p, gr, rt);
+        kt = tiles_of(entries());
         const int n = (int)min((int64_t)(kt + kSetup - at), units);
         k0 = max(0, at - kSetup);
         k1 = max(0, at + n - kSetup);
         left = units - n;
         return k1 > k0;
     }
+    __device__ __forceinline__ int entries() const
+    {
+        if constexpr (kChunk) return gr.tile_n;
+        return gr.n;
+    }
     __device__ __forceinline__ bool next(const DenseParams &p)
     {
         if (left <= 0) return false;
         if (++rt == row_tiles(gr)) {
-            do { gr = group_of(p, ++g); } while (units(gr) == 0);      // (ends: units are left)
-            rt = 0;
+            do { gr = group_of<kChunk>(p, ++g); } while (units(p, gr) == 0);      // (ends: units are left)
+            rt = kChunk ? empty_count(p, gr) / kRowsPair : 0;
         }
-        return take(0, left);
+        return take(p, 0, left);
     }
 };
 
@@ -171,12 +259,13 @@ static_assert(kDensePairsMax < kMaxPieces && kMaxPieces == 96, "join's weights")
 static_assert(kJoinThreads == 512 && CSA2_D == 4 * 128, "join's shifts");
 
 // What a pair works on.
+template <bool kChunk>
 struct Found {
-    Work w;
+    Work<kChunk> w;
     int64_t run;         // units of a pair's run
     int64_t u0;          // this pair's first
     int work;            // whether it has a piece
-    int empty;           // some group has rows but no entries
+    int empty;           // some row tile has no entries
     int groups;          // groups before the first whose offsets fall: those behind it may share rows with them
 };
 
@@ -187,30 +276,31 @@ struct Found {
 // groups from there on are taken out and the sums made again.  Ends without a barrier.
 constexpr int kFindWarps = 16;
 
-__device__ __forceinline__ void find(const DenseParams &p, int pair, int tid, bool count_bad, int64_t *sums, Found *out)
+template <bool kChunk>
+__device__ __forceinline__ void find(const DenseParams &p, int pair, int tid, bool count_bad, int64_t *sums, Found<kChunk> *out)
 {
     const int lane = tid & 31, warp = tid >> 5;
     const bool few = p.ng <= 32;
     if (few && warp != 0) return;
     const int each = (p.ng + 32 * kFindWarps - 1) / (32 * kFindWarps);
     const int g0 = warp < kFindWarps ? min(tid * each, p.ng) : p.ng, g1 = min(g0 + each, p.ng);
-    Group gr{};
+    Group<kChunk> gr{};
     int64_t mine = 0;
     int empty = 0, fall = p.ng;
     for (int g = g0; g < g1; ++g) {
-        gr = group_of(p, g);
+        gr = group_of<kChunk>(p, g);
         if (gr.falls) fall = min(fall, g);
         if (gr.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
-        if (!gr.bad && gr.n == 0 && gr.rows > 0) empty = 1;
-        mine += units(gr);
+        if (!gr.bad && gr.rows > 0 && tile_sees(p, gr, 0) == 0) empty = 1;
+        mine += units(p, gr);
     }
     int groups = p.ng;                         // in contract as far as their offsets go
     auto drop = [&](int from) {                // the groups from `from` on count no more
         groups = from;
         for (int g = max(g0, from); g < g1; ++g) {
-            const Group x = group_of(p, g);
+            const Group<kChunk> x = group_of<kChunk>(p, g);
             if (!x.bad && count_bad) count_event(p.counters, CSA2_CNT_BAD_INPUT);
-            mine -= units(x);
+            mine -= units(p, x);
         }
     };
     auto warp_sum = [&]() {                    // inclusive
@@ -262,14 +352,25 @@ __device__ __forceinline__ void find(const DenseParams &p, int pair, int tid, bo
         if (left > 0) {
             int g = g0;
             if (each > 1) {
-                for (gr = group_of(p, g); u0 >= before + units(gr); gr = group_of(p, ++g)) before += units(gr);
+                for (gr = group_of<kChunk>(p, g); u0 >= before + units(p, gr); gr = group_of<kChunk>(p, ++g)) before += units(p, gr);
             }
-            Work &w = out->w;
+            Work<kChunk> &w = out->w;
             w.gr = gr;
             w.g = g;
-            w.rt = (int)quotient(u0 - before, row_units(gr));
-            w.at = (int)(u0 - before - (int64_t)w.rt * row_units(gr));
-            out->work = w.take(w.at, left);
+            int rt = 0, per = row_units(tile_sees(p, gr, 0));
+            if constexpr (kChunk) {
+                for (;;) {                         // the stretch of row tiles that holds u0 (it is in this group)
+                    const int next = next_longer(p, gr, rt, tiles_of(tile_sees(p, gr, rt)));
+                    if (u0 < before + (int64_t)(next - rt) * per) break;
+                    before += (int64_t)(next - rt) * per;
+                    rt = next;
+                    per = row_units(tile_sees(p, gr, rt));
+                }
+            }
+            const int in = (int)quotient(u0 - before, per);
+            w.rt = rt + in;
+            w.at = (int)(u0 - before - (int64_t)in * per);
+            out->work = w.take(p, w.at, left);
         }
     }
 }
@@ -460,12 +561,12 @@ __device__ __forceinline__ void finish_q(const DenseParams &p, uint8_t *sQ, int 
     if ((t & 31) == 0) arrive_at(q_bar + 8 * h);
 }
 
-// Rows of a group without entries: the caller's partial result, or nothing.
+// `rows` rows from row0 on that have no entries: the caller's partial result, or nothing.
 template <int kOut>
-__device__ __forceinline__ void empty_rows(const DenseParams &p, const Group &gr, int first, int step)
+__device__ __forceinline__ void empty_rows(const DenseParams &p, int row0, int rows, int first, int step)
 {
-    for (int64_t i = first; i < (int64_t)gr.rows * (CSA2_D / 4); i += step) {
-        const int64_t row = gr.row0 + i / (CSA2_D / 4);
+    for (int64_t i = first; i < (int64_t)rows * (CSA2_D / 4); i += step) {
+        const int64_t row = row0 + i / (CSA2_D / 4);
         const int c = (int)(i % (CSA2_D / 4)) * 4;
         const float pl = p.prev_out ? p.prev_lse[row] : -INFINITY;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -475,7 +576,7 @@ __device__ __forceinline__ void empty_rows(const DenseParams &p, const Group &gr
     }
 }
 
-template <int kOut>
+template <int kOut, bool kChunk>
 __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 {
     const int tid = threadIdx.x, lane = tid & 31;
@@ -501,7 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     uint64_t *bar_done = bars + 22;            // (first CTA's) every MMA done
     int *sFlag = reinterpret_cast<int *>(bars + 23);         // [0] abort
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(sFlag + 1);
-    Found *sFound = reinterpret_cast<Found *>(bars + 24);
+    using Piece = Work<kChunk>;
+    Found<kChunk> *sFound = reinterpret_cast<Found<kChunk> *>(bars + 24);
     volatile int *abort_flag = sFlag;
 
     if (tid == 0) {
@@ -533,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem = *sTmem;
-    Work w = sFound->w;
+    Piece w = sFound->w;
     if (tid == 32 * (kWarpsSoft + kWarpsProd) && rank == 0) {
         // for the join: the row tile that this pair begins in
         DenseBegin d{};
@@ -548,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
     }
     bool more = sFound->work != 0;
     // A row tile's rows are halved between the CTAs: the first of this one's, in the tile
-    auto row_split = [&](const Work &x) { return (int)rank * ((min(kRowsPair, x.gr.rows - x.rt * kRowsPair) + 1) >> 1); };
-    auto row_count = [&](const Work &x) {
+    auto row_split = [&](const Piece &x) { return (int)rank * ((min(kRowsPair, x.gr.rows - x.rt * kRowsPair) + 1) >> 1); };
+    auto row_count = [&](const Piece &x) {
         const int n = min(kRowsPair, x.gr.rows - x.rt * kRowsPair);
         return rank == 0 ? (n + 1) >> 1 : n >> 1;
     };
@@ -662,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         uint32_t gs[4 * kStages];
         for (; more && ok; more = w.next(p)) {
             const int n_tiles = w.k1 - w.k0, n_blocks = 2 * n_tiles;
-            const int n_left = w.gr.n - w.k0 * kEnt;                     // entries from the piece's first on
+            const int n_left = w.entries() - w.k0 * kEnt;                // entries from the piece's first on
             const int64_t first = (int64_t)w.gr.base + w.k0 * kEnt;
             const uint8_t *const codes = p.codes + first * CSA2_CODE_BYTES;
             const uint8_t *const scales = p.scales + first * CSA2_SCALE_BYTES;
@@ -672,6 +774,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             const uint8_t *c0 = nullptr, *s0 = nullptr;
             int c_step = 0, s_step = 0, left = 0, left_s = 0;
             bool inside = true;                // the whole tile lies inside the sequence
+            // In pages a warp's 16 entries of a stage lie in one (a page holds a multiple of 16
+            // from a multiple of 16 on); its number is asked for a stage before it is needed.
+            const bool paged = kChunk && p.pages.table != nullptr;
+            const int32_t *table = nullptr;
+            int page[2] = {}, e_warp = 0, e_step = 0, ch_lane = 0;
+            if constexpr (kChunk) {
+                if (paged) table = p.pages.table + (int64_t)w.gr.seq * p.pages.ld;
+            }
             auto begin = [&](int b) {
                 const bool k = b == 0 || ((b & 1) != 0 && b != n_blocks - 1);
                 const int tile = b == 0 ? 0 : b == n_blocks - 1 ? n_tiles - 1 : (b & 1) ? (b + 1) >> 1 : (b >> 1) - 1;
@@ -684,14 +794,36 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 c_step = k ? 128 : 128 * CSA2_CODE_BYTES;
                 s_step = k ? 16 : 128 * CSA2_SCALE_BYTES;
                 left_s = k ? 0 : 128;
+                if constexpr (kChunk) {
+                    if (paged) {
+                        e_warp = e - e4 + w.k0 * kEnt;             // of the sequence
+                        e_step = k ? 0 : 128;
+                        ch_lane = ch;
+                        page[0] = left + e4 > 0 ? __ldg(table + (e_warp >> p.pages.log)) : 0;
+                        page[1] = k ? page[0] : left + e4 > 128 ? __ldg(table + ((e_warp + 128) >> p.pages.log)) : 0;
+                    }
+                }
             };
             auto load = [&](int s) {
                 const uint8_t *c = c0 + s * c_step, *sc = s0 + s * s_step;
+                int in = 0;                                        // (kChunk) entries from the lane's first on
+                if constexpr (kChunk) {
+                    in = left - left_s * s;
+                    if (paged) {
+                        const int64_t row = ((int64_t)page[s] << p.pages.log) + ((e_warp + e_step * s) & ((1 << p.pages.log) - 1)) + e4;
+                        c = p.codes + row * CSA2_CODE_BYTES + (ch_lane >> 1) + (e_step == 0 ? 128 * s : 0);
+                        sc = p.scales + row * CSA2_SCALE_BYTES + (ch_lane >> 4) + (e_step == 0 ? 16 * s : 0);
+                        if ((uint32_t)page[s] >= p.pages.pages) {        // no page of the cache: nothing is read
+                            if (in + e4 > 0 && lane == 0) count_event(p.counters, CSA2_CNT_BAD_INPUT);
+                            in = 0;
+                        }
+                    }
+                }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     uint4 v = make_uint4(0, 0, 0, 0);
                     uint32_t t = 0;
-                    if (inside || left_s * s + 4 * u < left) {
+                    if (kChunk ? 4 * u < in : inside || left_s * s + 4 * u < left) {
                         v = __ldg(reinterpret_cast<const uint4 *>(c + 4 * u * CSA2_CODE_BYTES));
                         t = __ldg(reinterpret_cast<const uint16_t *>(sc + 4 * u * CSA2_SCALE_BYTES));
                     }
@@ -776,7 +908,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             soft_sync();
             float l = 0.f;
             const int n_tiles = w.k1 - w.k0;
-            const int n_left = w.gr.n - w.k0 * kEnt;              // entries from the piece's first on
+            int n_left = w.entries() - w.k0 * kEnt;               // entries from the piece's first on
+            if constexpr (kChunk) n_left = sees(p, w.gr, min(r0 + row, w.gr.rows - 1) / p.H) - w.k0 * kEnt;   // of this row
             for (int i = 0; i < n_tiles; ++i, ++tile) {
                 const uint32_t tS = tmem + kColS + 128 * (tile & 1) + 64 * ch + lane_q;
                 bool got = mbar_wait<true>(&bar_s[tile & 1], (tile >> 1) & 1, abort_flag);
@@ -972,12 +1105,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         pdl_trigger();
         if (!ok && lane == 0) raise_abort(sFlag);
     }
-    // groups without entries
+    // rows without entries
     if (sFound->empty && warp != kWarpsSoft + kWarpsProd)
         for (int g = pair; g < sFound->groups; g += p.pairs) {
-            const Group gr = group_of(p, g);
-            if (!gr.bad && gr.n == 0)
-                empty_rows<kOut>(p, gr, (int)rank * 32 * (kWarpsSoft + kWarpsProd) + tid, 2 * 32 * (kWarpsSoft + kWarpsProd));
+            const Group<kChunk> gr = group_of<kChunk>(p, g);
+            if (!gr.bad)
+                empty_rows<kOut>(p, gr.row0, empty_count(p, gr), (int)rank * 32 * (kWarpsSoft + kWarpsProd) + tid, 2 * 32 * (kWarpsSoft + kWarpsProd));
         }
     tc_fence_before();
     __syncthreads();
@@ -1138,10 +1271,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) dense_join_kernel(DenseParams
 
 }  // namespace
 
-template <int kOut>
+template <int kOut, bool kChunk>
 static cudaError_t launch_dense_as(const DenseParams &p, cudaStream_t st)
 {
-    constexpr size_t smem = 1024 + kStages * kStage + kQBytes + kPBytes + 6 * kRowsCta * 4 + 24 * 8 + sizeof(Found);
+    constexpr size_t smem = 1024 + kStages * kStage + kQBytes + kPBytes + 6 * kRowsCta * 4 + 24 * 8 + sizeof(Found<kChunk>);
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     // the shared-memory attribute is set once per device (a bit each; setting it twice does no harm)
     static std::atomic<uint64_t> done{0};
@@ -1150,11 +1283,11 @@ static cudaError_t launch_dense_as(const DenseParams &p, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if ((done.load(std::memory_order_acquire) & bit) == 0) {
-        e = cudaFuncSetAttribute(dense_attn_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(dense_attn_kernel<kOut, kChunk>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_release);
     }
-    e = launch_k(dense_attn_kernel<kOut>, dim3(2 * p.pairs), dim3(kThreads), smem, st, 2, p);
+    e = launch_k(dense_attn_kernel<kOut, kChunk>, dim3(2 * p.pairs), dim3(kThreads), smem, st, 2, p);
     if (e == cudaSuccess && p.pairs > 1)
         e = launch_k(dense_join_kernel<kOut>, dim3(4 * p.pairs), dim3(kJoinThreads), 0, st, 0, p);
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -1162,9 +1295,16 @@ static cudaError_t launch_dense_as(const DenseParams &p, cudaStream_t st)
 
 cudaError_t launch_dense(const DenseParams &p, int out_type, cudaStream_t st)
 {
-    return out_type == CSA2_F32    ? launch_dense_as<CSA2_F32>(p, st)
-           : out_type == CSA2_BF16 ? launch_dense_as<CSA2_BF16>(p, st)
-                                   : launch_dense_as<CSA2_F16>(p, st);
+    return out_type == CSA2_F32    ? launch_dense_as<CSA2_F32, false>(p, st)
+           : out_type == CSA2_BF16 ? launch_dense_as<CSA2_BF16, false>(p, st)
+                                   : launch_dense_as<CSA2_F16, false>(p, st);
+}
+
+cudaError_t launch_chunk(const DenseParams &p, int out_type, cudaStream_t st)
+{
+    return out_type == CSA2_F32    ? launch_dense_as<CSA2_F32, true>(p, st)
+           : out_type == CSA2_BF16 ? launch_dense_as<CSA2_BF16, true>(p, st)
+                                   : launch_dense_as<CSA2_F16, true>(p, st);
 }
 
 }  // namespace csa2

@@ -120,6 +120,14 @@ cudaError_t launch_cache_read(const csa2_cache &c, const int64_t *rows, int64_t 
                               int x_type, int64_t ld_x, float *key, int64_t ld_key,
                               uint32_t *counters, cudaStream_t st);
 
+// ---- pages (csa2_pages): table null: rows from seq_base on
+struct PageMap {
+    const int32_t *table;
+    int64_t ld;
+    int log;            // entries of a page: 1 << log
+    uint32_t pages;     // of the whole cache
+};
+
 // ---- dense attention of query groups
 constexpr int kDenseRows = 128;         // (query, head) rows of a tile, one pair of CTAs
 constexpr int kDenseEntries = 256;      // entries of a tile
@@ -148,9 +156,76 @@ struct DenseParams {
     float *part_ml;     // [pairs][2][m | l][128]
     DenseBegin *begin;  // [pairs]
     uint32_t *counters;
+    // a chunk's (launch_chunk): token position of each group's first query (null: every
+    // query sees all), tokens per entry, and the pages
+    const int32_t *pos;
+    int m;
+    PageMap pages;
 };
 struct DensePlan { int pairs; size_t off_ml, off_begin, total; };
 DensePlan dense_plan(int ng, int nq, int H, int64_t max_n);
 cudaError_t launch_dense(const DenseParams &p, int out_type, cudaStream_t st);
+cudaError_t launch_chunk(const DenseParams &p, int out_type, cudaStream_t st);
+
+// ---- attention weights by entry
+constexpr int kMassRows = 128;          // (query, head) rows of a block
+constexpr int kMassEntries = 128;       // entries of a tile
+struct MassPlan { int ctas; int64_t blocks, parts; size_t off_groups, off_parts, total; };
+struct MassParams {
+    const uint8_t *codes, *scales;
+    const int64_t *seq_base;
+    const int32_t *seq_len;
+    int64_t cap;
+    int batch;
+    PageMap pages;
+    const int32_t *g_seq, *g_off, *g_len, *pos;
+    int m, ng, nq, H;
+    int64_t max_n;
+    const uint16_t *q;
+    int q_type;
+    float sm_scale;
+    const float *lse, *prev;
+    float decay;
+    float *mass;
+    int64_t ld_mass;
+    MassPlan plan;
+    uint8_t *ws;
+    uint32_t *counters;
+};
+MassPlan mass_plan(int batch, int ng, int nq, int H, int64_t max_n);
+cudaError_t launch_mass(const MassParams &p, cudaStream_t st);
+
+// ---- eviction
+struct EvictPlan { int64_t ld; size_t off_n, off_count, off_topk, total; };
+struct EvictParams {
+    csa2_cache src, dst;
+    PageMap src_pages, dst_pages;
+    const int32_t *seq;
+    int ns;
+    const float *mass;
+    int64_t ld_mass, max_n;
+    int keep, n_first, n_last;
+    int32_t *kept;
+    int64_t ld_kept;
+    float *mass_out;
+    int64_t ld_out;
+    uint32_t *counters;
+};
+EvictPlan evict_plan(int ns, int64_t max_n);
+cudaError_t launch_evict(const EvictParams &p, const EvictPlan &pl, uint8_t *ws, cudaStream_t st);
+
+// ---- norm and rotation
+struct RopeParams {
+    const void *x;
+    void *out;
+    uint32_t ld_x, ld_out, n, H;
+    const float *weight;
+    float eps;
+    const int32_t *pos;
+    const float *inv_freq;
+    int rot;
+    bool halves;
+};
+cudaError_t launch_norm_rope(const RopeParams &p, int type, int out_type, cudaStream_t st);
 
 }  // namespace csa2

@@ -1,0 +1,230 @@
+// csa2_rope.cu -- RMS norm of 512-wide rows and the rotation of their last channels
+// by the position of their token, in one pass.
+//
+//   y = x / sqrt(mean(x^2) + eps) * weight;  pairs (u, v) of the last rot channels:
+//   (u cos a - v sin a, u sin a + v cos a),  a = pos * inv_freq[p].
+//
+// Bound by memory traffic: a row is read and written once, 2 KB in bf16.  A warp
+// takes a whole row, so that the sum of squares is five shuffles and nothing leaves
+// the registers in between; a lane holds channels 8 lane .. and 256 + 8 lane .., 16
+// bytes each in 16-bit types, so that loads and stores are whole lines.
+//
+// The heads of a token turn by the same angles: a warp works on several heads of a
+// token in a row and finds the cosines once, lane by lane, into its own part of shared
+// memory.  The angle is kept in turns: inv_freq / 2 pi as 64-bit fixed point (made
+// once per block in fp64), times pos mod 2^64, is the fraction of a turn exactly,
+// however far the position; the top 32 bits of it are half-turns for sincospif.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "csa2_attn_device.cuh"
+#include "csa2_internal.h"
+
+namespace csa2 {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kResident = 4;                  // blocks to an SM
+
+// eight channels, 16-byte aligned
+template <typename T> struct Eight { uint4 w[sizeof(T) / 2]; };
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *src, Eight<T> &e)
+{
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) e.w[i] = reinterpret_cast<const uint4 *>(src)[i];
+}
+
+template <typename T>
+__device__ __forceinline__ void as_f32(const Eight<T> &e, float *x)
+{
+    if constexpr (__is_same(T, float)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x[4 * i] = __uint_as_float(e.w[i].x); x[4 * i + 1] = __uint_as_float(e.w[i].y);
+            x[4 * i + 2] = __uint_as_float(e.w[i].z); x[4 * i + 3] = __uint_as_float(e.w[i].w);
+        }
+    } else {
+        const uint32_t w[4] = {e.w[0].x, e.w[0].y, e.w[0].z, e.w[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (__is_same(T, __half)) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                x[2 * i] = f.x; x[2 * i + 1] = f.y;
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *dst, const float *x)
+{
+    if constexpr (__is_same(T, float)) {
+        reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (__is_same(T, __half)) w[i] = f32x2_to_f16x2(x[2 * i], x[2 * i + 1]);
+            else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+        }
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// `per` heads of a token to a warp, `parts` warps to a token.
+template <typename T, typename O>
+__global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeParams p, uint32_t per, uint32_t parts)
+{
+    __shared__ uint64_t sTurn[CSA2_D / 2];
+    __shared__ float4 sCs[kWarps][CSA2_D / 4];           // (cos, sin) of two pairs
+    __shared__ float4 sY[kWarps][CSA2_D / 4];            // the rotated part of a row (halves)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int pairs = p.rot / 2;
+    pdl_wait();
+    if ((int)threadIdx.x < pairs) {
+        // f / 2 pi in two parts, of which only the fraction of a turn counts
+        const double f = p.inv_freq[threadIdx.x];
+        const double hi = f * 0.15915494309189535, lo = fma(f, 0.15915494309189535, -hi) + f * -9.839338337591243e-18;
+        const double frac = hi - floor(hi);
+        sTurn[threadIdx.x] = (uint64_t)(frac * 0x1p64) + (uint64_t)(int64_t)(lo * 0x1p64);
+    }
+    float w[16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 v = p.weight ? *reinterpret_cast<const float4 *>(p.weight + 256 * h + 8 * lane + 4 * i)
+                                      : make_float4(1.f, 1.f, 1.f, 1.f);
+            w[8 * h + 4 * i] = v.x; w[8 * h + 4 * i + 1] = v.y; w[8 * h + 4 * i + 2] = v.z; w[8 * h + 4 * i + 3] = v.w;
+        }
+    __syncthreads();
+    // where a lane's two groups of eight channels lie in the rotated part (negative: before it)
+    const int at[2] = {8 * lane - (CSA2_D - p.rot), 256 + 8 * lane - (CSA2_D - p.rot)};
+    const T *const x = static_cast<const T *>(p.x);
+    O *const out = static_cast<O *>(p.out);
+    const uint32_t units = p.n * parts, step = gridDim.x * kWarps;
+    Eight<T> next[2];
+    auto load = [&](uint32_t token, uint32_t head) {
+        const T *src = x + (uint64_t)token * p.ld_x + head * CSA2_D + 8 * lane;
+        load8(src, next[0]);
+        load8(src + 256, next[1]);
+    };
+    uint32_t u = blockIdx.x * kWarps + warp;
+    uint32_t token = u / parts, head = (u - token * parts) * per, left = min(per, p.H - head);
+    if (u < units) load(token, head);
+    bool turn = true;                                    // a new token's angles are due
+    while (u < units) {
+        float v[16];
+        as_f32(next[0], v);
+        as_f32(next[1], v + 8);
+        O *const dst = out + (uint64_t)token * p.ld_out + head * CSA2_D + 8 * lane;
+        const bool due = turn;
+        const uint32_t now = token;
+        turn = --left == 0;
+        if (turn) {
+            u += step;
+            token = u / parts;
+            head = (u - token * parts) * per;
+            left = min(per, p.H - head);
+        } else {
+            ++head;
+        }
+        if (u < units) load(token, head);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float r = rsqrtf(fmaf(sum, 1.0f / CSA2_D, p.eps));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] *= r * w[i];
+        if (pairs > 0) {
+            if (due) {
+                const int64_t pos = p.pos[now];
+                __syncwarp();                            // (the last token's are read)
+                for (int i = lane; i < pairs; i += 32) {
+                    float s, c;
+                    sincospif((float)(int32_t)(((uint64_t)pos * sTurn[i]) >> 32) * 0x1p-31f, &s, &c);
+                    reinterpret_cast<float2 *>(sCs[warp])[i] = make_float2(c, s);
+                }
+                __syncwarp();
+            }
+            if (!p.halves) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (at[h] >= 0) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 cs = sCs[warp][at[h] / 4 + i];
+                            float *const y = v + 8 * h + 4 * i;
+                            const float a = y[0], b = y[1], c = y[2], d = y[3];
+                            y[0] = a * cs.x - b * cs.y; y[1] = a * cs.y + b * cs.x;
+                            y[2] = c * cs.z - d * cs.w; y[3] = c * cs.w + d * cs.z;
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (at[h] >= 0) {
+                        sY[warp][at[h] / 4] = make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
+                        sY[warp][at[h] / 4 + 1] = make_float4(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]);
+                    }
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (at[h] >= 0) {
+                        const bool second = at[h] >= pairs;          // (a group lies in one half: pairs is a multiple of 8)
+                        const int pair = at[h] - (second ? pairs : 0), other = pair + (second ? 0 : pairs);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 o = sY[warp][other / 4 + i];
+                            const float4 c0 = sCs[warp][pair / 2 + 2 * i], c1 = sCs[warp][pair / 2 + 2 * i + 1];
+                            const float oo[4] = {o.x, o.y, o.z, o.w}, c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
+                            float *const y = v + 8 * h + 4 * i;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) y[k] = y[k] * c[k] + (second ? oo[k] : -oo[k]) * s[k];
+                        }
+                    }
+                __syncwarp();                            // (the next row's part goes there)
+            }
+        }
+        store8(dst, v);
+        store8(dst + 256, v + 8);
+    }
+}
+
+}  // namespace
+
+template <typename T, typename O>
+static cudaError_t launch_rope_as(const RopeParams &p, cudaStream_t st)
+{
+    // as many heads to a warp as leave the GPU full
+    const uint64_t rows = (uint64_t)p.n * p.H, warps = (uint64_t)device_sm_count() * kResident * kWarps;
+    const uint32_t per = (uint32_t)std::min<uint64_t>(p.H, std::max<uint64_t>(1, rows / warps));
+    const uint32_t parts = (p.H + per - 1) / per;
+    const uint64_t blocks = ((uint64_t)p.n * parts + kWarps - 1) / kWarps;
+    const cudaError_t e = launch_k(norm_rope_kernel<T, O>, dim3((unsigned)std::min<uint64_t>(blocks, warps / kWarps)),
+                                   dim3(32 * kWarps), 0, st, 0, p, per, parts);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_norm_rope(const RopeParams &p, int type, int out_type, cudaStream_t st)
+{
+    auto to = [&](auto tag) {
+        using T = decltype(tag);
+        return out_type == CSA2_F32    ? launch_rope_as<T, float>(p, st)
+               : out_type == CSA2_BF16 ? launch_rope_as<T, __nv_bfloat16>(p, st)
+                                       : launch_rope_as<T, __half>(p, st);
+    };
+    return type == CSA2_F32 ? to(float{}) : type == CSA2_BF16 ? to(__nv_bfloat16{}) : to(__half{});
+}
+
+}  // namespace csa2
