@@ -47,16 +47,17 @@ static EncodeTiledFn encode_tiled()
 }
 
 cudaError_t make_tmap_rows_u8(CUtensorMap *map, const void *base, int64_t rows, int row_bytes,
-                              int box_rows, int swizzle_bytes)
+                              int box_rows, int swizzle_bytes, int box_bytes)
 {
     EncodeTiledFn fn = encode_tiled();
     if (fn == nullptr) return cudaErrorNotSupported;
     cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    cuuint32_t box[2] = {(cuuint32_t)row_bytes, (cuuint32_t)box_rows};
+    cuuint32_t box[2] = {(cuuint32_t)(box_bytes > 0 ? box_bytes : row_bytes), (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
-    CUtensorMapSwizzle sw = swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                                 : CU_TENSOR_MAP_SWIZZLE_64B;
+    CUtensorMapSwizzle sw = swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                            : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                  : CU_TENSOR_MAP_SWIZZLE_NONE;
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides,
                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

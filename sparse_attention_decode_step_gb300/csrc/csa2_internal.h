@@ -48,9 +48,9 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
 int device_sm_count();
 
 // 2-D tensor map over a row-major uint8 array [rows][row_bytes] with a box of
-// [box_rows][row_bytes] and the given swizzle width (64 or 128 bytes).
+// [box_rows][box_bytes] (0: whole rows) and the given swizzle width (64 or 128 bytes, 0: none).
 cudaError_t make_tmap_rows_u8(CUtensorMap *map, const void *base, int64_t rows, int row_bytes,
-                              int box_rows, int swizzle_bytes);
+                              int box_rows, int swizzle_bytes, int box_bytes = 0);
 
 // ---- append
 cudaError_t launch_append(const csa2_cache &c, const float *C, const float *Z, const float *key,

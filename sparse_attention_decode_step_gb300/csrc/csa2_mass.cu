@@ -5,28 +5,33 @@
 //               2^(l2s q_r . v_j - lse2_r),   l2s = sm_scale log2 e, lse2 = lse log2 e.
 //
 // The sum is over rows, so entries lie along the tensor core's M: one CTA takes 128
-// entries at a time against a block of up to 128 rows,
-//     S [128 entries x N rows] = K [128 x 512] . Q^T          (M 128, N 16 .. 128)
+// entries at a time against a block of up to 128 rows, 64 of them in one pass,
+//     S [128 entries x 64 rows] = K [128 x 512] . Q^T          (M 128, N 16 .. 64)
 // and a thread of the epilogue, which holds one entry's row of S in TMEM, sums over
 // its columns alone: no value crosses threads.  The block's queries stay in shared
-// memory (128 KB) while the entries go by, dequantised (E2M1 x E4M3 is exact in f16)
-// into a ring of 32 KB stages of 128 entries x 128 channels, four to a tile.  Which
-// channels a stage holds is free as long as queries and entries agree: those that a
-// lane of a producer has at once, so that every load is of whole 128-byte lines
-// and still every lane works on every stage (see slot()).
+// memory (128 KB) while the entries go by.  Their codes and scales come by TMA, as they
+// are stored (36 KB a tile); dequantised (E2M1 x E4M3 is exact in f16), they go straight
+// to TMEM, from where the MMAs read them: through shared memory, writing and reading
+// them would take 256 KB a tile and with the queries' reads more of its 128 bytes a
+// cycle than there are (32 x 64 heads over 65,536 entries: 245 us so).
+//
+// S is summed in two parts of 256 channels, which the epilogue adds: the tensor core's
+// additions to an fp32 sum are cut off, not rounded, each by up to 2^-23 of the sum so
+// far, and with two sums half as large the loss is half.
 //
 // A weight is computed as r 2^(l2s x - m), with m = lse2 rounded to a whole number and
 // r = 2^(m - lse2): the exponents that matter lie near zero then, and lse2's own
 // rounding (2^-20 at 20) does not come in.  Sums are fp32.
 //
-// Groups of one block write mass themselves.  The blocks of larger ones leave their
-// sums side by side in the workspace, which a second kernel adds in order: no atomics,
+// Groups of up to 64 rows write mass themselves.  The blocks of larger ones leave the
+// sums of each 64 rows side by side in the workspace, which a second kernel adds in order: no atomics,
 // results do not depend on the run.  A first kernel lays out the blocks; the work,
 // counted in tiles of entries over all blocks, is divided into equal runs.
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "csa2_attn_device.cuh"
 #include "csa2_internal.h"
@@ -35,14 +40,16 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kWarpsEpi = 4, kWarpsProd = 8;
-constexpr int kThreads = 32 * (kWarpsEpi + kWarpsProd + 1);
+constexpr int kWarpsEpi = 8, kWarpsProd = 8;          // and one issues the MMAs, one the loads
+constexpr int kThreads = 32 * (kWarpsEpi + kWarpsProd + 2);
+constexpr int kWarpMma = kWarpsEpi + kWarpsProd, kWarpLoad = kWarpMma + 1;
 constexpr int kRows = kMassRows, kEnt = kMassEntries;
-constexpr int kStages = 3;
-constexpr uint32_t kStage = 32768;                    // [2 atoms of 64 channels][128 entries][128 B]
-constexpr uint32_t kAtom = 128 * 128;
-constexpr uint32_t kQBytes = kRows * CSA2_D * 2;      // [4 stages][2 atoms][N rows][128 B]
-constexpr int kBufs = 4;                              // S buffers of 128 TMEM columns
+constexpr uint32_t kPass = 64;                             // rows of a pass
+constexpr int kUnits = 4, kScaleUnits = 3;            // codes: half tiles (256 channels), scales: tiles
+constexpr uint32_t kUnit = kEnt * 128, kScaleUnit = kEnt * CSA2_SCALE_BYTES;
+constexpr uint32_t kQBytes = kRows * CSA2_D * 2;      // [8 atoms of 64 channels][128 rows][128 B]
+constexpr uint32_t kQAtom = kRows * 128;
+constexpr uint32_t kColS = 256;                       // TMEM: K in columns 0 .. 255 (four stages of 128 channels), S from here
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPlanThreads = 1024;
 constexpr int kFinishThreads = 256;
@@ -57,7 +64,7 @@ struct Block {
     int pos;             // token position of the group's first query
     int n_group;
     int base;            // cache row of entry 0 (without pages)
-    int alone;           // the group's only block
+    int alone;           // the group's only block, of one pass: it writes mass itself
     int causal;
 };
 
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(MassParams p)
         r.seq = a.seq;
         r.n_group = a.n;
         r.base = a.base;
-        r.alone = nb == 1;
+        r.alone = nb == 1 && (a.e - a.a) * p.H <= (int)kPass;
         r.causal = p.pos != nullptr;
         r.pos = r.causal ? p.pos[g] : 0;
         for (int i = lane; i < nb; i += 32) {
@@ -208,26 +215,17 @@ __global__ void __launch_bounds__(kPlanThreads) mass_plan_kernel(MassParams p)
 }
 
 // ------------------------------------------------------------------ weights
-// The 16 bytes (8 channels) c of a row of 64 lie in stage slot_stage(c), there in the
-// 64-channel atom slot_atom(c), 16-byte piece slot_piece(c): lane l = 0 .. 7 of an
-// entry's 128 bytes of codes (256 channels, half h) holds the pieces 4 l .. 4 l + 3 of that
-// half; its first two go to stage 2 h, the others to 2 h + 1, as channels 16 l ..
-__device__ __forceinline__ int slot_stage(int c) { return 2 * (c >> 5) + ((c >> 1) & 1); }
-__device__ __forceinline__ int slot_atom(int c) { return (c >> 4) & 1; }
-__device__ __forceinline__ int slot_piece(int c) { return 2 * ((c >> 2) & 3) + (c & 1); }
-
-// A CTA's pieces of work in order: tiles k0 .. k1 of a block.
+// A CTA's pieces of work in order: tiles k0 .. k1 of a block.  (A role takes what it
+// needs of the block into registers itself.)
 struct Work {
-    Block blk;
     int b;
     int k0, k1;
     int64_t left;        // tiles after this piece
 
     __device__ __forceinline__ void take(const Space &ws, int at, int64_t tiles)
     {
-        blk = ws.blocks[b];
         k0 = at;
-        k1 = (int)min((int64_t)tiles_of(blk.n), at + tiles);
+        k1 = (int)min((int64_t)tiles_of(ws.blocks[b].n), at + tiles);
         left = tiles - (k1 - k0);
     }
     __device__ __forceinline__ bool next(const Space &ws)
@@ -238,6 +236,9 @@ struct Work {
         return true;
     }
 };
+
+// Columns of S that a block of rows takes.
+__device__ __forceinline__ int columns(int rows) { return max(16, (rows + 15) & ~15); }
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarpsEpi) : "memory"); }
 
@@ -258,44 +259,145 @@ __device__ __forceinline__ bool epi_any(bool v)
     return r != 0;
 }
 
+// An arrival that hands nothing over in memory.  (With release it waits for the warp's
+// global loads and stores on their way: 2,500 cycles a tile in the epilogue.)
+__device__ __forceinline__ void arrive_relaxed(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // A row without weight: its log sum is infinite.
 __device__ __forceinline__ bool no_weight(float lse) { return fabsf(lse) > 0x1p29f; }
 
-__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v)
+// D (TMEM) += A (TMEM, K-major) . B (shared memory)
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 lanes x 32 columns
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// 16 columns of both parts of S; wait_s: they are there.
+__device__ __forceinline__ void load_s(uint32_t tS, float (&x)[2][16])
+{
+    tmem_ld16(tS, x[0]);
+    tmem_ld16(tS + 64, x[1]);
+}
+
+__device__ __forceinline__ void wait_s(float (&x)[2][16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(x[0][i]), "+f"(x[1][i]));      // (what is done with them stays behind the wait)
+}
+
+// Adds an entry's weights of `cols` rows (a multiple of 16).  kPlain: all of them see the
+// entry and one m serves them all; else a NaN of a row that does not see it stays out.
+template <bool kPlain>
+__device__ __forceinline__ void weigh(uint32_t tS, int cols, const float *r, const float *m, const int *see, int e, float l2s, float m_all,
+                                      float (&sum)[4])
+{
+    auto add = [&](int c0, const float (&x)[2][16]) {
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+            const float4 row = *reinterpret_cast<const float4 *>(r + c0 + c);
+            float4 mm = make_float4(m_all, m_all, m_all, m_all);
+            if (!kPlain) mm = *reinterpret_cast<const float4 *>(m + c0 + c);
+            const float2 y = fma_f32x2(make_float2(x[0][c] + x[1][c], x[0][c + 1] + x[1][c + 1]), make_float2(l2s, l2s), make_float2(-mm.x, -mm.y));
+            const float2 z = fma_f32x2(make_float2(x[0][c + 2] + x[1][c + 2], x[0][c + 3] + x[1][c + 3]), make_float2(l2s, l2s),
+                                       make_float2(-mm.z, -mm.w));
+            const float s0 = fmaf(fast_exp2(y.x), row.x, sum[0]), s1 = fmaf(fast_exp2(y.y), row.y, sum[1]);
+            const float s2 = fmaf(fast_exp2(z.x), row.z, sum[2]), s3 = fmaf(fast_exp2(z.y), row.w, sum[3]);
+            if (kPlain) {
+                sum[0] = s0; sum[1] = s1; sum[2] = s2; sum[3] = s3;
+            } else {
+                const int4 v = *reinterpret_cast<const int4 *>(see + c0 + c);
+                if (e < v.x) sum[0] = s0;
+                if (e < v.y) sum[1] = s1;
+                if (e < v.z) sum[2] = s2;
+                if (e < v.w) sum[3] = s3;
+            }
+        }
+    };
+    if (kPlain && cols == (int)kPass) {                     // the next columns on their way
+        float x[2][2][16];
+        load_s(tS, x[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wait_s(x[i & 1]);
+            if (i < 3) load_s(tS + 16 * (i + 1), x[(i + 1) & 1]);
+            add(16 * i, x[i & 1]);
+        }
+    } else {
+        for (int c0 = 0; c0 < cols; c0 += 16) {
+            float x[2][16];
+            load_s(tS + c0, x);
+            wait_s(x);
+            add(c0, x);
+        }
+    }
 }
 
 // Blocks b0 .. b1 - 1 of the plan (b1 may lie behind the last).
-__global__ void __launch_bounds__(kThreads, 1) mass_kernel(MassParams p, int b0, int b1)
+__global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap scales,
+                                                           MassParams p, int b0, int b1, int run_log)
 {
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *sRing = smem;
-    uint8_t *sQ = sRing + kStages * kStage;
-    float2 *sRow = reinterpret_cast<float2 *>(sQ + kQBytes);         // [128] (m, r) of a row
-    int *sSees = reinterpret_cast<int *>(sRow + kRows);              // [128]
-    uint64_t *bar_full = reinterpret_cast<uint64_t *>(sSees + kRows);   // [3] stage filled
-    uint64_t *bar_empty = bar_full + kStages;                        // [3] stage's MMAs done
-    uint64_t *bar_s = bar_empty + kStages;                           // [4] S buffer complete
-    uint64_t *bar_free = bar_s + kBufs;                              // [4] S buffer read
-    uint64_t *bar_q = bar_free + kBufs;                              // queries stored
-    uint64_t *bar_done = bar_q + 1;                                  // every MMA done
-    int *sFlag = reinterpret_cast<int *>(bar_done + 1);              // [0] abort, [1] first block
+    uint8_t *sQ = smem;
+    uint8_t *sCodes = sQ + kQBytes;                                  // [4][128 entries][128 B], swizzled
+    uint8_t *sScales = sCodes + kUnits * kUnit;                      // [3][128 entries][32 B]
+    float *sM = reinterpret_cast<float *>(sScales + kScaleUnits * kScaleUnit);       // [128] m and r of a row
+    float *sR = sM + kRows;
+    int *sSees = reinterpret_cast<int *>(sR + kRows);                // [128]
+    float *sTop = reinterpret_cast<float *>(sSees + kRows);          // [8] largest and smallest lse2 of four warps
+    uint64_t *bar_raw = reinterpret_cast<uint64_t *>(sTop + 8);      // [4] half tile loaded
+    uint64_t *bar_read = bar_raw + kUnits;                           // [4] half tile dequantised
+    uint64_t *bar_sc = bar_read + kUnits;                            // [3] scales loaded
+    uint64_t *bar_scread = bar_sc + kScaleUnits;                     // [3] scales read
+    uint64_t *bar_k = bar_scread + kScaleUnits;                      // [4] stage of K stored
+    uint64_t *bar_kfree = bar_k + 4;                                 // [4] its MMAs done
+    uint64_t *bar_s = bar_kfree + 4;                                 // [2] S complete
+    uint64_t *bar_sfree = bar_s + 2;                                 // [2] S read
+    uint64_t *bar_q = bar_sfree + 2;                                 // queries stored
+    uint64_t *bar_piece = bar_q + 1;                                 // a piece's MMAs done
+    int *sFlag = reinterpret_cast<int *>(bar_piece + 1);             // [0] abort, [1] first block
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(sFlag + 2);
     volatile int *abort_flag = sFlag;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) { mbar_init(&bar_full[i], kWarpsProd); mbar_init(&bar_empty[i], 1); }
-        for (int i = 0; i < kBufs; ++i) { mbar_init(&bar_s[i], 1); mbar_init(&bar_free[i], kWarpsEpi); }
+        for (int i = 0; i < kUnits; ++i) { mbar_init(&bar_raw[i], 1); mbar_init(&bar_read[i], kWarpsProd / 2); }   // (a half tile, a stage: four warps)
+        for (int i = 0; i < kScaleUnits; ++i) { mbar_init(&bar_sc[i], 1); mbar_init(&bar_scread[i], kWarpsProd); }
+        for (int i = 0; i < 4; ++i) { mbar_init(&bar_k[i], kWarpsProd / 2); mbar_init(&bar_kfree[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&bar_s[i], 1); mbar_init(&bar_sfree[i], kWarpsEpi / 2); }
         mbar_init(bar_q, kWarpsProd);
-        mbar_init(bar_done, 1);
+        mbar_init(bar_piece, 1);
         sFlag[0] = 0;
         fence_barrier_init();
+        prefetch_tmap(&codes);
+        prefetch_tmap(&scales);
     }
-    if (warp == kWarpsEpi + kWarpsProd) {
+    if (warp == kWarpMma) {
         tmem_alloc(sTmem, 512);
         tmem_relinquish();
     }
@@ -322,210 +424,278 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(MassParams p, int b0,
         w.b = sFlag[1];
         w.take(ws, (int)(u0 - ws.blocks[w.b].first), run);
     }
-    auto columns = [](const Block &b) { return max(16, (b.rows + 15) & ~15); };
     bool ok = true;
 
-    if (warp == kWarpsEpi + kWarpsProd) {
+    if (warp == kWarpMma) {
         // ============================================== MMA issuer (the whole warp runs the loop, one lane issues)
+        // Buffers, stages and passes are unrolled, so that every address and descriptor is
+        // an immediate away from two registers: the MMAs take theirs from uniform
+        // registers, and moving five of them there for each costs 55 cycles, 33 being its own.
         uint32_t elected;
         asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(elected));
-        const uint32_t ring = __shfl_sync(0xffffffffu, smem_u32(sRing), 0), t0 = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t dk = smem_desc(ring, 16, 1024, kLayoutSW128), dq = smem_desc(ring + kStages * kStage, 16, 1024, kLayoutSW128);
-        uint32_t stage = 0, phase = 0, tile = 0, pieces = 0;
+        const uint32_t q0 = __shfl_sync(0xffffffffu, smem_u32(sQ), 0), t0 = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dq = smem_desc(q0, 16, 1024, kLayoutSW128);
+        uint32_t tile = 0, pieces = 0, used[2] = {1, 1};       // parities of the waits
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
             tc_fence_after();
         };
+        // a pass over the rows kR .. into buffer kBuf; fill: K is made for it, last: and not used again
+        auto pass_as = [&](auto buf, auto r, uint32_t id, bool last) {
+            constexpr uint32_t kBuf = decltype(buf)::value, kR = decltype(r)::value;
+            wait(&bar_sfree[kBuf], used[kBuf]);
+            used[kBuf] ^= 1;
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                if (kR == 0) wait(&bar_k[j], tile & 1);
+                if (!ok) break;
+                if (elected) {
+#pragma unroll
+                    for (uint32_t ks = 0; ks < 8; ++ks)
+                        mma_f16_ts(t0 + (kColS + 128 * kBuf + 64 * (j >> 1)), t0 + (64 * j + 8 * ks),
+                                   dq + (kR * 128 / 16 + (2 * j + (ks >> 2)) * (kQAtom >> 4) + 2 * (ks & 3)), id, ks > 0 ? 1u : j & 1);
+                    if (last) mma_commit(&bar_kfree[j]);
+                    if (j == 3) mma_commit(&bar_s[kBuf]);
+                }
+                __syncwarp();
+            }
+        };
+        constexpr uint32_t id64 = instr_desc(128, kPass, 0, 0, 0, 0);
+        using B0 = std::integral_constant<uint32_t, 0>;
+        using B1 = std::integral_constant<uint32_t, 1>;
+        using R1 = std::integral_constant<uint32_t, kPass>;
         for (; more && ok; more = w.next(ws), ++pieces) {
-            const uint32_t n = (uint32_t)columns(w.blk), id = instr_desc(128, 0, 0, 0, 0, 0) | ((n >> 3) << 17);
+            const uint32_t n = (uint32_t)columns(ws.blocks[w.b].rows), rest = n > kPass ? n - kPass : n;
+            const uint32_t id = instr_desc(128, 0, 0, 0, 0, 0) | ((rest >> 3) << 17);
             wait(bar_q, pieces & 1);
             for (int t = w.k0; t < w.k1 && ok; ++t, ++tile) {
-                const uint32_t buf = tile % kBufs;
-                if (tile >= kBufs) wait(&bar_free[buf], (tile / kBufs - 1) & 1);
-#pragma unroll 1
-                for (uint32_t j = 0; j < 4; ++j) {
-                    wait(&bar_full[stage], phase);
-                    if (!ok) break;
-                    if (elected) {
-#pragma unroll
-                        for (uint32_t ks = 0; ks < 8; ++ks)
-                            mma_f16(t0 + 128 * buf, dk + (stage * (kStage >> 4) + (ks >> 2) * (kAtom >> 4) + 2 * (ks & 3)),
-                                    dq + ((2 * j + (ks >> 2)) * (n * 128 >> 4) + 2 * (ks & 3)), id, ks > 0 ? 1u : j);
-                        mma_commit(&bar_empty[stage]);
-                        if (j == 3) mma_commit(&bar_s[buf]);
+                if (n > kPass) {
+                    pass_as(B0{}, B0{}, id64, false);
+                    if (rest == kPass) pass_as(B1{}, R1{}, id64, true);
+                    else pass_as(B1{}, R1{}, id, true);
+                } else if (tile & 1) {
+                    if (rest == kPass) pass_as(B1{}, B0{}, id64, true);
+                    else pass_as(B1{}, B0{}, id, true);
+                } else {
+                    if (rest == kPass) pass_as(B0{}, B0{}, id64, true);
+                    else pass_as(B0{}, B0{}, id, true);
+                }
+            }
+            if (ok && elected) mma_commit(bar_piece);
+            __syncwarp();
+        }
+        // every MMA has completed before TMEM and shared memory go back
+        if (!ok) {
+            volatile int no_abort = 0;
+            if (elected) mma_commit(bar_piece);
+            __syncwarp();
+            mbar_wait<true>(bar_piece, (pieces - 1) & 1, &no_abort);       // (the piece that gave up is counted)
+        } else if (pieces > 0) {
+            wait(bar_piece, (pieces - 1) & 1);
+        }
+    } else if (warp == kWarpLoad) {
+        // ============================================== loads: lane i has the entries run i .. of a tile
+        // (One copy for as many entries as lie in one page, 128 at most; the warp goes through
+        // them together, since a copy that lanes issue apart takes the place of several.)
+        uint32_t unit = 0, sc_loads = 0;
+        uint32_t elected;
+        asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(elected));
+        for (; more && ok; more = w.next(ws)) {
+            const bool paged = p.pages.table != nullptr;
+            const int n = ws.blocks[w.b].n, base = ws.blocks[w.b].base;
+            const int32_t *const table = p.pages.table + (int64_t)ws.blocks[w.b].seq * p.pages.ld;      // (if paged)
+            auto entry = [&](int t) { return t * kEnt + (lane << run_log); };
+            auto there = [&](int t) { return lane < kEnt >> run_log && t < w.k1 && entry(t) < n; };
+            auto page_of = [&](int t) { return paged && there(t) ? __ldg(table + (entry(t) >> p.pages.log)) : 0; };
+            int page = page_of(w.k0);
+            for (int t = w.k0; t < w.k1 && ok; ++t) {
+                bool in = there(t);
+                const int e = entry(t);
+                int row = base + e;
+                if (paged) {
+                    if (in && (uint32_t)page >= p.pages.pages) {           // no page of the cache: nothing is read
+                        count_event(p.counters, CSA2_CNT_BAD_INPUT);
+                        in = false;
                     }
+                    row = (int)((uint32_t)page << p.pages.log) + (e & ((1 << p.pages.log) - 1));
+                    page = page_of(t + 1);
+                }
+                const uint32_t loads = __ballot_sync(0xffffffffu, in), tile = unit / 2, s = tile % kScaleUnits;
+                // the tile's copies of `bytes` a row to `to`, once what was there is read
+                auto load = [&](uint64_t *read, uint32_t parity, uint64_t *full, const CUtensorMap *map, uint8_t *to, int x, uint32_t bytes) {
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(read, parity, abort_flag));
+                    if (!ok) return;
+                    if (elected) mbar_arrive_expect_tx(full, __popc(loads) * (bytes << run_log));
                     __syncwarp();
-                    if (++stage == kStages) { stage = 0; phase ^= 1; }
+                    for (uint32_t left = loads; left; left &= left - 1) {
+                        const int i = __ffs(left) - 1, r = __shfl_sync(0xffffffffu, row, i);
+                        if (elected) tma_load_2d(to + i * (bytes << run_log), map, x, r, full);
+                        __syncwarp();
+                    }
+                };
+                load(&bar_scread[s], ((tile / kScaleUnits) & 1) ^ 1, &bar_sc[s], &scales, sScales + s * kScaleUnit, 0, CSA2_SCALE_BYTES);
+                if (ok) sc_loads = tile + 1;
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t u = unit % kUnits;
+                    load(&bar_read[u], ((unit / kUnits) & 1) ^ 1, &bar_raw[u], &codes, sCodes + u * kUnit, 128 * h, 128);
+                    if (ok) ++unit;
                 }
             }
         }
-        // every MMA has completed before TMEM and shared memory go back
-        volatile int no_abort = 0;
-        if (elected) mma_commit(bar_done);
-        __syncwarp();
-        if (!mbar_wait<true>(bar_done, 0, &no_abort)) ok = false;
+        // (copies on their way end before the CTA does)
+        if (!ok) {
+            volatile int no_abort = 0;
+            for (uint32_t i = unit > kUnits ? unit - kUnits : 0; i < unit; ++i) mbar_wait<true>(&bar_raw[i % kUnits], (i / kUnits) & 1, &no_abort);
+            for (uint32_t i = sc_loads > kScaleUnits ? sc_loads - kScaleUnits : 0; i < sc_loads; ++i)
+                mbar_wait<true>(&bar_sc[i % kScaleUnits], (i / kScaleUnits) & 1, &no_abort);
+        }
     } else if (warp >= kWarpsEpi) {
         // ============================================== producers
-        // Warp pw dequantises the entries 16 pw .. 16 pw + 15 of a tile, four at a time
-        // (e4), eight lanes to an entry.  A lane's 16 code bytes feed two stages; the next
-        // tile's are loaded as soon as their registers are free.
-        const int pw = warp - kWarpsEpi, l = lane & 7, e4 = lane >> 3;
-        const bool turn = l >= 4;              // (its atom's stores go in the other order: eight bank groups at every store)
-        const int row = 16 * pw + e4;          // of entry u: row + 4 u
-        uint32_t piece[2];                     // of entry u: ^ 64 where u is odd, + 512 u
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            piece[j] = smem_u32(sRing) + (l >> 2) * kAtom + row * 128u + (uint32_t)(((2 * (l & 3) + (j ^ (int)turn)) ^ (row & 7)) << 4);
-        uint32_t stage = 0, phase = 1, tile = 0;
-        uint4 gc[2][4];
-        uint32_t gs[2][4];
-        const bool paged = p.pages.table != nullptr;
-        for (; more && ok; more = w.next(ws)) {
-            const int32_t *const table = p.pages.table + (int64_t)w.blk.seq * p.pages.ld;      // (if paged)
-            // a warp's 16 entries lie in one page
-            auto page_of = [&](int t) {
-                const int e = t * kEnt + 16 * pw;
-                return paged && t < w.k1 && e < w.blk.n ? __ldg(table + (e >> p.pages.log)) : 0;
-            };
-            int page = page_of(w.k0);
-            int left = 0;                      // entries from the lane's first on
-            const uint8_t *c0 = nullptr, *s0 = nullptr;
-            auto begin = [&](int t) {
-                const int e = t * kEnt + 16 * pw;
-                left = t < w.k1 ? w.blk.n - e - e4 : 0;
-                int64_t r = (int64_t)w.blk.base + e;
-                if (paged) {
-                    if ((uint32_t)page >= p.pages.pages) {     // no page of the cache: nothing is read
-                        if (lane == 0 && left > 0) count_event(p.counters, CSA2_CNT_BAD_INPUT);
-                        left = 0;
-                    }
-                    r = ((int64_t)page << p.pages.log) + (e & ((1 << p.pages.log) - 1));
-                    page = page_of(t + 1);
-                }
-                c0 = p.codes + (r + e4) * CSA2_CODE_BYTES + 16 * l;
-                s0 = p.scales + (r + e4) * CSA2_SCALE_BYTES + 2 * l;
-            };
-            auto load = [&](int h) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    gc[h][u] = make_uint4(0, 0, 0, 0);
-                    gs[h][u] = 0;
-                    if (4 * u < left) {
-                        gc[h][u] = __ldg(reinterpret_cast<const uint4 *>(c0 + 4 * u * CSA2_CODE_BYTES + 128 * h));
-                        gs[h][u] = __ldg(reinterpret_cast<const uint16_t *>(s0 + 4 * u * CSA2_SCALE_BYTES + 16 * h));
-                    }
-                }
-            };
-            begin(w.k0);
-            load(0);
-            load(1);
+        // A warp dequantises the 32 entries of its TMEM lanes, an entry a lane, in one
+        // half of the channels: two of the four stages, 64 bytes of codes each.
+        const int pw = warp - kWarpsEpi, quarter = warp & 3, half = pw >> 2;
+        const int row = 32 * quarter + lane;
+        const uint32_t to = tmem + 128 * half + ((uint32_t)(32 * quarter) << 16);
+        uint32_t tile = 0, pieces = 0;
+        for (; more && ok; more = w.next(ws), ++pieces) {
             // ---- the block's queries, once the last block's products are done
-            if (tile > 0) ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[(tile - 1) % kBufs], ((tile - 1) / kBufs) & 1, abort_flag));
+            if (pieces > 0) ok = __all_sync(0xffffffffu, mbar_wait<true>(bar_piece, (pieces - 1) & 1, abort_flag));
             if (!ok) break;
-            const int n = columns(w.blk);
-            const uint4 *const q = reinterpret_cast<const uint4 *>(p.q) + (int64_t)w.blk.row0 * (CSA2_D / 8);
-            for (int i0 = 32 * pw + lane; i0 < n * 64; i0 += 8 * 32 * kWarpsProd) {
-                uint4 v[8];
+            const int rows = ws.blocks[w.b].rows, row0 = ws.blocks[w.b].row0, n = columns(rows);
+            const uint4 *const q = reinterpret_cast<const uint4 *>(p.q) + (int64_t)row0 * (CSA2_D / 8);
+            for (int i0 = 32 * pw + lane; i0 < n * 64; i0 += 4 * 32 * kWarpsProd) {
+                uint4 v[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const int i = i0 + k * 32 * kWarpsProd;
                     // (zeros for a row without weight: whatever its query holds stays out)
-                    const bool in = i < w.blk.rows * 64 && !no_weight(__ldg(p.lse + w.blk.row0 + (i >> 6)));
+                    const bool in = i < rows * 64 && !no_weight(__ldg(p.lse + row0 + (i >> 6)));
                     v[k] = in ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const int i = i0 + k * 32 * kWarpsProd, r = i >> 6, c = i & 63;
                     if (i >= n * 64) break;
                     if (p.q_type == CSA2_BF16)
                         v[k] = make_uint4(bf16x2_to_f16x2(v[k].x), bf16x2_to_f16x2(v[k].y), bf16x2_to_f16x2(v[k].z), bf16x2_to_f16x2(v[k].w));
-                    *reinterpret_cast<uint4 *>(sQ + (2 * slot_stage(c) + slot_atom(c)) * n * 128 + sw128(r, slot_piece(c))) = v[k];
+                    *reinterpret_cast<uint4 *>(sQ + (c >> 3) * kQAtom + sw128(r, c & 7)) = v[k];
                 }
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_q);
-            tile += w.k1 - w.k0;
-            for (int t = w.k0; t < w.k1 && ok; ++t) {
+            for (int t = w.k0; t < w.k1 && ok; ++t, ++tile) {
+                const uint32_t unit = 2 * tile + half, u = unit % kUnits, s = tile % kScaleUnits;
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_sc[s], (tile / kScaleUnits) & 1, abort_flag) &&
+                                                 mbar_wait<true>(&bar_raw[u], (unit / kUnits) & 1, abort_flag));
+                if (!ok) break;
+                const uint8_t *const src = sCodes + u * kUnit;
+                const uint4 sc = *reinterpret_cast<const uint4 *>(sScales + s * kScaleUnit + row * CSA2_SCALE_BYTES + 16 * half);
+                const uint32_t scale[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int h = j >> 1, x = j & 1;
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(&bar_empty[stage], phase, abort_flag));
+                for (int j = 0; j < 2; ++j) {
+                    uint4 c[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4 *>(src + sw128(row, 4 * j + i));
+                    // (dequantised before the stage is free: what lies between its MMAs and the next
+                    // ones' is then no more than the stores)
+                    uint32_t r[2][32];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint4 v = c[2 * i + k];
+                            const uint32_t s2 = e4m3x2_to_f16x2(scale[2 * j + i] >> (16 * k));
+                            const uint32_t lo = __byte_perm(s2, 0, 0x1010), hi = __byte_perm(s2, 0, 0x3232);
+                            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint4 o = fp4x8_to_f16(in[x], x < 2 ? lo : hi);
+                                uint32_t *const to = r[i] + 16 * k + 4 * x;
+                                to[0] = o.x; to[1] = o.y; to[2] = o.z; to[3] = o.w;
+                            }
+                        }
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(&bar_kfree[2 * half + j], (tile & 1) ^ 1, abort_flag));
                     if (!ok) break;
-                    const uint32_t to = stage * kStage;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t sc = scale_pair((gs[h][u] >> (8 * x)) & 0xFFu);
-                        uint32_t a = x ? gc[h][u].z : gc[h][u].x, b = x ? gc[h][u].w : gc[h][u].y;
-                        if (turn) { const uint32_t z = a; a = b; b = z; }
-                        const uint32_t at = to + 512 * u, odd = (u & 1) * 64;
-                        st_shared16((piece[0] ^ odd) + at, fp4x8_to_f16(a, sc));
-                        st_shared16((piece[1] ^ odd) + at, fp4x8_to_f16(b, sc));
-                    }
-                    fence_async_smem();
+                    tc_fence_after();
+                    tmem_st32u(to + 64 * j, r[0]);
+                    tmem_st32u(to + 64 * j + 32, r[1]);
+                    tmem_wait_st();
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_full[stage]);
-                    if (++stage == kStages) { stage = 0; phase ^= 1; }
-                    if (j == 1) { begin(t + 1); load(0); }
-                    if (j == 3) load(1);
+                    if (lane == 0) mbar_arrive(&bar_k[2 * half + j]);
+                }
+                if (lane == 0) {
+                    mbar_arrive(&bar_read[u]);
+                    mbar_arrive(&bar_scread[s]);
                 }
             }
         }
     } else {
         // ============================================== epilogue: a thread has an entry
+        // Two sets of four warps, each with an S buffer of its own: of up to 64 rows they take
+        // tiles in turn, of more each takes its half of the rows.  What a tile costs in
+        // latency (S read, exponentials, prev) then has two passes' time.
         const float l2s = p.sm_scale * kLog2e;
-        const uint32_t lane_q = (uint32_t)(32 * warp) << 16;
-        uint32_t tile = 0;
+        const int ent = tid & (kEnt - 1), set = tid / kEnt;
+        const uint32_t tS = tmem + kColS + 128 * set + ((uint32_t)(32 * (warp & 3)) << 16);
+        uint32_t tile = 0, used = 0;           // parity of the next wait
         for (; more && ok; more = w.next(ws)) {
+            const Block &blk = ws.blocks[w.b];
+            const int rows = blk.rows, n = columns(rows), n_ent = blk.n;
+            const bool alone = blk.alone;
+            // Where the rows' lse2 lie within 2^64 of each other, one m (the largest) serves them all.
+            float lse2 = NAN;                  // (a row without weight, or past the block's)
+            int s = 0;
+            if (tid < rows) {
+                const float lse = p.lse[blk.row0 + tid];
+                if (!no_weight(lse)) lse2 = lse * kLog2e;
+                s = sees(p, blk.causal, blk.pos, blk.n_group, (blk.k0 + tid) / p.H);
+            }
+            float top = lse2, low = lse2;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+            }
+            if (warp < kRows / 32 && lane == 0) { sTop[warp] = top; sTop[4 + warp] = low; }
+            epi_sync();
+            top = fmaxf(fmaxf(sTop[0], sTop[1]), fmaxf(sTop[2], sTop[3]));
+            low = fminf(fminf(sTop[4], sTop[5]), fminf(sTop[6], sTop[7]));
+            const float m_all = rintf(top);
+            const bool near = top - low < 64.f;            // (false without any weight)
             if (tid < kRows) {
-                float m = 0.f, r = 0.f;        // (rows past the block's, or without a sum: no weight)
-                int s = 0;
-                if (tid < w.blk.rows) {
-                    const float lse = p.lse[w.blk.row0 + tid];
-                    if (!no_weight(lse)) {
-                        m = rintf(lse * kLog2e);
-                        r = exp2f(-fmaf(lse, kLog2e, -m));
-                    }
-                    s = sees(p, w.blk.causal, w.blk.pos, w.blk.n_group, (w.blk.k0 + tid) / p.H);
-                }
-                sRow[tid] = make_float2(m, r);
+                const float m = near ? m_all : lse2 == lse2 ? rintf(lse2) : 0.f;
+                sM[tid] = m;
+                // (a NaN lse stays one)
+                float r = 0.f;
+                if (tid < rows && !no_weight(p.lse[blk.row0 + tid])) r = exp2f(-fmaf(p.lse[blk.row0 + tid], kLog2e, -m));
+                sR[tid] = r;
                 sSees[tid] = s;
             }
+            const bool halves = n > (int)kPass;
+            float *const to = alone ? p.mass + (int64_t)blk.seq * p.ld_mass : ws.parts + (2 * (int64_t)(w.b - b0) + (halves ? set : 0)) * p.max_n;
+            const float *const prev = alone && p.prev ? p.prev + (int64_t)blk.seq * p.ld_mass : nullptr;
             epi_sync();
-            const int all = w.blk.rows > 0 ? sSees[0] : 0;        // entries that every row sees
-            const int n = columns(w.blk);
-            const int64_t part = (int64_t)(w.b - b0) * p.max_n;
-            float *const mass = p.mass + (int64_t)w.blk.seq * p.ld_mass;
-            const float *const prev = p.prev + (int64_t)w.blk.seq * p.ld_mass;
-            for (int t = w.k0; t < w.k1; ++t, ++tile) {
-                const uint32_t buf = tile % kBufs;
-                ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[buf], (tile / kBufs) & 1, abort_flag));
+            const int r0 = halves ? set * (int)kPass : 0, cols = min(n - r0, (int)kPass);
+            const int all = near && r0 < rows ? sSees[r0] : 0;    // entries that every row sees
+            for (int t = w.k0; t < w.k1 && ok; ++t, ++tile) {
+                if (!halves && (int)(tile & 1) != set) continue;
+                const int e = t * kEnt + ent;
+                const float before = prev && e < n_ent ? prev[e] : 0.f;     // (on its way while S is made)
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[set], used, abort_flag));
                 tc_fence_after();
                 if (!ok) break;
-                const int e = t * kEnt + tid;
-                const bool whole = (t + 1) * kEnt <= all;
+                used ^= 1;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                for (int c0 = 0; c0 < n; c0 += 16) {
-                    float x[16];
-                    tmem_ld16(tmem + 128 * buf + c0 + lane_q, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 16; c += 2) {
-                        const float4 row = *reinterpret_cast<const float4 *>(sRow + c0 + c);       // m, r, m, r
-                        const float2 y = fma_f32x2(make_float2(x[c], x[c + 1]), make_float2(l2s, l2s), make_float2(-row.x, -row.z));
-                        // (a NaN of a row that does not see the entry stays out)
-                        const float a = fmaf(fast_exp2(y.x), row.y, sum[c & 2]), b = fmaf(fast_exp2(y.y), row.w, sum[(c & 2) + 1]);
-                        if (whole || e < sSees[c0 + c]) sum[c & 2] = a;
-                        if (whole || e < sSees[c0 + c + 1]) sum[(c & 2) + 1] = b;
-                    }
-                }
+                if ((t + 1) * kEnt <= all) weigh<true>(tS, cols, sR + r0, sM + r0, sSees + r0, e, l2s, m_all, sum);
+                else weigh<false>(tS, cols, sR + r0, sM + r0, sSees + r0, e, l2s, m_all, sum);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_free[buf]);
-                if (e >= w.blk.n) continue;
+                if (lane == 0) arrive_relaxed(&bar_sfree[set]);
+                if (e >= n_ent) continue;
                 const float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                if (w.blk.alone) mass[e] = p.prev ? fmaf(p.decay, prev[e], s) : s;
-                else ws.parts[part + e] = s;
+                to[e] = prev ? fmaf(p.decay, before, s) : s;
             }
             // (all leave together if a wait gave up; else the block's rows are read)
             ok = !epi_any(!ok);
@@ -535,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(MassParams p, int b0,
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && *abort_flag) count_event(p.counters, CSA2_CNT_TIMEOUT);
-    if (warp == kWarpsEpi + kWarpsProd) {
+    if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -551,14 +721,18 @@ __global__ void __launch_bounds__(kFinishThreads) mass_finish_kernel(MassParams 
     for (int64_t item = blockIdx.x; item < p.ng * chunks; item += gridDim.x) {
         const int g = (int)(item / chunks), f = ws.group_first[g], l = ws.group_first[g + 1];
         const int lo = max(f, b0), hi = min(l, b1);
-        if (l - f < 2 || lo >= hi) continue;
+        if (lo >= hi || ws.blocks[f].alone) continue;
         const int64_t e = (item - g * chunks) * kFinishThreads + threadIdx.x;
         const Block &any = ws.blocks[f];
         if (e >= any.n_group) continue;
         float *const at = p.mass + any.seq * p.ld_mass + e;
         float s = 0.f;
         for (int b = lo; b < hi; ++b)
-            if (e < ws.blocks[b].n) s += ws.parts[(int64_t)(b - b0) * p.max_n + e];
+            if (e < ws.blocks[b].n) {
+                const float *const part = ws.parts + 2 * (int64_t)(b - b0) * p.max_n + e;
+                s += part[0];
+                if (ws.blocks[b].rows > (int)kPass) s += part[p.max_n];
+            }
         if (lo > f) *at += s;
         else *at = p.prev ? fmaf(p.decay, p.prev[any.seq * p.ld_mass + e], s) : s;
     }
@@ -566,27 +740,27 @@ __global__ void __launch_bounds__(kFinishThreads) mass_finish_kernel(MassParams 
 
 }  // namespace
 
-// Parts are kept for so many blocks at a time that they take up to 256 MB; more blocks
-// go in turns.
+// Parts, two to a block, are kept for so many blocks at a time that they take up to
+// 256 MB; more blocks go in turns.
 MassPlan mass_plan(int batch, int ng, int nq, int H, int64_t max_n)
 {
     MassPlan pl{};
     const int64_t blocks = ((int64_t)nq * H + kRows - 1) / kRows + ng;
-    pl.parts = std::max<int64_t>(64, (256ll << 20) / 4 / std::max<int64_t>(1, max_n));
+    pl.parts = std::max<int64_t>(32, (256ll << 20) / 8 / std::max<int64_t>(1, max_n));
     pl.blocks = blocks;
     const int64_t units = blocks * ((max_n + kEnt - 1) / kEnt);
     pl.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), units));
     pl.off_groups = align_up((size_t)(blocks + 1) * sizeof(Block), 256);
     pl.off_parts = pl.off_groups + align_up(((size_t)ng + 1 + batch) * 4, 256);
-    // (a single block's group has no parts, and there is none without 129 rows)
-    const bool any = (int64_t)nq * H > kRows;
-    pl.total = pl.off_parts + (any ? (size_t)std::min(pl.parts, blocks) * max_n * 4 : 0);
+    // (a group of one pass has no parts)
+    const bool any = (int64_t)nq * H > (int64_t)kPass;
+    pl.total = pl.off_parts + (any ? (size_t)std::min(pl.parts, blocks) * max_n * 8 : 0);
     return pl;
 }
 
 cudaError_t launch_mass(const MassParams &p, cudaStream_t st)
 {
-    constexpr size_t smem = 1024 + kStages * kStage + kQBytes + kRows * 12 + (2 * kStages + 2 * kBufs + 2) * 8 + 16;
+    constexpr size_t smem = 1024 + kQBytes + kUnits * kUnit + kScaleUnits * kScaleUnit + kRows * 12 + 32 + (2 * kUnits + 2 * kScaleUnits + 14) * 8 + 16;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     // the shared-memory attribute is set once per device (a bit each; setting it twice does no harm)
     static std::atomic<uint64_t> done{0};
@@ -599,12 +773,18 @@ cudaError_t launch_mass(const MassParams &p, cudaStream_t st)
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_release);
     }
+    static_assert(kEnt == 128, "seven bits");
+    const int run_log = p.pages.table != nullptr ? std::min(p.pages.log, 7) : 7;
+    CUtensorMap codes, scales;
+    e = make_tmap_rows_u8(&codes, p.codes, p.cap, CSA2_CODE_BYTES, 1 << run_log, 128, 128);
+    if (e == cudaSuccess) e = make_tmap_rows_u8(&scales, p.scales, p.cap, CSA2_SCALE_BYTES, 1 << run_log, 0);
+    if (e != cudaSuccess) return e;
     e = launch_k(mass_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 0, p);
     const int64_t items = p.ng * ((p.max_n + kFinishThreads - 1) / kFinishThreads);
     for (int64_t b0 = 0; b0 < p.plan.blocks && e == cudaSuccess; b0 += p.plan.parts) {
         const int b1 = (int)std::min(b0 + p.plan.parts, p.plan.blocks);
-        e = launch_k(mass_kernel, dim3(p.plan.ctas), dim3(kThreads), smem, st, 0, p, (int)b0, b1);
-        if (e == cudaSuccess && (int64_t)p.nq * p.H > kRows && items > 0)
+        e = launch_k(mass_kernel, dim3(p.plan.ctas), dim3(kThreads), smem, st, 0, codes, scales, p, (int)b0, b1, run_log);
+        if (e == cudaSuccess && (int64_t)p.nq * p.H > (int64_t)kPass && items > 0)
             e = launch_k(mass_finish_kernel, dim3((unsigned)std::min<int64_t>(items, device_sm_count() * 8)), dim3(kFinishThreads), 0, st, 0,
                          p, (int)b0, b1);
     }

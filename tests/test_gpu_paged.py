@@ -382,7 +382,7 @@ def test_mass_of_the_attention_adds_up():
 
 
 def test_mass_more_blocks_than_parts():
-    # 256 MB of parts hold 64 blocks at a million entries: 70 blocks of one group go in two turns
+    # 256 MB of parts hold 32 blocks at a million entries: 70 blocks of one group go in turns
     n, nq, h = 700, 70, 128
     s = Paged([n, 50], 64, 23)
     q = _queries(nq + 1, h, torch.bfloat16, 24)
