@@ -592,42 +592,42 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 const uint8_t *const src = sCodes + u * kUnit;
                 const uint4 sc = *reinterpret_cast<const uint4 *>(sScales + s * kScaleUnit + row * CSA2_SCALE_BYTES + 16 * half);
                 const uint32_t scale[4] = {sc.x, sc.y, sc.z, sc.w};
+                // (in registers at once, so that the next load of the unit is under way early)
+                uint4 c[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = *reinterpret_cast<const uint4 *>(src + sw128(row, i));
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar_read[u]);
+                    mbar_arrive(&bar_scread[s]);
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    uint4 c[4];
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(&bar_kfree[2 * half + j], (tile & 1) ^ 1, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4 *>(src + sw128(row, 4 * j + i));
-                    // (dequantised before the stage is free: what lies between its MMAs and the next
-                    // ones' is then no more than the stores)
-                    uint32_t r[2][32];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t r[32];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint4 v = c[2 * i + k];
+                            const uint4 v = c[4 * j + 2 * i + k];
                             const uint32_t s2 = e4m3x2_to_f16x2(scale[2 * j + i] >> (16 * k));
                             const uint32_t lo = __byte_perm(s2, 0, 0x1010), hi = __byte_perm(s2, 0, 0x3232);
                             const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 const uint4 o = fp4x8_to_f16(in[x], x < 2 ? lo : hi);
-                                uint32_t *const to = r[i] + 16 * k + 4 * x;
-                                to[0] = o.x; to[1] = o.y; to[2] = o.z; to[3] = o.w;
+                                uint32_t *const at = r + 16 * k + 4 * x;
+                                at[0] = o.x; at[1] = o.y; at[2] = o.z; at[3] = o.w;
                             }
                         }
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(&bar_kfree[2 * half + j], (tile & 1) ^ 1, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-                    tmem_st32u(to + 64 * j, r[0]);
-                    tmem_st32u(to + 64 * j + 32, r[1]);
+                        tmem_st32u(to + 64 * j + 32 * i, r);
+                    }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar_k[2 * half + j]);
-                }
-                if (lane == 0) {
-                    mbar_arrive(&bar_read[u]);
-                    mbar_arrive(&bar_scread[s]);
                 }
             }
         }
