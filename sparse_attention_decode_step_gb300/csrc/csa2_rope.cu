@@ -28,35 +28,49 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kResident = 4;                  // blocks to an SM
 
-// eight channels, 16-byte aligned
-template <typename T> struct Eight { uint4 w[sizeof(T) / 2]; };
+// Rows of x on their way to a warp, each in a slot of shared memory.  A lane copies the
+// 16 bytes 512 i + 16 lane of a row, so that a copy is of whole lines; of 16-bit types these
+// are its own channels, so that no other thread is waited for.
+// (4,096 x 64 bf16 rows: 115 us with one row ahead in registers, 104 with three here.)
+template <typename T>
+constexpr int kSlots = sizeof(T) == 2 ? 4 : 2;
 
 template <typename T>
-__device__ __forceinline__ void load8(const T *src, Eight<T> &e)
+constexpr uint32_t kPieces = 2 * sizeof(T) / 2;             // of a lane: 16 bytes of 16-bit types are eight channels
+
+template <typename T>
+__device__ __forceinline__ void copy_row(uint32_t slot, const T *src, int lane, bool in)
 {
+    if (in) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) e.w[i] = reinterpret_cast<const uint4 *>(src)[i];
+        for (int i = 0; i < (int)kPieces<T>; ++i) {
+            const T *const from = src + (32 * i + lane) * (16 / (int)sizeof(T));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + 512 * i + 16 * lane), "l"(from) : "memory");
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 template <typename T>
-__device__ __forceinline__ void as_f32(const Eight<T> &e, float *x)
+__device__ __forceinline__ void read_row(uint32_t slot, int lane, float (&x)[16])
 {
-    if constexpr (__is_same(T, float)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            x[4 * i] = __uint_as_float(e.w[i].x); x[4 * i + 1] = __uint_as_float(e.w[i].y);
-            x[4 * i + 2] = __uint_as_float(e.w[i].z); x[4 * i + 3] = __uint_as_float(e.w[i].w);
-        }
-    } else {
-        const uint32_t w[4] = {e.w[0].x, e.w[0].y, e.w[0].z, e.w[0].w};
+    for (int i = 0; i < (int)kPieces<T>; ++i) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(sizeof(T) == 2 ? slot + 512 * i + 16 * lane : slot + 1024 * (i >> 1) + 32 * lane + 16 * (i & 1))
+                     : "memory");
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (__is_same(T, __half)) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                x[2 * i] = f.x; x[2 * i + 1] = f.y;
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (__is_same(T, float)) {
+                x[4 * i + k] = __uint_as_float(w[k]);
+            } else if constexpr (__is_same(T, __half)) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                x[8 * i + 2 * k] = f.x; x[8 * i + 2 * k + 1] = f.y;
             } else {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+                x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
             }
         }
     }
@@ -83,11 +97,13 @@ __device__ __forceinline__ void store8(T *dst, const float *x)
 template <typename T, typename O>
 __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeParams p, uint32_t per, uint32_t parts)
 {
-    __shared__ uint64_t sTurn[CSA2_D / 2];
-    __shared__ float4 sCs[kWarps][CSA2_D / 4];           // (cos, sin) of two pairs
-    __shared__ float4 sY[kWarps][CSA2_D / 4];            // the rotated part of a row (halves)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int pairs = p.rot / 2;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint32_t slots = smem_u32(smem) + warp * (kSlots<T> * CSA2_D * (uint32_t)sizeof(T));       // [slots][row]
+    uint64_t *const sTurn = reinterpret_cast<uint64_t *>(smem + kWarps * kSlots<T> * CSA2_D * sizeof(T));
+    float4 *const sCs = reinterpret_cast<float4 *>(sTurn + pairs) + warp * (pairs / 2);           // (cos, sin) of two pairs
+    float4 *const sY = reinterpret_cast<float4 *>(sTurn + pairs) + (kWarps + warp) * (pairs / 2); // the rotated part of a row (halves)
     pdl_wait();
     if ((int)threadIdx.x < pairs) {
         // f / 2 pi in two parts, of which only the fraction of a turn counts
@@ -111,33 +127,43 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
     const T *const x = static_cast<const T *>(p.x);
     O *const out = static_cast<O *>(p.out);
     const uint32_t units = p.n * parts, step = gridDim.x * kWarps;
-    Eight<T> next[2];
-    auto load = [&](uint32_t token, uint32_t head) {
-        const T *src = x + (uint64_t)token * p.ld_x + head * CSA2_D + 8 * lane;
-        load8(src, next[0]);
-        load8(src + 256, next[1]);
-    };
-    uint32_t u = blockIdx.x * kWarps + warp;
-    uint32_t token = u / parts, head = (u - token * parts) * per, left = min(per, p.H - head);
-    if (u < units) load(token, head);
-    bool turn = true;                                    // a new token's angles are due
-    while (u < units) {
-        float v[16];
-        as_f32(next[0], v);
-        as_f32(next[1], v + 8);
-        O *const dst = out + (uint64_t)token * p.ld_out + head * CSA2_D + 8 * lane;
-        const bool due = turn;
-        const uint32_t now = token;
-        turn = --left == 0;
-        if (turn) {
-            u += step;
+    // a warp's rows in order
+    struct Place {
+        uint32_t u, token, head, left;
+        __device__ __forceinline__ void start(uint32_t at, uint32_t per, uint32_t parts, uint32_t H)
+        {
+            u = at;
             token = u / parts;
             head = (u - token * parts) * per;
-            left = min(per, p.H - head);
-        } else {
-            ++head;
+            left = min(per, H - head);
         }
-        if (u < units) load(token, head);
+        __device__ __forceinline__ bool next(uint32_t step, uint32_t per, uint32_t parts, uint32_t H)      // true: another unit
+        {
+            if (--left > 0) { ++head; return false; }
+            start(u + step, per, parts, H);
+            return true;
+        }
+    };
+    Place now, ahead;
+    now.start(blockIdx.x * kWarps + warp, per, parts, p.H);
+    ahead = now;
+    auto load = [&](uint32_t slot) {
+        copy_row(slots + slot * (uint32_t)(CSA2_D * sizeof(T)), x + (uint64_t)ahead.token * p.ld_x + ahead.head * CSA2_D, lane, ahead.u < units);
+        if (ahead.u < units) ahead.next(step, per, parts, p.H);
+    };
+#pragma unroll
+    for (int i = 0; i < kSlots<T> - 1; ++i) load(i);
+    bool turn = true;                                    // a new token's angles are due
+    for (uint32_t slot = 0; now.u < units; slot = (slot + 1) % kSlots<T>) {
+        load((slot + kSlots<T> - 1) % kSlots<T>);              // (the row before was read from there)
+        asm volatile("cp.async.wait_group %0;" ::"n"(kSlots<T> - 1) : "memory");
+        if constexpr (sizeof(T) == 4) __syncwarp();      // (the row before is read: its sum came from every lane)
+        float v[16];
+        read_row<T>(slots + slot * (uint32_t)(CSA2_D * sizeof(T)), lane, v);
+        O *const dst = out + (uint64_t)now.token * p.ld_out + now.head * CSA2_D + 8 * lane;
+        const bool due = turn;
+        const uint32_t token = now.token;
+        turn = now.next(step, per, parts, p.H);
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
@@ -148,12 +174,12 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
         for (int i = 0; i < 16; ++i) v[i] *= r * w[i];
         if (pairs > 0) {
             if (due) {
-                const int64_t pos = p.pos[now];
+                const int64_t pos = p.pos[token];
                 __syncwarp();                            // (the last token's are read)
                 for (int i = lane; i < pairs; i += 32) {
                     float s, c;
                     sincospif((float)(int32_t)(((uint64_t)pos * sTurn[i]) >> 32) * 0x1p-31f, &s, &c);
-                    reinterpret_cast<float2 *>(sCs[warp])[i] = make_float2(c, s);
+                    reinterpret_cast<float2 *>(sCs)[i] = make_float2(c, s);
                 }
                 __syncwarp();
             }
@@ -163,7 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
                     if (at[h] >= 0) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float4 cs = sCs[warp][at[h] / 4 + i];
+                            const float4 cs = sCs[at[h] / 4 + i];
                             float *const y = v + 8 * h + 4 * i;
                             const float a = y[0], b = y[1], c = y[2], d = y[3];
                             y[0] = a * cs.x - b * cs.y; y[1] = a * cs.y + b * cs.x;
@@ -174,8 +200,8 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (at[h] >= 0) {
-                        sY[warp][at[h] / 4] = make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
-                        sY[warp][at[h] / 4 + 1] = make_float4(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]);
+                        sY[at[h] / 4] = make_float4(v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]);
+                        sY[at[h] / 4 + 1] = make_float4(v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]);
                     }
                 __syncwarp();
 #pragma unroll
@@ -185,8 +211,8 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
                         const int pair = at[h] - (second ? pairs : 0), other = pair + (second ? 0 : pairs);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float4 o = sY[warp][other / 4 + i];
-                            const float4 c0 = sCs[warp][pair / 2 + 2 * i], c1 = sCs[warp][pair / 2 + 2 * i + 1];
+                            const float4 o = sY[other / 4 + i];
+                            const float4 c0 = sCs[pair / 2 + 2 * i], c1 = sCs[pair / 2 + 2 * i + 1];
                             const float oo[4] = {o.x, o.y, o.z, o.w}, c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
                             float *const y = v + 8 * h + 4 * i;
 #pragma unroll
@@ -206,13 +232,18 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
 template <typename T, typename O>
 static cudaError_t launch_rope_as(const RopeParams &p, cudaStream_t st)
 {
-    // as many heads to a warp as leave the GPU full
+    // as many heads (a power of two) to a unit as leave each warp of a full GPU eight units
     const uint64_t rows = (uint64_t)p.n * p.H, warps = (uint64_t)device_sm_count() * kResident * kWarps;
-    const uint32_t per = (uint32_t)std::min<uint64_t>(p.H, std::max<uint64_t>(1, rows / warps));
+    uint32_t per = 1;
+    while (2 * per <= p.H && 2 * per * 8 * warps <= rows) per *= 2;
     const uint32_t parts = (p.H + per - 1) / per;
     const uint64_t blocks = ((uint64_t)p.n * parts + kWarps - 1) / kWarps;
-    const cudaError_t e = launch_k(norm_rope_kernel<T, O>, dim3((unsigned)std::min<uint64_t>(blocks, warps / kWarps)),
-                                   dim3(32 * kWarps), 0, st, 0, p, per, parts);
+    // slots, turns, and for each warp (cos, sin) and, for halves, a row's rotated part
+    const size_t smem = kWarps * kSlots<T> * CSA2_D * sizeof(T) + (size_t)p.rot / 2 * 8 + (size_t)kWarps * p.rot * 4 * (p.halves ? 2 : 1);
+    cudaError_t e = cudaSuccess;
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(norm_rope_kernel<T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+    if (e == cudaSuccess)
+        e = launch_k(norm_rope_kernel<T, O>, dim3((unsigned)std::min<uint64_t>(blocks, warps / kWarps)), dim3(32 * kWarps), smem, st, 0, p, per, parts);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
