@@ -148,11 +148,12 @@ csa2_status check_cache(const csa2_cache *c, bool need_keys, bool need_base = tr
     return CSA2_OK;
 }
 
-csa2_status check_pages(const csa2_pages *p)
+csa2_status check_pages(const csa2_pages *p, int64_t cap)
 {
     if (p == nullptr) return CSA2_OK;
     CSA2_REQUIRE(p->table && p->ld >= 1 && p->ld < (1LL << 31), CSA2_ERR_INVALID_ARG);
     CSA2_REQUIRE(p->page >= 16 && (p->page & (p->page - 1)) == 0, CSA2_ERR_UNSUPPORTED);
+    CSA2_REQUIRE(p->page <= cap, CSA2_ERR_INVALID_ARG);
     CSA2_REQUIRE(al4(p->table), CSA2_ERR_ALIGN);
     return CSA2_OK;
 }
@@ -657,7 +658,7 @@ csa2_status group_attn(const csa2_cache *cache, bool chunk, const csa2_pages *pa
                        void *workspace, size_t ws_bytes, uint32_t *counters, void *stream)
 {
     csa2_status s = check_cache(cache, false, pages == nullptr);
-    if (s == CSA2_OK) s = check_pages(pages);
+    if (s == CSA2_OK) s = check_pages(pages, cache->cap);
     if (s != CSA2_OK) return s;
     CSA2_REQUIRE(groups != nullptr && groups->ng >= 0 && groups->nq >= 0, CSA2_ERR_INVALID_ARG);
     if (groups->ng == 0 || groups->nq == 0) return CSA2_OK;
@@ -740,7 +741,7 @@ csa2_status csa2_attn_mass(const csa2_cache *cache, const csa2_pages *pages, con
                            int64_t ld_mass, void *workspace, size_t ws_bytes, uint32_t *counters, void *stream)
 {
     csa2_status s = check_cache(cache, false, pages == nullptr);
-    if (s == CSA2_OK) s = check_pages(pages);
+    if (s == CSA2_OK) s = check_pages(pages, cache->cap);
     if (s != CSA2_OK) return s;
     CSA2_REQUIRE(groups != nullptr && groups->ng >= 0 && groups->nq >= 0, CSA2_ERR_INVALID_ARG);
     if (groups->ng == 0) return CSA2_OK;
@@ -802,8 +803,8 @@ csa2_status csa2_cache_evict(const csa2_cache *cache, const csa2_pages *pages, c
     const bool keys = cache != nullptr && cache->kidx != nullptr;
     csa2_status s = check_cache(cache, keys, pages == nullptr);
     if (s == CSA2_OK) s = check_cache(dst, keys, dst_pages == nullptr);
-    if (s == CSA2_OK) s = check_pages(pages);
-    if (s == CSA2_OK) s = check_pages(dst_pages);
+    if (s == CSA2_OK) s = check_pages(pages, cache->cap);
+    if (s == CSA2_OK) s = check_pages(dst_pages, dst->cap);
     if (s != CSA2_OK) return s;
     CSA2_REQUIRE(cache->batch == dst->batch && keys == (dst->kidx != nullptr) && (!keys || cache->d_idx == dst->d_idx),
                  CSA2_ERR_INVALID_ARG);
