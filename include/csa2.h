@@ -488,7 +488,8 @@ size_t csa2_mass_workspace_size(int32_t batch, int32_t ng, int32_t nq, int32_t H
  * Sequences outside the contract (number, n < 0 or above max_n, pages or room too
  * few on either side) are skipped, counted in CSA2_CNT_BAD_INPUT (room: in
  * CSA2_CNT_CAPACITY), and their seq_len left.  Rows that the call writes must not be
- * among those it reads, nor mass_out overlap mass (refused).
+ * among those it reads (the same arrays with the same pages, or with the same
+ * seq_base, are refused), nor mass_out overlap mass (refused).
  * kept, mass, mass_out: 4-byte aligned; workspace 16-byte. */
 csa2_status csa2_cache_evict(const csa2_cache *cache, const csa2_pages *pages,
                              const csa2_cache *dst, const csa2_pages *dst_pages,

@@ -808,6 +808,10 @@ csa2_status csa2_cache_evict(const csa2_cache *cache, const csa2_pages *pages, c
     if (s != CSA2_OK) return s;
     CSA2_REQUIRE(cache->batch == dst->batch && keys == (dst->kidx != nullptr) && (!keys || cache->d_idx == dst->d_idx),
                  CSA2_ERR_INVALID_ARG);
+    // (rows onto themselves)
+    CSA2_REQUIRE(cache->codes != dst->codes || (pages == nullptr) != (dst_pages == nullptr) ||
+                     (pages ? pages->table != dst_pages->table : cache->seq_base != dst->seq_base),
+                 CSA2_ERR_INVALID_ARG);
     CSA2_REQUIRE(ns <= 65535, CSA2_ERR_UNSUPPORTED);
     CSA2_REQUIRE(ns >= 0 && (seq != nullptr || ns == cache->batch), CSA2_ERR_INVALID_ARG);
     if (ns == 0) return CSA2_OK;

@@ -663,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             top = fmaxf(fmaxf(sTop[0], sTop[1]), fmaxf(sTop[2], sTop[3]));
             low = fminf(fminf(sTop[4], sTop[5]), fminf(sTop[6], sTop[7]));
             const float m_all = rintf(top);
-            const bool near = top - low < 64.f;            // (false without any weight)
+            // (false without any weight; below 2^-96 a column without a row, whose S is 0, would not stay finite)
+            const bool near = top - low < 64.f && top > -96.f;
             if (tid < kRows) {
                 const float m = near ? m_all : lse2 == lse2 ? rintf(lse2) : 0.f;
                 sM[tid] = m;

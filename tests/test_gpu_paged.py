@@ -395,6 +395,54 @@ def test_mass_more_blocks_than_parts():
     assert not mass[0, n:].any() and not mass[1, 50:].any()
 
 
+@pytest.mark.parametrize("lens", [[1], [5, 3, 130], [1000, 7]])
+def test_mass_of_contiguous_sequences(lens):
+    # rows from seq_base on, of any alignment; a cache smaller than a tile
+    base = [0]
+    for n in lens:
+        base.append(base[-1] + n)
+    cap = -(-base[-1] // 8) * 8
+    g = torch.Generator().manual_seed(27)
+    codes = torch.randint(0, 256, (cap, 256), generator=g, dtype=torch.uint8)
+    scales = torch.randint(0x20, 0x3C, (cap, 32), generator=g, dtype=torch.uint8)
+    cache = csa.Cache.over(codes.to(DEV), scales.to(DEV), None, None, torch.tensor(base, device=DEV), _ints(lens), 1)
+    off = [0] + [3 * (b + 1) for b in range(len(lens))]
+    q = _queries(off[-1], 20, torch.bfloat16, 28)
+    lse = torch.full((off[-1], 20), 5.0, device=DEV)
+    mass = torch.zeros(len(lens), max(lens), device=DEV)
+    csa.attn_mass(cache, csa.Groups(list(range(len(lens))), off), q, lse, mass)
+    torch.cuda.synchronize()
+
+    def values(b):
+        r = slice(base[b], base[b + 1])
+        return torch.from_numpy(O.fp4_decode_rows(codes[r].numpy(), scales[r].numpy())).reshape(-1, 512).to(DEV)
+
+    _check_mass(values, off, lens, None, 1, q, lse, None, 0.0, mass)
+
+
+@pytest.mark.parametrize("far", [-150.0, 150.0])
+@pytest.mark.parametrize("spread", [0.0, 90.0])
+def test_mass_of_logits_far_from_zero(far, spread):
+    # every value of the cache near 3, every query near far / (3 * 512): logits, and so lse, far from zero;
+    # rows that lie far from each other; columns without a row (5 and 65 of 16 and 80)
+    s = Paged([700, 100], 16, 29)
+    g = torch.Generator().manual_seed(30)
+    nib = torch.randint(4, 7, s.cache.codes.shape + (2,), generator=g, dtype=torch.uint8)
+    s.cache.codes.copy_(nib[..., 0] | (nib[..., 1] << 4))
+    s.cache.scales.fill_(0x38)                                    # 1.0
+    at = torch.full((14,), far)
+    at[1::3] -= math.copysign(spread, far)
+    q = ((at / 1536)[:, None, None] + 0.002 * torch.randn(14, 5, 512, generator=g)).to(torch.float16).to(DEV)
+    groups, pos = csa.Groups([1, 0], [0, 1, 14]), _ints([99, 687])
+    out, lse = torch.zeros(14, 5, 512, device=DEV), torch.zeros(14, 5, device=DEV)
+    csa.chunk_attn(s.cache, groups, q, out, lse, pos=pos, pages=s.pages)
+    mass = torch.zeros(2, 700, device=DEV)
+    csa.attn_mass(s.cache, groups, q, lse, mass, pos=pos, pages=s.pages)
+    torch.cuda.synchronize()
+    assert lse[0, 0].abs() > 100
+    _check_mass(lambda i: s.values(1 - i), [0, 1, 14], [100, 700], [99, 687], 1, q, lse, None, 0.0, mass, seqs=[1, 0])
+
+
 def test_mass_out_of_contract():
     s = Paged([200, 100, 300], 32, 25)
     seqs, off = [0, 0, 3, 2, 2], [0, 3, 5, 6, 8, 9]               # groups 1 and 4: again; 2: no sequence
@@ -440,6 +488,7 @@ EVICTS = [
     (16, 0, [20 + 3 * i for i in range(130)], 37, 2, 5),
     (128, 128, [513], 1, 0, 1),
     (128, 64, [100], 1 << 20, 5, 7),
+    (32, 0, [12000 - 50 * i for i in range(100)], 5000, 100, 200),
 ]
 
 
@@ -510,6 +559,34 @@ def test_evict_some_sequences_in_place_of_their_lengths():
         assert _np(kept[i]).tolist() == want
         src = s._rows(s.table_host, 16, b, lens[b])[torch.tensor(want)].to(DEV)
         assert torch.equal(s.cache.codes[s._rows(s.to_host, 16, b, 64).to(DEV)], s.cache.codes[src])
+
+
+def test_rows_past_two_gigabytes_of_codes():
+    # pages at the far end of a cache of 17 million rows give what a small cache gives
+    s = Paged([900, 130], 64, 75, to=[50, 50])
+    cap, shift = 17 << 20, (17 << 20) // 64 - 40
+    codes = torch.empty(cap, 256, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(cap, 32, dtype=torch.uint8, device=DEV)
+    n = s.cache.codes.shape[0]
+    assert n <= 40 * 64
+    codes[shift * 64:shift * 64 + n], scales[shift * 64:shift * 64 + n] = s.cache.codes, s.cache.scales
+    big = csa.Cache.over(codes, scales, None, None, None, s.seq_len, 1)
+    q = _queries(40, 64, torch.bfloat16, 76)
+    groups, pos = csa.Groups([0, 1], [0, 30, 40]), _ints([870, 120])
+    got = []
+    for cache, add in ((s.cache, 0), (big, shift)):
+        pages, to = csa.Pages((s.table_host + add).to(DEV), 64), csa.Pages((s.to_host + add).to(DEV), 64)
+        out, lse, mass = torch.zeros(40, 64, 512, device=DEV), torch.zeros(40, 64, device=DEV), torch.zeros(2, 900, device=DEV)
+        csa.chunk_attn(cache, groups, q, out, lse, pos=pos, pages=pages)
+        csa.attn_mass(cache, groups, q, lse, mass, pos=pos, pages=pages)
+        kept = torch.zeros(2, 50, dtype=torch.int32, device=DEV)
+        short = csa.Cache.over(cache.codes, cache.scales, None, None, None, torch.zeros_like(s.seq_len), 1)
+        csa.cache_evict(cache, short, mass, 50, kept, pages=pages, to_pages=to)
+        x = torch.zeros(100, 512, device=DEV)
+        csa.cache_read(short, to.rows(torch.arange(2, device=DEV).repeat_interleave(50), torch.arange(50, device=DEV).repeat(2)), x)
+        got.append((out, lse, mass, kept, x))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
 def test_evict_out_of_contract():

@@ -100,7 +100,7 @@ def test_mass_workspace_sizes():
 # ---------------------------------------------------------------- eviction
 def _evict(cache=None, pages=None, to=None, to_pages=None, seq=None, ns=2, mass=P, ld=64, max_n=64, keep=16, first=2, last=3, kept=P,
            ld_kept=16, out=None, ld_out=0, ws=P, ws_bytes=1 << 40, counters=None):
-    return csa.lib().csa2_cache_evict(cache or _cache(), pages, to or _cache(), to_pages, seq, ns, mass, ld, max_n, keep, first, last,
+    return csa.lib().csa2_cache_evict(cache or _cache(), pages, to or _cache(codes=8192), to_pages, seq, ns, mass, ld, max_n, keep, first, last,
                                       kept, ld_kept, out, ld_out, ws, ws_bytes, counters, None)
 
 
@@ -114,7 +114,8 @@ def test_evict_rejects_bad_arguments_on_host():
                 dict(mass=ctypes.c_void_p(8192), out=ctypes.c_void_p(8192 - 16 * 2 * 4 + 4), ld_out=16),
                 dict(to=_cache(batch=3)), dict(to=_cache(kidx=None)), dict(cache=_cache(kidx=None)), dict(to=_cache(d_idx=64)),
                 dict(cache=_cache(seq_base=None)), dict(to=_cache(seq_base=None)), dict(to_pages=_pages(ld=0)),
-                dict(to=_cache(cap=8), to_pages=_pages(page=16)), dict(ws=None), dict(first=(1 << 31) - 1, last=(1 << 31) - 1)):
+                dict(to=_cache(cap=8), to_pages=_pages(page=16)), dict(ws=None), dict(first=(1 << 31) - 1, last=(1 << 31) - 1),
+                dict(to=_cache()), dict(to=_cache(), pages=_pages(), to_pages=_pages())):          # onto itself
         assert _evict(**bad) == INVALID, bad
     for bad in (dict(ns=65536, seq=P), dict(cache=_cache(d_idx=96), to=_cache(d_idx=96)), dict(to_pages=_pages(page=17))):
         assert _evict(**bad) == UNSUPPORTED, bad
