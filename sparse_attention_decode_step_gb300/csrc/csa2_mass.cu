@@ -40,16 +40,18 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kWarpsEpi = 8, kWarpsProd = 8;          // and one issues the MMAs, one the loads
-constexpr int kThreads = 32 * (kWarpsEpi + kWarpsProd + 2);
-constexpr int kWarpMma = kWarpsEpi + kWarpsProd, kWarpLoad = kWarpMma + 1;
+// Warp 0 issues the MMAs, warp 1 the loads (the first ones: of the warps that could issue, a
+// scheduler seems to take the first, and these two hold up all others), 2 and 3 are
+// idle, so that a warp's TMEM lanes go by its number mod 4.
+constexpr int kWarpMma = 0, kWarpLoad = 1, kWarpEpi = 4, kWarpsEpi = 8, kWarpProd = 12, kWarpsProd = 8;
+constexpr int kThreads = 32 * (kWarpProd + kWarpsProd);
 constexpr int kRows = kMassRows, kEnt = kMassEntries;
 constexpr uint32_t kPass = 64;                             // rows of a pass
 constexpr int kUnits = 4, kScaleUnits = 3;            // codes: half tiles (256 channels), scales: tiles
 constexpr uint32_t kUnit = kEnt * 128, kScaleUnit = kEnt * CSA2_SCALE_BYTES;
 constexpr uint32_t kQBytes = kRows * CSA2_D * 2;      // [8 atoms of 64 channels][128 rows][128 B]
 constexpr uint32_t kQAtom = kRows * 128;
-constexpr uint32_t kColS = 256;                       // TMEM: K in columns 0 .. 255 (four stages of 128 channels), S from here
+constexpr uint32_t kColS = 256;                       // TMEM: K in columns 0 .. 255 (two halves), S from here
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPlanThreads = 1024;
 constexpr int kFinishThreads = 256;
@@ -376,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     uint64_t *bar_read = bar_raw + kUnits;                           // [4] half tile dequantised
     uint64_t *bar_sc = bar_read + kUnits;                            // [3] scales loaded
     uint64_t *bar_scread = bar_sc + kScaleUnits;                     // [3] scales read
-    uint64_t *bar_k = bar_scread + kScaleUnits;                      // [4] stage of K stored
-    uint64_t *bar_kfree = bar_k + 4;                                 // [4] its MMAs done
-    uint64_t *bar_s = bar_kfree + 4;                                 // [2] S complete
+    uint64_t *bar_k = bar_scread + kScaleUnits;                      // [2] half of K stored
+    uint64_t *bar_kfree = bar_k + 2;                                 // [2] its MMAs done
+    uint64_t *bar_s = bar_kfree + 2;                                 // [2] S complete
     uint64_t *bar_sfree = bar_s + 2;                                 // [2] S read
     uint64_t *bar_q = bar_sfree + 2;                                 // queries stored
     uint64_t *bar_piece = bar_q + 1;                                 // a piece's MMAs done
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     if (tid == 0) {
         for (int i = 0; i < kUnits; ++i) { mbar_init(&bar_raw[i], 1); mbar_init(&bar_read[i], kWarpsProd / 2); }   // (a half tile, a stage: four warps)
         for (int i = 0; i < kScaleUnits; ++i) { mbar_init(&bar_sc[i], 1); mbar_init(&bar_scread[i], kWarpsProd); }
-        for (int i = 0; i < 4; ++i) { mbar_init(&bar_k[i], kWarpsProd / 2); mbar_init(&bar_kfree[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&bar_k[i], kWarpsProd / 2); mbar_init(&bar_kfree[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&bar_s[i], 1); mbar_init(&bar_sfree[i], kWarpsEpi / 2); }
         mbar_init(bar_q, kWarpsProd);
         mbar_init(bar_piece, 1);
@@ -446,16 +448,16 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             wait(&bar_sfree[kBuf], used[kBuf]);
             used[kBuf] ^= 1;
 #pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
-                if (kR == 0) wait(&bar_k[j], tile & 1);
+            for (uint32_t h = 0; h < 2; ++h) {
+                if (kR == 0) wait(&bar_k[h], tile & 1);
                 if (!ok) break;
                 if (elected) {
 #pragma unroll
-                    for (uint32_t ks = 0; ks < 8; ++ks)
-                        mma_f16_ts(t0 + (kColS + 128 * kBuf + 64 * (j >> 1)), t0 + (64 * j + 8 * ks),
-                                   dq + (kR * 128 / 16 + (2 * j + (ks >> 2)) * (kQAtom >> 4) + 2 * (ks & 3)), id, ks > 0 ? 1u : j & 1);
-                    if (last) mma_commit(&bar_kfree[j]);
-                    if (j == 3) mma_commit(&bar_s[kBuf]);
+                    for (uint32_t ks = 0; ks < 16; ++ks)
+                        mma_f16_ts(t0 + (kColS + 128 * kBuf + 64 * h), t0 + (128 * h + 8 * ks),
+                                   dq + (kR * 128 / 16 + (4 * h + (ks >> 2)) * (kQAtom >> 4) + 2 * (ks & 3)), id, ks > 0 ? 1u : 0u);
+                    if (last) mma_commit(&bar_kfree[h]);
+                    if (h == 1) mma_commit(&bar_s[kBuf]);
                 }
                 __syncwarp();
             }
@@ -549,11 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             for (uint32_t i = sc_loads > kScaleUnits ? sc_loads - kScaleUnits : 0; i < sc_loads; ++i)
                 mbar_wait<true>(&bar_sc[i % kScaleUnits], (i / kScaleUnits) & 1, &no_abort);
         }
-    } else if (warp >= kWarpsEpi) {
+    } else if (warp >= kWarpProd) {
         // ============================================== producers
         // A warp dequantises the 32 entries of its TMEM lanes, an entry a lane, in one
-        // half of the channels: two of the four stages, 64 bytes of codes each.
-        const int pw = warp - kWarpsEpi, quarter = warp & 3, half = pw >> 2;
+        // half of the channels: 128 bytes of codes, 128 TMEM columns.
+        const int pw = warp - kWarpProd, quarter = warp & 3, half = pw >> 2;
         const int row = 32 * quarter + lane;
         const uint32_t to = tmem + 128 * half + ((uint32_t)(32 * quarter) << 16);
         uint32_t tile = 0, pieces = 0;
@@ -601,43 +603,40 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                     mbar_arrive(&bar_read[u]);
                     mbar_arrive(&bar_scread[s]);
                 }
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_kfree[half], (tile & 1) ^ 1, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(&bar_kfree[2 * half + j], (tile & 1) ^ 1, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t r[32];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t r[32];
+                    for (int k = 0; k < 2; ++k) {
+                        const uint4 v = c[2 * i + k];
+                        const uint32_t s2 = e4m3x2_to_f16x2(scale[i] >> (16 * k));
+                        const uint32_t lo = __byte_perm(s2, 0, 0x1010), hi = __byte_perm(s2, 0, 0x3232);
+                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint4 v = c[4 * j + 2 * i + k];
-                            const uint32_t s2 = e4m3x2_to_f16x2(scale[2 * j + i] >> (16 * k));
-                            const uint32_t lo = __byte_perm(s2, 0, 0x1010), hi = __byte_perm(s2, 0, 0x3232);
-                            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const uint4 o = fp4x8_to_f16(in[x], x < 2 ? lo : hi);
-                                uint32_t *const at = r + 16 * k + 4 * x;
-                                at[0] = o.x; at[1] = o.y; at[2] = o.z; at[3] = o.w;
-                            }
+                        for (int x = 0; x < 4; ++x) {
+                            const uint4 o = fp4x8_to_f16(in[x], x < 2 ? lo : hi);
+                            uint32_t *const at = r + 16 * k + 4 * x;
+                            at[0] = o.x; at[1] = o.y; at[2] = o.z; at[3] = o.w;
                         }
-                        tmem_st32u(to + 64 * j + 32 * i, r);
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_k[2 * half + j]);
+                    tmem_st32u(to + 32 * i, r);
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_k[half]);
             }
         }
-    } else {
+    } else if (warp >= kWarpEpi) {
         // ============================================== epilogue: a thread has an entry
         // Two sets of four warps, each with an S buffer of its own: of up to 64 rows they take
         // tiles in turn, of more each takes its half of the rows.  What a tile costs in
         // latency (S read, exponentials, prev) then has two passes' time.
         const float l2s = p.sm_scale * kLog2e;
-        const int ent = tid & (kEnt - 1), set = tid / kEnt;
+        const int at = tid - 32 * kWarpEpi, ent = at & (kEnt - 1), set = at / kEnt;
         const uint32_t tS = tmem + kColS + 128 * set + ((uint32_t)(32 * (warp & 3)) << 16);
         uint32_t tile = 0, used = 0;           // parity of the next wait
         for (; more && ok; more = w.next(ws)) {
@@ -647,10 +646,10 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             // Where the rows' lse2 lie within 2^64 of each other, one m (the largest) serves them all.
             float lse2 = NAN;                  // (a row without weight, or past the block's)
             int s = 0;
-            if (tid < rows) {
-                const float lse = p.lse[blk.row0 + tid];
+            if (at < rows) {
+                const float lse = p.lse[blk.row0 + at];
                 if (!no_weight(lse)) lse2 = lse * kLog2e;
-                s = sees(p, blk.causal, blk.pos, blk.n_group, (blk.k0 + tid) / p.H);
+                s = sees(p, blk.causal, blk.pos, blk.n_group, (blk.k0 + at) / p.H);
             }
             float top = lse2, low = lse2;
 #pragma unroll
@@ -658,21 +657,21 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
             }
-            if (warp < kRows / 32 && lane == 0) { sTop[warp] = top; sTop[4 + warp] = low; }
+            if (at < kRows && lane == 0) { sTop[at >> 5] = top; sTop[4 + (at >> 5)] = low; }
             epi_sync();
             top = fmaxf(fmaxf(sTop[0], sTop[1]), fmaxf(sTop[2], sTop[3]));
             low = fminf(fminf(sTop[4], sTop[5]), fminf(sTop[6], sTop[7]));
             const float m_all = rintf(top);
             // (false without any weight; below 2^-96 a column without a row, whose S is 0, would not stay finite)
             const bool near = top - low < 64.f && top > -96.f;
-            if (tid < kRows) {
+            if (at < kRows) {
                 const float m = near ? m_all : lse2 == lse2 ? rintf(lse2) : 0.f;
-                sM[tid] = m;
+                sM[at] = m;
                 // (a NaN lse stays one)
                 float r = 0.f;
-                if (tid < rows && !no_weight(p.lse[blk.row0 + tid])) r = exp2f(-fmaf(p.lse[blk.row0 + tid], kLog2e, -m));
-                sR[tid] = r;
-                sSees[tid] = s;
+                if (at < rows && !no_weight(p.lse[blk.row0 + at])) r = exp2f(-fmaf(p.lse[blk.row0 + at], kLog2e, -m));
+                sR[at] = r;
+                sSees[at] = s;
             }
             const bool halves = n > (int)kPass;
             float *const to = alone ? p.mass + (int64_t)blk.seq * p.ld_mass : ws.parts + (2 * (int64_t)(w.b - b0) + (halves ? set : 0)) * p.max_n;
@@ -761,7 +760,7 @@ MassPlan mass_plan(int batch, int ng, int nq, int H, int64_t max_n)
 
 cudaError_t launch_mass(const MassParams &p, cudaStream_t st)
 {
-    constexpr size_t smem = 1024 + kQBytes + kUnits * kUnit + kScaleUnits * kScaleUnit + kRows * 12 + 32 + (2 * kUnits + 2 * kScaleUnits + 14) * 8 + 16;
+    constexpr size_t smem = 1024 + kQBytes + kUnits * kUnit + kScaleUnits * kScaleUnit + kRows * 12 + 32 + (2 * kUnits + 2 * kScaleUnits + 10) * 8 + 16;
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     // the shared-memory attribute is set once per device (a bit each; setting it twice does no harm)
     static std::atomic<uint64_t> done{0};
