@@ -101,6 +101,7 @@ struct Group<true> : Group<false> {
     int seq;
     bool causal;
     int pos;             // token position of its first query
+    int queries;
     int tile_n;          // (of a piece of work:) entries that some row of its row tile sees
 };
 
@@ -109,6 +110,10 @@ __device__ __forceinline__ Group<kChunk> group_of(const DenseParams &p, int g)
 {
     Group<kChunk> r{};
     const int b = p.g_seq[g], a = p.g_off[g], e = p.g_off[g + 1];
+    if constexpr (kChunk) {
+        r.causal = p.pos != nullptr;
+        if (r.causal) r.pos = p.pos[g];
+    }
     r.falls = e < a;
     r.bad = b < 0 || b >= p.batch || a < 0 || e < a || e > p.nq;
     if (r.bad) return r;
@@ -128,8 +133,7 @@ __device__ __forceinline__ Group<kChunk> group_of(const DenseParams &p, int g)
     r.rows = (e - a) * p.H;
     if constexpr (kChunk) {
         r.seq = b;
-        r.causal = p.pos != nullptr;
-        if (r.causal) r.pos = p.pos[g];
+        r.queries = e - a;
     }
     return r;
 }
@@ -160,7 +164,7 @@ template <bool kChunk>
 __device__ __forceinline__ int tile_sees(const DenseParams &p, const Group<kChunk> &g, int rt)
 {
     if constexpr (kChunk) {
-        if (g.causal) return sees(p, g, (min((rt + 1) * kRowsPair, g.rows) - 1) / p.H);
+        if (g.causal) return sees(p, g, (rt + 1) * kRowsPair >= g.rows ? g.queries - 1 : ((rt + 1) * kRowsPair - 1) / p.H);
     }
     return g.n;
 }

@@ -34,6 +34,7 @@ __device__ __forceinline__ bool has_rows(const csa2_cache &c, const PageMap &m, 
 __global__ void __launch_bounds__(kThreads) evict_keys_kernel(EvictParams p, float *keys, int64_t ld, int32_t *n_valid, int32_t *skip)
 {
     pdl_wait();
+    pdl_trigger();
     const int s = blockIdx.y;
     const int b = p.seq ? p.seq[s] : s;
     bool bad = b < 0 || b >= p.src.batch;
