@@ -26,12 +26,13 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kResident = 4;                  // blocks to an SM
+constexpr int kResident = 3;                  // blocks to an SM (4, of 64 registers and spills: 93.1 us, see below; 3, of 80: 92.4)
 
 // Rows of x on their way to a warp, each in a slot of shared memory.  A lane copies the
 // 16 bytes 512 i + 16 lane of a row, so that a copy is of whole lines; of 16-bit types these
 // are its own channels, so that no other thread is waited for.
-// (4,096 x 64 bf16 rows: 115 us with one row ahead in registers, 104 with three here.)
+// (4,096 x 64 bf16 rows: 115 us with one row ahead in registers, 104 with three here;
+// 90 now, 88 % of the measured copy.)
 template <typename T>
 constexpr int kSlots = sizeof(T) == 2 ? 4 : 2;
 
@@ -94,7 +95,7 @@ __device__ __forceinline__ void store8(T *dst, const float *x)
 }
 
 // `per` heads of a token to a warp, `parts` warps to a token.
-template <typename T, typename O>
+template <typename T, typename O, bool kWeight>
 __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeParams p, uint32_t per, uint32_t parts)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -112,15 +113,14 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
         const double frac = hi - floor(hi);
         sTurn[threadIdx.x] = (uint64_t)(frac * 0x1p64) + (uint64_t)(int64_t)(lo * 0x1p64);
     }
-    float w[16];
+    float w[kWeight ? 16 : 1];
+    if constexpr (kWeight) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 v = p.weight ? *reinterpret_cast<const float4 *>(p.weight + 256 * h + 8 * lane + 4 * i)
-                                      : make_float4(1.f, 1.f, 1.f, 1.f);
-            w[8 * h + 4 * i] = v.x; w[8 * h + 4 * i + 1] = v.y; w[8 * h + 4 * i + 2] = v.z; w[8 * h + 4 * i + 3] = v.w;
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(p.weight + 256 * (i >> 1) + 8 * lane + 4 * (i & 1));
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         }
+    }
     __syncthreads();
     // where a lane's two groups of eight channels lie in the rotated part (negative: before it)
     const int at[2] = {8 * lane - (CSA2_D - p.rot), 256 + 8 * lane - (CSA2_D - p.rot)};
@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
         const bool due = turn;
         const uint32_t token = now.token;
         turn = now.next(step, per, parts, p.H);
+        // (two values an instruction: a row is some 300 of them, and issue was 71 % busy)
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float r = rsqrtf(fmaf(sum, 1.0f / CSA2_D, p.eps));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] *= r * w[i];
+        for (int i = 0; i < 16; ++i) v[i] *= kWeight ? r * w[kWeight ? i : 0] : r;
         if (pairs > 0) {
             if (due) {
                 const int64_t pos = p.pos[token];
@@ -229,31 +230,35 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
 
 }  // namespace
 
-template <typename T, typename O>
+template <typename T, typename O, bool kWeight>
 static cudaError_t launch_rope_as(const RopeParams &p, cudaStream_t st)
 {
-    // as many heads (a power of two) to a unit as leave each warp of a full GPU eight units
+    // as many heads (a power of two) to a unit as leave each warp of a full GPU four units or
+    // more (eight: 92.4 us instead of 90.2 for 4,096 x 64 rows, more cosines; a share of all
+    // rows each, which need not divide evenly: 104)
     const uint64_t rows = (uint64_t)p.n * p.H, warps = (uint64_t)device_sm_count() * kResident * kWarps;
     uint32_t per = 1;
-    while (2 * per <= p.H && 2 * per * 8 * warps <= rows) per *= 2;
+    while (2 * per <= p.H && 2 * per * 4 * warps <= rows) per *= 2;
     const uint32_t parts = (p.H + per - 1) / per;
     const uint64_t blocks = ((uint64_t)p.n * parts + kWarps - 1) / kWarps;
     // slots, turns, and for each warp (cos, sin) and, for halves, a row's rotated part
     const size_t smem = kWarps * kSlots<T> * CSA2_D * sizeof(T) + (size_t)p.rot / 2 * 8 + (size_t)kWarps * p.rot * 4 * (p.halves ? 2 : 1);
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(norm_rope_kernel<T, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(norm_rope_kernel<T, O, kWeight>, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
     if (e == cudaSuccess)
-        e = launch_k(norm_rope_kernel<T, O>, dim3((unsigned)std::min<uint64_t>(blocks, warps / kWarps)), dim3(32 * kWarps), smem, st, 0, p, per, parts);
+        e = launch_k(norm_rope_kernel<T, O, kWeight>, dim3((unsigned)std::min<uint64_t>(blocks, warps / kWarps)), dim3(32 * kWarps), smem, st, 0, p, per, parts);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_norm_rope(const RopeParams &p, int type, int out_type, cudaStream_t st)
 {
-    auto to = [&](auto tag) {
-        using T = decltype(tag);
-        return out_type == CSA2_F32    ? launch_rope_as<T, float>(p, st)
-               : out_type == CSA2_BF16 ? launch_rope_as<T, __nv_bfloat16>(p, st)
-                                       : launch_rope_as<T, __half>(p, st);
+    auto as = [&](auto from, auto to) {
+        using T = decltype(from);
+        using O = decltype(to);
+        return p.weight != nullptr ? launch_rope_as<T, O, true>(p, st) : launch_rope_as<T, O, false>(p, st);
+    };
+    auto to = [&](auto from) {
+        return out_type == CSA2_F32 ? as(from, float{}) : out_type == CSA2_BF16 ? as(from, __nv_bfloat16{}) : as(from, __half{});
     };
     return type == CSA2_F32 ? to(float{}) : type == CSA2_BF16 ? to(__nv_bfloat16{}) : to(__half{});
 }
