@@ -1,6 +1,8 @@
 // csa2_dense.cu -- attention of groups of queries over whole sequences of the
 // FP4 latent cache: a prompt that many sequences share (read once for all of
-// them), or an encoder's entries attended by a decoder sequence's queries.
+// them), or an encoder's entries attended by a decoder sequence's queries.  With
+// kChunk, of chunks of new tokens, each of which sees the entries up to its own, over
+// sequences that may lie in pages.
 //
 // Every row (query, head) of group g sees the entries j < n_g of one sequence:
 //     x_j = sm_scale q . v_j,   M = max(max_j x_j, lse_prev),

@@ -13,7 +13,15 @@
 // are stored (36 KB a tile); dequantised (E2M1 x E4M3 is exact in f16), they go straight
 // to TMEM, from where the MMAs read them: through shared memory, writing and reading
 // them would take 256 KB a tile and with the queries' reads more of its 128 bytes a
-// cycle than there are (32 x 64 heads over 65,536 entries: 245 us so).
+// cycle than there are (32 x 64 heads over 65,536 entries: 245 us so, 162 now; and an
+// MMA of N = 64 takes 33 cycles with A in TMEM, 50 with both operands in shared memory).
+//
+// What bounds it: no unit.  A tile takes some 3,000 cycles, the tensor pipe 1,020 of them
+// (2,040 for 128 rows), HBM 1,360 (621 MB in 162 us: 56 % of the measured copy).  The rest
+// are waits, commits and hand-overs between loader, producers, issuer and epilogue: with the
+// arithmetic of all of them taken out it was 144 us, with three quarters of the loads out as
+// well 116.  TMEM holds one tile of K beside two buffers of S, so that what lies between a
+// half's last MMA and its next first one is not hidden.
 //
 // S is summed in two parts of 256 channels, which the epilogue adds: the tensor core's
 // additions to an fp32 sum are cut off, not rounded, each by up to 2^-23 of the sum so
@@ -438,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(sFlag + 2);
     volatile int *abort_flag = sFlag;
     if (tid == 0) {
-        for (int i = 0; i < kUnits; ++i) { mbar_init(&bar_raw[i], 1); mbar_init(&bar_read[i], kWarpsProd / 2); }   // (a half tile, a stage: four warps)
+        for (int i = 0; i < kUnits; ++i) { mbar_init(&bar_raw[i], 1); mbar_init(&bar_read[i], kWarpsProd / 2); }   // (half a tile: four warps)
         for (int i = 0; i < kScaleUnits; ++i) { mbar_init(&bar_sc[i], 1); mbar_init(&bar_scread[i], kWarpsProd); }
         for (int i = 0; i < 2; ++i) { mbar_init(&bar_k[i], kWarpsProd / 2); mbar_init(&bar_kfree[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&bar_s[i], 1); mbar_init(&bar_sfree[i], kWarpsEpi / 2); }
@@ -480,9 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
 
     if (warp == kWarpMma) {
         // ============================================== MMA issuer (the whole warp runs the loop, one lane issues)
-        // Buffers, stages and passes are unrolled, so that every address and descriptor is
+        // Buffers, halves and passes are unrolled, so that every address and descriptor is
         // an immediate away from two registers: the MMAs take theirs from uniform
         // registers, and moving five of them there for each costs 55 cycles, 33 being its own.
+        // K comes in two halves, not more: a wait or a commit costs the warp some 100
+        // cycles (four stages: 178 us instead of 163 for 32 x 64 rows over 65,536 entries).
         uint32_t elected;
         asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(elected));
         const uint32_t q0 = __shfl_sync(0xffffffffu, smem_u32(sQ), 0), t0 = __shfl_sync(0xffffffffu, tmem, 0);
@@ -492,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
             tc_fence_after();
         };
-        // a pass over the rows kR .. into buffer kBuf; fill: K is made for it, last: and not used again
+        // a pass over the rows kR .. (the first waits for K) into buffer kBuf; last: K is not used again
         auto pass_as = [&](auto buf, auto r, uint32_t id, bool last) {
             constexpr uint32_t kBuf = decltype(buf)::value, kR = decltype(r)::value;
             wait(&bar_sfree[kBuf], used[kBuf]);

@@ -1,5 +1,5 @@
-// csa2_torch.cpp -- the Python binding's short calls (cache rows, dense
-// attention): arguments are taken from tensors here, because on the GPU these
+// csa2_torch.cpp -- the Python binding's short calls (cache rows, dense and chunk
+// attention, attention weights, eviction, norm with rotation): arguments are taken from tensors here, because on the GPU these
 // calls can be shorter than the interpreter needs for the same checks (a row
 // read of 129 rows: 1.7 us on the GPU, 8 us of checks and ctypes in Python).
 // Marshalling only, as in the rest of the binding: every refusal is a CsaError
