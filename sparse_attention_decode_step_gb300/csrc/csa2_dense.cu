@@ -101,8 +101,7 @@ struct Group {
 template <>
 struct Group<true> : Group<false> {
     int seq;
-    bool causal;
-    int pos;             // token position of its first query
+    int pos;             // token position of its first query (if there are positions)
     int queries;
     int tile_n;          // (of a piece of work:) entries that some row of its row tile sees
 };
@@ -113,8 +112,7 @@ __device__ __forceinline__ Group<kChunk> group_of(const DenseParams &p, int g)
     Group<kChunk> r{};
     const int b = p.g_seq[g], a = p.g_off[g], e = p.g_off[g + 1];
     if constexpr (kChunk) {
-        r.causal = p.pos != nullptr;
-        if (r.causal) r.pos = p.pos[g];
+        if (p.pos != nullptr) r.pos = p.pos[g];
     }
     r.falls = e < a;
     r.bad = b < 0 || b >= p.batch || a < 0 || e < a || e > p.nq;
@@ -153,7 +151,7 @@ template <bool kChunk>
 __device__ __forceinline__ int sees(const DenseParams &p, const Group<kChunk> &g, int k)
 {
     if constexpr (kChunk) {
-        if (g.causal) {
+        if (p.pos != nullptr) {
             const int64_t t = (int64_t)g.pos + k + 1;              // (under 2^32)
             if (t <= 0) return 0;
             return (int)min(p.m == 1 ? (uint32_t)t : (uint32_t)t / (uint32_t)p.m, (uint32_t)g.n);
@@ -166,7 +164,7 @@ template <bool kChunk>
 __device__ __forceinline__ int tile_sees(const DenseParams &p, const Group<kChunk> &g, int rt)
 {
     if constexpr (kChunk) {
-        if (g.causal) return sees(p, g, (rt + 1) * kRowsPair >= g.rows ? g.queries - 1 : ((rt + 1) * kRowsPair - 1) / p.H);
+        if (p.pos != nullptr) return sees(p, g, (rt + 1) * kRowsPair >= g.rows ? g.queries - 1 : ((rt + 1) * kRowsPair - 1) / p.H);
     }
     return g.n;
 }
@@ -797,14 +795,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             // needed, and a block's addresses made once (in the loads themselves: 520 us
             // instead of 459 for 2,048 queries x 64 heads over 2,048 entries each).
             const bool paged = kChunk && p.pages.table != nullptr;
-            const int32_t *const table = kChunk && paged ? p.pages.table + (int64_t)seq_of(w.gr) * p.pages.ld : nullptr;
             int page[2] = {};
-            int64_t step_c = 0;                // (kChunk) from stage 0's codes to stage 1's; scales: an eighth of it
+            int row[2] = {}, chan = 0;         // (kChunk) the lane's first rows of the stages, its byte in the first's codes
             auto want = [&](int b) {
                 if (!paged || b >= n_blocks) return;
                 bool k;
                 int tile;
                 const int e = block_of(b, k, tile) - e4;
+                const int32_t *const table = p.pages.table + (int64_t)seq_of(w.gr) * p.pages.ld;
                 page[0] = e < n_left ? __ldg(table + ((e + w.k0 * kEnt) >> p.pages.log)) : 0;
                 page[1] = !k && e + 128 < n_left ? __ldg(table + ((e + 128 + w.k0 * kEnt) >> p.pages.log)) : 0;
             };
@@ -818,22 +816,22 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 left_s = k ? 0 : 128;
                 if constexpr (kChunk) {
                     const int at = e - e4 + w.k0 * kEnt;
-                    int row = w.gr.base + at, row1 = row + 128;
+                    row[0] = w.gr.base + at + e4;
+                    row[1] = row[0] + 128;
                     if (paged) {
+                        const int mask = (1 << p.pages.log) - 1;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                        for (int i = 0; i < 2; ++i) {
                             if ((uint32_t)page[i] >= p.pages.pages) {      // no page of the cache: the first one stands for it
                                 if (lane == 0) count_event(p.counters, CSA2_CNT_BAD_INPUT);
                                 page[i] = 0;
                             }
-                        const int mask = (1 << p.pages.log) - 1;
-                        row = (page[0] << p.pages.log) + (at & mask);
-                        row1 = (page[1] << p.pages.log) + ((at + 128) & mask);
+                            row[i] = (page[i] << p.pages.log) + ((at + 128 * i) & mask) + e4;
+                        }
                         want(b + 1);
                     }
-                    c0 = p.codes + (int64_t)(row + e4) * CSA2_CODE_BYTES + (ch >> 1);
-                    s0 = p.scales + (int64_t)(row + e4) * CSA2_SCALE_BYTES + (ch >> 4);
-                    step_c = k ? 128 : (int64_t)(row1 - row) * CSA2_CODE_BYTES;
+                    if (k) row[1] = row[0];
+                    chan = ch >> 1;
                 } else {
                     c0 = codes + (int64_t)e * CSA2_CODE_BYTES + (ch >> 1);
                     s0 = scales + (int64_t)e * CSA2_SCALE_BYTES + (ch >> 4);
@@ -843,9 +841,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             };
             auto load = [&](int s) {
                 const uint8_t *c = c0 + s * c_step, *sc = s0 + s * s_step;
-                if constexpr (kChunk) {
-                    c = s ? c0 + step_c : c0;
-                    sc = s ? s0 + (step_c >> 3) : s0;
+                if constexpr (kChunk) {        // (made here from 32 bits each: pointers would be spilled)
+                    const int at = chan + s * (128 - left_s);
+                    c = p.codes + (int64_t)row[s] * CSA2_CODE_BYTES + at;
+                    sc = p.scales + (int64_t)row[s] * CSA2_SCALE_BYTES + (at >> 3);
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
