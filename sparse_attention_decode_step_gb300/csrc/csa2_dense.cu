@@ -497,6 +497,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32])
 }
 
 // ------------------------------------------------------------------ results
+// Two values of 16 bits, the lower channel first.
+template <int kOut>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    if constexpr (kOut == CSA2_BF16) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
+    } else {
+        return f32x2_to_f16x2(a, b);
+    }
+}
+
 template <int kOut>
 __device__ __forceinline__ void store4(void *out, int64_t at, float a, float b, float c, float d)
 {
@@ -797,14 +810,15 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             const bool paged = kChunk && p.pages.table != nullptr;
             int page[2] = {};
             int row[2] = {}, chan = 0;         // (kChunk) the lane's first rows of the stages, its byte in the first's codes
+            bool astray = false;               // a page number outside the cache
+            const int page_log = paged ? p.pages.log : 31;
             auto want = [&](int b) {
-                if (!paged || b >= n_blocks) return;
                 bool k;
                 int tile;
                 const int e = block_of(b, k, tile) - e4;
                 const int32_t *const table = p.pages.table + (int64_t)seq_of(w.gr) * p.pages.ld;
-                page[0] = e < n_left ? __ldg(table + ((e + w.k0 * kEnt) >> p.pages.log)) : 0;
-                page[1] = !k && e + 128 < n_left ? __ldg(table + ((e + 128 + w.k0 * kEnt) >> p.pages.log)) : 0;
+                page[0] = paged && e < n_left ? __ldg(table + ((e + w.k0 * kEnt) >> p.pages.log)) : 0;
+                page[1] = paged && !k && e + 128 < n_left ? __ldg(table + ((e + 128 + w.k0 * kEnt) >> p.pages.log)) : 0;
             };
             auto begin = [&](int b) {
                 bool k;
@@ -816,20 +830,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 left_s = k ? 0 : 128;
                 if constexpr (kChunk) {
                     const int at = e - e4 + w.k0 * kEnt;
-                    row[0] = w.gr.base + at + e4;
-                    row[1] = row[0] + 128;
-                    if (paged) {
-                        const int mask = (1 << p.pages.log) - 1;
+                    const int mask = (int)((1u << page_log) - 1);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if ((uint32_t)page[i] >= p.pages.pages) {      // no page of the cache: the first one stands for it
-                                if (lane == 0) count_event(p.counters, CSA2_CNT_BAD_INPUT);
-                                page[i] = 0;
-                            }
-                            row[i] = (page[i] << p.pages.log) + ((at + 128 * i) & mask) + e4;
-                        }
-                        want(b + 1);
+                    for (int i = 0; i < 2; ++i) {
+                        const bool off = paged && (uint32_t)page[i] >= p.pages.pages;      // (the first page stands for it)
+                        astray |= off;
+                        row[i] = w.gr.base + (off ? 0 : page[i] << page_log) + ((at + 128 * i) & mask) + e4;
                     }
+                    want(b + 1);
                     if (k) row[1] = row[0];
                     chan = ch >> 1;
                 } else {
@@ -858,31 +866,33 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                     gs[4 * s + u] = t;
                 }
             };
-            want(0);
-            begin(0);
-            load(0);
             // ---- Q, once the last piece's scores are done (the first piece's comes from
             // the softmax warps, which have nothing else to do then)
-            if (tiles > 0) {
+            want(0);
+            const bool q_due = tiles > 0;
+            if (q_due) {
                 ok = __all_sync(0xffffffffu, mbar_wait<true>(&bar_s[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, abort_flag));
                 if (!ok) break;
                 const int r0 = w.rt * kRowsPair + row_split(w);
                 const int n_rows = row_count(w);
                 issue_q(p, sQ, (int64_t)(w.gr.row0 + r0), n_rows, 32 * pw + lane);
-                load(1);
+            }
+            begin(0);
+            load(0);
+            if (q_due) {
                 finish_q<0>(p, sQ, 32 * pw + lane, q_full);
                 finish_q<1>(p, sQ, 32 * pw + lane, q_full);
-            } else {
-                load(1);
             }
+            load(1);
             tiles += n_tiles;
             for (int b = 0; b < n_blocks && ok; ++b) {
                 const bool ahead = b + 1 < n_blocks;
-                if (ahead) begin(b + 1);
+                if (!kChunk && ahead) begin(b + 1);
 #pragma unroll
                 for (int s = 0; s < kStages; ++s) {
                     ok = ok && __all_sync(0xffffffffu, mbar_wait<true>(&bar_empty[s], fills, abort_flag));
                     if (!ok) break;
+                    if (kChunk && s == 0) begin(b + 1);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const uint32_t sc = e4m3x2_to_f16x2(gs[4 * s + u]);
@@ -905,6 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 }
                 fills ^= 1;
             }
+            if (kChunk && astray && lane == 0) count_event(p.counters, CSA2_CNT_BAD_INPUT);
         }
         if (!ok && lane == 0) raise_abort(sFlag);
     } else {
@@ -922,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
         const float worst = l2s >= 0.f ? -INFINITY : INFINITY;     // a score that never is the largest logit
         uint32_t tile = 0;
         bool ok = true;
-        for (; more && ok; more = w.next(p)) {
+        while (more && ok) {
             const int r_tile = row_split(w);                     // of the tile's 128
             const int r0 = w.rt * kRowsPair + r_tile;
             const int n_rows = row_count(w);
@@ -1051,7 +1062,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             }
             if (!ok) break;
             // ---- the piece's sums: complete rows are finished, others left for the join
+            // (what comes next is worked out while the last products run)
             const bool whole = w.k0 == 0 && w.k1 == w.kt;
+            const int64_t piece = 2 * (int64_t)pair + (w.k0 == 0 ? 1 : 0);
+            more = w.next(p);
             const bool done = mbar_wait<true>(bar_o, (tile - 1) & 1, abort_flag);
             tc_fence_after();
             sRed[which * kRowsCta + row] = l;
@@ -1060,7 +1074,6 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             l = (sRed[row] + sRed[kRowsCta + row]) + (sRed[2 * kRowsCta + row] + sRed[3 * kRowsCta + row]);
             const float m = l != l ? 0.f : sM[row];             // (a NaN row is not an empty one)
             const int chan = 256 * (quarter >> 1) + 128 * ch;
-            const int64_t piece = 2 * (int64_t)pair + (w.k0 == 0 ? 1 : 0);
             Joined j{1.f, 0.f, 0.f};
             if (whole && row < n_rows)
                 j = join_prev(m, l, p.prev_out != nullptr, p.prev_out ? p.prev_lse[row0 + row] : 0.f);
@@ -1083,7 +1096,37 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
             const int mine = (n_rows - r_base + 3) / 4;       // of this lane's 8 rows r_base + 4 i
             const int64_t out0 = (row0 + r_base) * CSA2_D + c_lane;
             float *const part0 = p.part_o + (piece * kRowsPair + r_tile + r_base) * CSA2_D + c_lane;
-            const int chunks = 32 * (quarter & 1) < n_rows ? 4 : 0;
+            int chunks = 32 * (quarter & 1) < n_rows ? 4 : 0;
+            if constexpr (kChunk && kOut != CSA2_F32) {
+                if (whole && p.prev_out == nullptr) {
+                    // 64 channels at a time, already in 16 bits: a store fills whole lines
+                    uint16_t *const to = static_cast<uint16_t *>(p.out) + (row0 + r_base) * CSA2_D + chan + 8 * (lane & 7);
+#pragma unroll 1
+                    for (int c = 0; c < chunks; c += 2) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float o[32];
+                            tmem_ld32(tmem + 128 * ch + 32 * (c + h) + lane_q, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint4 *>(turn + sw128((uint32_t)lane, (uint32_t)(4 * h + k))) =
+                                    make_uint4(pack2<kOut>(o[8 * k] * j.own, o[8 * k + 1] * j.own), pack2<kOut>(o[8 * k + 2] * j.own, o[8 * k + 3] * j.own),
+                                               pack2<kOut>(o[8 * k + 4] * j.own, o[8 * k + 5] * j.own), pack2<kOut>(o[8 * k + 6] * j.own, o[8 * k + 7] * j.own));
+                        }
+                        __syncwarp();
+                        uint4 v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = *reinterpret_cast<const uint4 *>(turn + sw128((uint32_t)((lane >> 3) + 4 * i), (uint32_t)(lane & 7)));
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i < mine) *reinterpret_cast<uint4 *>(to + 4 * i * CSA2_D + 32 * c) = v[i];
+                    }
+                    chunks = 0;
+                }
+            }
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 float o[32];
