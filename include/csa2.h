@@ -413,7 +413,7 @@ typedef struct {
  *   a = pos[i] * inv_freq[p];  u' = u cos a - v sin a,  v' = u sin a + v cos a.
  *   x, out [n][H][512] of type and out_type (any of the three): token i at i * ld_x
  *   (ld_out) elements, its H heads 512 apart; out may be x itself (same type and
- *   ld).  weight [512] fp32; pos [n] (negative: rotates back), inv_freq [rot / 2]
+ *   ld, else refused), and rows of one may not lie over other rows of the other.  weight [512] fp32; pos [n] (negative: rotates back), inv_freq [rot / 2]
  *   fp32 radians per position, both NULL allowed when rot == 0.
  *   rot: 0 .. 512, a multiple of 16.  1 <= H <= 128, n * H < 2^31.
  * Sums, the norm and the rotation are fp32 and rounded once at the end; the angle

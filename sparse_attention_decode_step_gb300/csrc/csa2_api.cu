@@ -869,6 +869,8 @@ csa2_status csa2_norm_rope(const void *x, csa2_dtype type, int64_t ld_x, int64_t
     CSA2_REQUIRE(al16(x) && al16(out) && (ld_x * bx) % 16 == 0 && (ld_out * bo) % 16 == 0 &&
                      (weight == nullptr || al16(weight)) && (pos == nullptr || al4(pos)) && (inv_freq == nullptr || al4(inv_freq)),
                  CSA2_ERR_ALIGN);
+    // (in place, a row is written where that row alone was read)
+    CSA2_REQUIRE(x != out || (type == out_type && ld_x == ld_out), CSA2_ERR_INVALID_ARG);
     RopeParams p{};
     p.x = x;
     p.out = out;

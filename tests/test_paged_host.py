@@ -42,6 +42,11 @@ def test_norm_rope_rejects_bad_arguments_on_host():
         assert _rope(**bad) == ALIGN, bad
 
 
+def test_norm_rope_in_place_needs_one_type_and_one_stride():
+    for bad in (dict(out_type=0), dict(out_type=2), dict(ld_out=4096), dict(ld_x=4096)):
+        assert _rope(**bad) == INVALID, bad
+
+
 # ---------------------------------------------------------------- pages and groups
 def _chunk(cache=None, pages=None, ng=2, nq=5, seq=4096, off=4096, length=None, groups=True, pos=None, max_n=64, q=P, q_type=1, H=16,
            prev=(None, None), out=P, out_type=1, lse=None, ws=P, ws_bytes=1 << 40, counters=None):
