@@ -132,7 +132,7 @@ struct PageMap {
 constexpr int kDenseRows = 128;         // (query, head) rows of a tile, one pair of CTAs
 constexpr int kDenseEntries = 256;      // entries of a tile
 constexpr int kDenseSetup = 1;          // units of a row tile besides its entry tiles
-constexpr int kChunkSetup = 2;          // the same of csa2_chunk_attn, whose pieces are shorter (a prompt of 2,048: 365 us with 1, 318 with 2, 334 with 3)
+constexpr int kChunkSetup = 2;          // the same of csa2_chunk_attn, whose pieces are shorter (a prompt of 2,048: 299 us with 1, 282 with 2, 296 with 3)
 constexpr int kDensePairsMax = 95;      // pairs of CTAs of a launch (one per two SMs, on up to 191)
 // Where a pair's run begins: the units [first, last) of the row tile's entries,
 // its rows, and the units of a run.  rows = 0: the pair has no work.
