@@ -437,7 +437,8 @@ csa2_status csa2_norm_rope(const void *x, csa2_dtype type, int64_t ld_x, int64_t
  * chunk's length.  Everything else, prev_out, lse, the contract of groups and the
  * arithmetic, is csa2_dense_attn's; a query that sees nothing has prev, or 0 and
  * lse -inf.  The size of the workspace is csa2_dense_workspace_size's.  A page number
- * outside the cache changes nothing for the queries that see none of its entries.
+ * outside the cache changes nothing for the queries that see none of its entries; an
+ * entry of NaN scales makes every query that sees it NaN, and no other.
  *   pos [ng], 4-byte aligned, any int32. */
 csa2_status csa2_chunk_attn(const csa2_cache *cache, const csa2_pages *pages,
                             const csa2_groups *groups, const int32_t *pos, int64_t max_n,

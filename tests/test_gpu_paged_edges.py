@@ -49,3 +49,18 @@ def test_chunk_a_bad_page_stays_with_the_tokens_that_see_it(h, first, bad, types
     k = bad - first
     _check(lambda _g: s.values(0, bad), [0, k], [bad], [first], 1, q[:k], out[:k], lse[:k])
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("groups", [slice(0, 32), slice(7, 8), slice(31, 32)])
+@pytest.mark.parametrize("types", [("bf16", "f32"), ("f16", "bf16")])
+@pytest.mark.parametrize("h, first, bad", BORDERS)
+def test_chunk_a_nan_entry_stays_with_the_tokens_that_see_it(h, first, bad, types, groups):
+    # one entry whose scales, all or one, are NaN: the tokens that see it are NaN, the others as without it
+    s, q, out, lse = _prompt(h, first, 103, types)
+    row = s._rows(s.table_host, 16, 0, 600)[bad].item()
+    s.cache.scales[row, groups] = 0x7F if h != 16 else 0xFF
+    csa.chunk_attn(s.cache, csa.Groups([0], [0, 600 - first]), q, out, lse, pos=_ints([first]), pages=s.pages)
+    torch.cuda.synchronize()
+    k = bad - first
+    _check(lambda _g: s.values(0, bad), [0, k], [bad], [first], 1, q[:k], out[:k], lse[:k])
+    assert torch.isnan(out[k:]).all() and torch.isnan(lse[k:]).all()
