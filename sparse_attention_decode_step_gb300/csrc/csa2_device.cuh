@@ -22,10 +22,12 @@ __device__ __forceinline__ void count_event(uint32_t *counters, int slot, uint32
 }
 
 // Order-preserving map fp32 -> uint32 (larger float -> larger key); -0 and +0
-// map to the same key.
+// map to the same key. A NaN with a clear sign bit lies above +infinity (the eviction
+// marks what stays in any case by one).
 __device__ __forceinline__ uint32_t score_key(float f)
 {
-    uint32_t b = __float_as_uint(f == 0.0f ? 0.0f : f);
+    uint32_t b = __float_as_uint(f);
+    if (b == 0x80000000u) b = 0u;       // (by bits: a comparison of floats may order a NaN anywhere)
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 

@@ -2,13 +2,11 @@
 // attention weight (its first and last ones in any case) are copied, in order, to
 // other rows.
 //
-// Three steps on the stream: the selection's keys (the weights, infinite where an
-// entry stays in any case, so that ties and order are the top-k's: the lower entry
+// Three steps on the stream: the selection's keys (the weights, and above infinity
+// what stays in any case, so that ties and order are the top-k's: the lower entry
 // first), the library's top-k over them, and the copy.  Nothing is moved within a
 // sequence, which would have to wait for its own reads: every kept row is read once
 // and written once.
-#include <cfloat>
-
 #include <algorithm>
 
 #include "csa2_device.cuh"
@@ -65,7 +63,8 @@ __global__ void __launch_bounds__(kThreads) evict_keys_kernel(EvictParams p, flo
         const int64_t j = j0 + i * kThreads;
         if (j >= n) continue;
         const float v = mass[j];
-        out[j] = j < p.n_first || j >= last ? INFINITY : v != v ? -INFINITY : fminf(v, FLT_MAX);
+        // (the top-k orders keys by their bits: a positive NaN lies above infinity)
+        out[j] = j < p.n_first || j >= last ? __uint_as_float(0x7FC00000u) : v != v ? -INFINITY : v;
     }
 }
 

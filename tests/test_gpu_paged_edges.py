@@ -1,11 +1,13 @@
 """Edges of the calls around a paged cache. Bounds as in test_gpu_paged, whose references
 these tests use."""
+import math
+
 import pytest
 import torch
 
 import sparse_attention_decode_step_gb300 as csa
 from helpers import need_gpu
-from test_gpu_paged import DEV, TYPES, Paged, _check, _ints, _np, _queries
+from test_gpu_paged import DEV, TYPES, Paged, _check, _ints, _kept, _np, _queries
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +66,20 @@ def test_chunk_a_nan_entry_stays_with_the_tokens_that_see_it(h, first, bad, type
     k = bad - first
     _check(lambda _g: s.values(0, bad), [0, k], [bad], [first], 1, q[:k], out[:k], lse[:k])
     assert torch.isnan(out[k:]).all() and torch.isnan(lse[k:]).all()
+
+
+# ================================================================ eviction: weights at the ends of fp32
+@pytest.mark.parametrize("lens", [[300], [70000], [300000], [500] * 130])
+def test_evict_prefers_infinity_to_the_largest_number(lens):
+    s = Paged(lens, 16, 107, to=[40] * len(lens))
+    w = torch.rand(len(lens), max(lens))
+    big = torch.finfo(torch.float32).max
+    w[:, 10:40] = big                                       # more of them than there is room for, in front of
+    w[:, 200::7][:, :20] = math.inf                         # the infinite ones
+    w[:, 5:8], w[:, -9:] = math.nan, -big
+    kept = torch.zeros(len(lens), 40, dtype=torch.int32, device=DEV)
+    csa.cache_evict(s.cache, s.cache, w.to(DEV), 40, kept, first=4, last=8, pages=s.pages, to_pages=csa.Pages(s.to_host.to(DEV), 16))
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        want = _kept(w[b].tolist(), n, 40, 4, 8)
+        assert _np(kept[b]).tolist() == want
