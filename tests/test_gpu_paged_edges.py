@@ -7,7 +7,7 @@ import torch
 
 import sparse_attention_decode_step_gb300 as csa
 from helpers import need_gpu
-from test_gpu_paged import DEV, TYPES, Paged, _check, _ints, _kept, _np, _queries
+from test_gpu_paged import DEV, TYPES, Paged, _check, _check_mass, _ints, _kept, _np, _queries, _rope_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -68,6 +68,28 @@ def test_chunk_a_nan_entry_stays_with_the_tokens_that_see_it(h, first, bad, type
     assert torch.isnan(out[k:]).all() and torch.isnan(lse[k:]).all()
 
 
+# ================================================================ attention weights: plans
+@pytest.mark.parametrize("tokens", [1019, 1020, 1090])
+def test_mass_few_groups_of_many_blocks(tokens):
+    # 128 heads: a block to a token, and one more for each of the five of another sequence: up to 1,024 blocks a
+    # plan of few groups is made by a thread to a block, more the general way. A sequence once more, offsets that
+    # fall and the group behind them are counted once each.
+    h, nq = 128, tokens + 10
+    s = Paged([40, 33, 20, 17], 16, 105)
+    q = _queries(nq, h, torch.bfloat16, 106)
+    lse = torch.full((nq, h), 5.0, device=DEV)
+    prev = torch.rand(4, 64, device=DEV)
+    mass = torch.full((4, 64), 7.0, device=DEV)
+    cnt = csa.new_counters()
+    off, pos = [0, tokens, tokens + 5, nq, nq - 2, nq], [45 - tokens, 0, 30, 0, 0]
+    csa.attn_mass(s.cache, csa.Groups([0, 0, 1, 2, 3], off), q, lse, mass, pos=_ints(pos), pages=s.pages, prev=prev, decay=0.5, counters=cnt)
+    torch.cuda.synchronize()
+    assert _np(cnt).tolist() == [0, 0, 3, 0]
+    _check_mass(s.values, [0, tokens], [40], [pos[0]], 1, q, lse, prev, 0.5, mass)
+    _check_mass(lambda g: s.values(1), [tokens + 5, nq], [33], [30], 1, q, lse, prev, 0.5, mass, seqs=[1])
+    assert (mass[2:] == 7).all() and (mass[0, 40:] == 7).all() and (mass[1, 33:] == 7).all()
+
+
 # ================================================================ eviction: weights at the ends of fp32
 @pytest.mark.parametrize("lens", [[300], [70000], [300000], [500] * 130])
 def test_evict_prefers_infinity_to_the_largest_number(lens):
@@ -83,3 +105,64 @@ def test_evict_prefers_infinity_to_the_largest_number(lens):
     for b, n in enumerate(lens):
         want = _kept(w[b].tolist(), n, 40, 4, 8)
         assert _np(kept[b]).tolist() == want
+
+
+# ================================================================ norm and rotation
+SPLITS = [
+    # tokens, heads, rotated, type, out: enough rows that a warp takes 2, 4, 8 or 16 heads of a token, of which the
+    # last warp's are fewer where the heads do not divide
+    (6001, 5, 64, "bf16", "bf16"),
+    (12001, 5, 512, "bf16", "f16"),
+    (6001, 20, 64, "f16", "bf16"),
+    (900, 65, 96, "f32", "f32"),
+    (1850, 65, 128, "bf16", "bf16"),
+    (1900, 127, 16, "bf16", "f32"),
+    (4096, 64, 64, "bf16", "bf16"),
+]
+
+
+def _rope_check(got, x, w, eps, pos, freq, halves):
+    y, size = _rope_reference(x, w, eps, pos, freq, halves)
+    e = torch.finfo(got.dtype).eps / 2
+    got64 = got.double().cpu()
+    far = (got64 - y).abs() - size * 2.0 ** -20 - e * y.abs() * (1 + 2.0 ** -10) - torch.finfo(got.dtype).tiny * 2 * e
+    assert torch.isfinite(got64).all() and far.max() <= 0, far.max().item()
+
+
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("n, h, rot, t, to", SPLITS)
+def test_norm_rope_splits_of_heads(n, h, rot, t, to, weighted, halves):
+    g = torch.Generator().manual_seed(n + h)
+    gd = torch.Generator(DEV).manual_seed(n + h)
+    x = torch.randn(n, h, 512, generator=gd, device=DEV).to(TYPES[t])
+    pos = torch.randint(-1000, 1 << 20, (n,), generator=g, dtype=torch.int32)
+    freq = (10000.0 ** (-torch.arange(rot // 2).double() / (rot // 2))).float()
+    w = torch.randn(512, generator=g) if weighted else None
+    kw = dict(weight=None if w is None else w.to(DEV), eps=1e-5, inv_freq=freq.to(DEV), halves=halves)
+    out = torch.full((n, h, 512), float("nan"), dtype=TYPES[to], device=DEV)
+    csa.norm_rope(x, out, pos=pos.to(DEV), **kw)
+    # some tokens against float64, all of them against calls of few tokens, whose warps take a head each
+    some = torch.cat([torch.tensor([0, n - 1]), torch.randint(0, n, (60,), generator=g)])
+    torch.cuda.synchronize()
+    _rope_check(out[some.to(DEV)], x[some.to(DEV)].cpu(), w, 1e-5, pos[some], freq, halves)
+    few = torch.full_like(out, float("nan"))
+    step = max(1, 20000 // h)
+    for i in range(0, n, step):
+        csa.norm_rope(x[i:i + step], few[i:i + step], pos=pos[i:i + step].to(DEV), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(out, few)
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("to", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n, h", [(1, 1), (1, 20), (7, 0), (700, 5)])
+def test_norm_without_rotation(n, h, t, to, weighted):
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn(*((n, h, 512) if h else (n, 512)), generator=g).to(TYPES[t])
+    w = torch.randn(512, generator=g) if weighted else None
+    out = torch.full(x.shape, float("nan"), dtype=TYPES[to], device=DEV)
+    csa.norm_rope(x.to(DEV), out, weight=None if w is None else w.to(DEV), eps=1e-5)
+    torch.cuda.synchronize()
+    _rope_check(out, x, w, 1e-5, None, None, False)
