@@ -800,8 +800,11 @@ __global__ void __launch_bounds__(kFinishThreads) mass_finish_kernel(MassParams 
 
 }  // namespace
 
-// Parts, two to a block, are kept for so many blocks at a time that they take up to
-// 256 MB; more blocks go in turns.
+// Parts, two to a block, are kept for 32 blocks or, up to a million entries, as many as take
+// 256 MB; more blocks go in turns.  Which blocks leave parts (those of groups of more than 64
+// rows) only the device knows, so that all are counted: with single tokens of 64 heads, which leave
+// none, a call has their memory and their turns all the same (64 of them over a million entries: 256 MB
+// and three turns instead of one).
 MassPlan mass_plan(int batch, int ng, int nq, int H, int64_t max_n)
 {
     MassPlan pl{};

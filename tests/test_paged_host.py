@@ -102,6 +102,16 @@ def test_mass_workspace_sizes():
     assert size(8, 1, 1 << 20, 128, 1 << 20) < (256 << 20) + (1 << 20) * 80 + (1 << 16)
 
 
+@pytest.mark.parametrize("n", [1 << 20, (1 << 20) + 1, 1 << 22, 1 << 24, (1 << 31) - 1])
+def test_mass_workspace_of_long_sequences(n):
+    # beyond a million entries the parts of 32 blocks of rows, 8 bytes an entry each, or of as many as there are
+    size = csa.mass_workspace_size
+    most, plan = 32 * 8 * n, (1 << 20) * 80 + (1 << 16)
+    assert most <= size(8, 1, 1 << 20, 128, n) < most + plan
+    assert 2 * 8 * n <= size(8, 1, 2, 64, n) < 2 * 8 * n + (1 << 16)
+    assert size(8, 1, 1, 64, n) < 1 << 16
+
+
 # ---------------------------------------------------------------- eviction
 def _evict(cache=None, pages=None, to=None, to_pages=None, seq=None, ns=2, mass=P, ld=64, max_n=64, keep=16, first=2, last=3, kept=P,
            ld_kept=16, out=None, ld_out=0, ws=P, ws_bytes=1 << 40, counters=None):
