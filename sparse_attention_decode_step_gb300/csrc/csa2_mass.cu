@@ -703,7 +703,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             const Block &blk = ws.blocks[w.b];
             const int rows = blk.rows, n = columns(rows), n_ent = blk.n;
             const bool alone = blk.alone;
-            // Where the rows' lse2 lie within 2^64 of each other, one m (the largest) serves them all.
+            // Where the rows' lse2 lie within 2^64 of each other, one m in the middle serves them all:
+            // a weight is 2^(l2s x - m) times up to 2^32, so that what the exponential flushes
+            // to zero below 2^-126 is below 2^-94 (with the largest it was 2^-62).
             float lse2 = NAN;                  // (a row without weight, or past the block's)
             int s = 0;
             if (at < rows) {
@@ -721,9 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             epi_sync();
             top = fmaxf(fmaxf(sTop[0], sTop[1]), fmaxf(sTop[2], sTop[3]));
             low = fminf(fminf(sTop[4], sTop[5]), fminf(sTop[6], sTop[7]));
-            const float m_all = rintf(top);
+            const float m_all = rintf(0.5f * (top + low));
             // (false without any weight; below 2^-96 a column without a row, whose S is 0, would not stay finite)
-            const bool near = top - low < 64.f && top > -96.f;
+            const bool near = top - low < 64.f && m_all > -96.f;
             if (at < kRows) {
                 const float m = near ? m_all : lse2 == lse2 ? rintf(lse2) : 0.f;
                 sM[at] = m;

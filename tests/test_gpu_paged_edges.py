@@ -7,7 +7,7 @@ import torch
 
 import sparse_attention_decode_step_gb300 as csa
 from helpers import need_gpu
-from test_gpu_paged import DEV, TYPES, Paged, _check, _check_mass, _ints, _kept, _np, _queries, _rope_reference
+from test_gpu_paged import DEV, TYPES, Paged, _check, _check_mass, _ints, _kept, _mass_reference, _np, _queries, _rope_reference, _sees
 
 pytestmark = pytest.mark.gpu
 
@@ -88,6 +88,35 @@ def test_mass_few_groups_of_many_blocks(tokens):
     _check_mass(s.values, [0, tokens], [40], [pos[0]], 1, q, lse, prev, 0.5, mass)
     _check_mass(lambda g: s.values(1), [tokens + 5, nq], [33], [30], 1, q, lse, prev, 0.5, mass, seqs=[1])
     assert (mass[2:] == 7).all() and (mass[0, 40:] == 7).all() and (mass[1, 33:] == 7).all()
+
+
+@pytest.mark.parametrize("h, tokens", [(2, 1), (64, 1), (20, 7), (128, 3)])
+@pytest.mark.parametrize("spread", [0.0, 20.0, 40.0, 43.0, 46.0, 90.0])
+@pytest.mark.parametrize("at", [-30.0, 10.0, 60.0])
+def test_mass_small_weights_of_rows_far_apart(at, spread, h, tokens):
+    # log sums of a block's rows that lie up to `spread` apart (a merged partial result makes one large), and weights
+    # down to nothing: an fp32 exponential loses what lies below 2^-126, and a row is at most 2^32 from what its
+    # block is computed relative to, so a weight may lose 2^-94 besides its relative error
+    s = Paged([700, 90], 16, 109)
+    q = _queries(2 * tokens, h, torch.float16, 110, 0.5)
+    g = torch.Generator().manual_seed(111)
+    lse = at + spread * torch.rand(2 * tokens, h, generator=g)
+    lse[::2, 0], lse[1::2, -1] = at, at + spread
+    lse = lse.to(DEV)
+    off = [0, tokens, 2 * tokens]
+    groups, pos = csa.Groups([0, 1], off), _ints([650, 60])
+    out, own = torch.zeros(2 * tokens, h, 512, device=DEV), torch.zeros(2 * tokens, h, device=DEV)
+    csa.chunk_attn(s.cache, groups, q, out, own, pos=pos, pages=s.pages, sm_scale=2.0)
+    lse = torch.maximum(lse, own)                           # (a weight is at most 1)
+    mass = torch.zeros(2, 700, device=DEV)
+    csa.attn_mass(s.cache, groups, q, lse, mass, pos=pos, pages=s.pages, sm_scale=2.0)
+    torch.cuda.synchronize()
+    for b, n in enumerate([700, 90]):
+        rows = slice(off[b], off[b + 1])
+        want, bound = _mass_reference(s.values(b), q[rows].reshape(-1, 512), lse[rows].reshape(-1),
+                                      _sees(off, b, n, [650, 60], 1, h), 2.0)
+        far = (mass[b, :n].double() - want).abs() - bound - 2.0 ** -23 * want - tokens * h * 2.0 ** -94
+        assert torch.isfinite(mass[b]).all() and far.max() <= 0, (far.max().item(), want[far.argmax()].item())
 
 
 # ================================================================ eviction: weights at the ends of fp32
