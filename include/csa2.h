@@ -364,7 +364,8 @@ csa2_status csa2_cache_read(const csa2_cache *cache, const int64_t *rows, int64_
  *   max_n: host bound on every n_g; it sets how a group's entries are divided.
  * Arithmetic as in csa2_sparse_attn: exact f16 latents, q as f16 (bf16: exact
  * for magnitudes in [2^-14, 65504]), logits |x_j| below 2^27, softmax weights rounded to f16 (off by 2^-11
- * of themselves, or by 2^-32 of the row's largest where that is more), every sum in
+ * of themselves, or by 2^-32 of the row's largest where that is more), exponentials by
+ * the GPU's approximation of 2^x (within 2^-22), every sum in
  * fp32; results do not depend on the run (fixed order).  Each level of shared
  * prompts rounds its own weights once.
  * Group arrays: 4-byte aligned; q, prev_out, out, workspace: 16-byte. */
@@ -416,7 +417,9 @@ typedef struct {
  *   ld, else refused), and rows of one may not lie over other rows of the other.  weight [512] fp32; pos [n] (negative: rotates back), inv_freq [rot / 2]
  *   fp32 radians per position, both NULL allowed when rot == 0.
  *   rot: 0 .. 512, a multiple of 16.  1 <= H <= 128, n * H < 2^31.
- * Sums, the norm and the rotation are fp32 and rounded once at the end; the angle
+ * Sums, the norm and the rotation are fp32 and rounded once at the end, so the squares have to
+ * stay in fp32: |x| below 2^59, and with eps below 2^-100 no row but of zeros whose root mean
+ * square is below 2^-50; the angle
  * is reduced in turns of 64-bit fixed point, so that it is as exact at position
  * 2^30 as near 0 (cos and sin within 2^-21).  A row of zeros gives zeros if eps > 0.
  * x, out, weight: 16-byte aligned, ld_x and ld_out at least H * 512, below 2^31 and a
@@ -459,9 +462,15 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const csa2_pages *pages,
  *   groups as in csa2_chunk_attn, but a sequence may be in one group only: a group
  *   whose sequence an earlier one has is skipped and counted in CSA2_CNT_BAD_INPUT;
  *   q [nq][H][512] of q_type CSA2_BF16 or CSA2_F16, 1 <= H <= 128; lse [nq][H];
- *   prev, mass [batch][ld_mass] fp32, ld_mass >= max_n; prev may be mass itself.
- * Arithmetic: products of exact f16 latents and q as f16 (as in csa2_dense_attn),
- * everything else in fp32; results do not depend on the run (fixed order).
+ *   prev, mass [batch][ld_mass] fp32, ld_mass >= max_n; prev may be mass itself, and
+ *   must not overlap it otherwise.
+ * Arithmetic: products of exact f16 latents and q as f16, exponentials as in
+ * csa2_dense_attn, everything else in fp32; the tensor core's additions are cut off, not
+ * rounded: a logit is off by up to 32 * 2^-23 of the sum of |q_c v_c|, and a weight by as
+ * much of itself; a weight below 2^-94 may count as 0; results do not depend on the run
+ * (fixed order).
+ * The workspace grows with max_n where groups have more than 64 rows (queries x heads): 8
+ * bytes an entry for each 128 rows, of 32 blocks of rows or 256 MB at a time, whichever is more.
  * lse, prev, mass: 4-byte aligned; q, workspace: 16-byte. */
 csa2_status csa2_attn_mass(const csa2_cache *cache, const csa2_pages *pages,
                            const csa2_groups *groups, const int32_t *pos, int64_t max_n,
@@ -475,7 +484,7 @@ size_t csa2_mass_workspace_size(int32_t batch, int32_t ng, int32_t nq, int32_t H
 /* ---- 14. eviction ---------------------------------------------------------------------
  * Sequence b of `cache` (n = seq_len[b] entries) is cut to min(n, keep) entries: its
  * first n_first, its last n_last, and of those between the ones with the largest
- * mass[b][j] (ties to the lower entry; -0 equals 0; NaN counts as the smallest).
+ * mass[b][j] (ties to the lower entry; -0 equals 0; NaN counts as minus infinity).
  * They are copied in order, indexer keys included, to the entries 0, 1, ... of
  * sequence b of `dst`, whose seq_len[b] becomes their number.  The old entries stay
  * as they were: dst may be the same arrays with other pages (whose old ones are
@@ -487,6 +496,8 @@ size_t csa2_mass_workspace_size(int32_t batch, int32_t ng, int32_t nq, int32_t H
  *   ld_out >= keep): the kept entries' mass, sequence by sequence;
  *   max_n: host bound on every n; keep >= 1, n_first + n_last <= keep;
  *   dst: as many sequences, keys if and only if `cache` has them, of the same d_idx.
+ * Sections 2 to 7 score and attend by seq_base: keys that are evicted into pages are there
+ * for csa2_cache_read and further evictions, into a contiguous cache for the indexer too.
  * Sequences outside the contract (number, n < 0 or above max_n, pages or room too
  * few on either side) are skipped, counted in CSA2_CNT_BAD_INPUT (room: in
  * CSA2_CNT_CAPACITY), and their seq_len left.  Rows that the call writes must not be

@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         // (a page number outside the cache: zeros stand for its entries. A test of
-                        // the row's sign at the loads instead: 287 us for the prompt of 2,048, so 282)
+                        // the row's sign at the loads instead: 287 us for the prompt of 2,048, so 284)
                         const bool off = paged && (uint32_t)page[i] >= p.pages.pages;
                         astray |= off;
                         if (off) inside = false;
@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_attn_kernel(DenseParams p)
                 // A row whose token does not see an entry has weight 0 for it, and 0 times NaN would
                 // be NaN for every row of the tile: NaN scales become 448 in V (the least of a NaN
                 // and a number is the number; 448 is E4M3's largest). In K they stay, so that a row
-                // that sees the entry has a NaN weight. (Under 1 us of the prompt's 283.)
+                // that sees the entry has a NaN weight. (Under 1 us of the prompt's 284.)
                 uint32_t most = 0x7FFF7FFFu;                              // (two NaN)
                 if (kChunk && b != 0 && ((b & 1) == 0 || b == n_blocks - 1)) most = 0x5F005F00u;      // (two 448)
                 if (!kChunk && ahead) begin(b + 1);

@@ -132,7 +132,9 @@ struct PageMap {
 constexpr int kDenseRows = 128;         // (query, head) rows of a tile, one pair of CTAs
 constexpr int kDenseEntries = 256;      // entries of a tile
 constexpr int kDenseSetup = 1;          // units of a row tile besides its entry tiles
-constexpr int kChunkSetup = 2;          // the same of csa2_chunk_attn, whose pieces are shorter (a prompt of 2,048: 299 us with 1, 282 with 2, 296 with 3)
+// The same of csa2_chunk_attn, whose pieces are shorter.  With 1 / 2 / 3, us: a prompt of 2,048 300 / 284 / 298,
+// 601 queries over up to 30,011 entries 151 / 142 / 146, 32 single tokens over up to 65,536 73.3 / 71.7 / 74.7.
+constexpr int kChunkSetup = 2;
 constexpr int kDensePairsMax = 95;      // pairs of CTAs of a launch (one per two SMs, on up to 191)
 // Where a pair's run begins: the units [first, last) of the row tile's entries,
 // its rows, and the units of a run.  rows = 0: the pair has no work.

@@ -26,7 +26,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kResident = 3;                  // blocks to an SM (4, of 64 registers and spills: 93.1 us, see below; 3, of 80: 92.4)
+constexpr int kResident = 3;                  // blocks to an SM, of 80 registers (4, of 64 and spills: 93.1 us where 3 took 92.4)
 
 // Rows of x on their way to a warp, each in a slot of shared memory.  A lane copies the
 // 16 bytes 512 i + 16 lane of a row, so that a copy is of whole lines; of 16-bit types these
@@ -164,7 +164,6 @@ __global__ void __launch_bounds__(32 * kWarps, kResident) norm_rope_kernel(RopeP
         const bool due = turn;
         const uint32_t token = now.token;
         turn = now.next(step, per, parts, p.H);
-        // (two values an instruction: a row is some 300 of them, and issue was 71 % busy)
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
@@ -235,7 +234,9 @@ static cudaError_t launch_rope_as(const RopeParams &p, cudaStream_t st)
 {
     // as many heads (a power of two) to a unit as leave each warp of a full GPU four units or
     // more (eight: 92.4 us instead of 90.2 for 4,096 x 64 rows, more cosines; a share of all
-    // rows each, which need not divide evenly: 104)
+    // rows each, which need not divide evenly: 104).  Below some 58,000 rows that is one or two, and
+    // the angles of a token are made by every warp that has a head of it: 500 x 64 rows 11.5 us,
+    // 9.6 by their bytes; 160 x 64 5.7 us, 3.1 by theirs.
     const uint64_t rows = (uint64_t)p.n * p.H, warps = (uint64_t)device_sm_count() * kResident * kWarps;
     uint32_t per = 1;
     while (2 * per <= p.H && 2 * per * 4 * warps <= rows) per *= 2;
